@@ -41,6 +41,13 @@ SIGNATURES = {
     "fa_bwd_dq": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
     "fa_bwd_noalloc_scratch_bytes": (_SZ, []),
+    "fa_cache_append": (_I, [_P] * 7 + [_I] * 7 + [_P]),
+    "fa_fwd_paged_workspace_bytes": (_SZ, [_I] * 5),
+    "fa_fwd_paged": (_I, [_P] * 7 + [_I, _P, _P] + [_I] * 9 + [_F, _P, _SZ, _P]),
+    "fa_cache_compact": (_I, [_P] * 7 + [_I] * 8 + [_P]),
+    "fa_cache_fork": (_I, [_P] * 5 + [_I] * 4 + [_P]),
+    "fa_cache_resize_workspace_bytes": (_SZ, [_I]),
+    "fa_cache_resize": (_I, [_P] * 8 + [_I] * 7 + [_P, _SZ, _P]),
     "fa_exp2_poly": (_I, [_P, _P, _LL, _P]),
     "fa_last_device_status": (_I, [_P]),
     "fa_last_device_status_site": (_I, [_P, _P]),
@@ -172,6 +179,49 @@ def fa_bwd_noalloc(q, k, v, o, lse, dO, dq, dk, dv, B, H, Hkv, N, d, scale, caus
 def fa_bwd_noalloc_scratch_bytes() -> int:
     """Size of fa_bwd_noalloc's built-in scratch array, as the library was built."""
     return int(lib().fa_bwd_noalloc_scratch_bytes())
+
+
+def fa_cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, B, max_pages, num_pages, page_size,
+                    total, Hkv, d, stream=None) -> int:
+    return lib().fa_cache_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens),
+                                 _ptr(cu_seqlens), B, max_pages, num_pages, page_size, total, Hkv, d, _stream(stream))
+
+
+def fa_fwd_paged_workspace_bytes(B, max_new, H, Hkv, d) -> int:
+    return int(lib().fa_fwd_paged_workspace_bytes(B, max_new, H, Hkv, d))
+
+
+def fa_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, tree_mask, mask_words, o, lse, B, max_pages,
+                 num_pages, page_size, max_new, total, H, Hkv, d, scale, workspace, workspace_bytes,
+                 stream=None) -> int:
+    return lib().fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens),
+                              _ptr(cu_seqlens), _ptr(tree_mask), mask_words, _ptr(o), _ptr(lse), B, max_pages,
+                              num_pages, page_size, max_new, total, H, Hkv, d, float(scale), _ptr(workspace),
+                              int(workspace_bytes), _stream(stream))
+
+
+def fa_cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, lens_out, B, max_accepted,
+                     max_pages, num_pages, page_size, layers, Hkv, d, stream=None) -> int:
+    return lib().fa_cache_compact(_ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens), _ptr(accepted),
+                                  _ptr(n_accepted), _ptr(lens_out), B, max_accepted, max_pages, num_pages, page_size,
+                                  layers, Hkv, d, _stream(stream))
+
+
+def fa_cache_fork(page_refs, page_table, cache_lens, parents, lens_out, B, max_pages, num_pages, page_size,
+                  stream=None) -> int:
+    return lib().fa_cache_fork(_ptr(page_refs), _ptr(page_table), _ptr(cache_lens), _ptr(parents), _ptr(lens_out), B,
+                               max_pages, num_pages, page_size, _stream(stream))
+
+
+def fa_cache_resize_workspace_bytes(B) -> int:
+    return int(lib().fa_cache_resize_workspace_bytes(B))
+
+
+def fa_cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, lens_out, status, B, max_pages,
+                    num_pages, page_size, layers, Hkv, d, workspace, workspace_bytes, stream=None) -> int:
+    return lib().fa_cache_resize(_ptr(page_refs), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens),
+                                 _ptr(new_lens), _ptr(lens_out), _ptr(status), B, max_pages, num_pages, page_size,
+                                 layers, Hkv, d, _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
 def fa_exp2_poly(x, y, n, stream=None) -> int:
@@ -360,3 +410,223 @@ def attention_bwd(q, k, v, o, lse, dO, scale=None, causal=False, workspace=None,
     if st != FA_OK:
         raise FaError(st, "fa_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ paged cache
+def _same_device(*checked):
+    """Raise ValueError unless all tensors are on one CUDA device; returns it."""
+    dev = checked[0][1].device
+    for name, t in checked:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {checked[0][0]} on {dev}")
+    return dev
+
+
+class _On:
+    """Makes `dev` the current device and `stream` (None: its current stream) the current stream, so
+    that what a call allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, dev, stream):
+        import torch
+
+        self.device = torch.cuda.device(dev)
+        self.stream = None
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self.stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _elsewhere(dev, stream):
+    """Whether a call on tensors of `dev` has to switch device or stream first (see _On)."""
+    import torch
+
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _check_pages(k_pages, v_pages, layered):
+    import torch
+
+    dims = k_pages.dim()
+    if dims != 4 and not (layered and dims == 5):
+        raise ValueError("k_pages and v_pages must be [num_pages, page_size, Hkv, d]"
+                         + (", or the same with a leading [layers]" if layered else ""))
+    c = [_check("k_pages", k_pages, torch.bfloat16, k_pages.shape),
+         _check("v_pages", v_pages, torch.bfloat16, k_pages.shape)]
+    return c, (1 if dims == 4 else k_pages.shape[0]), *k_pages.shape[-4:]
+
+
+def _check_table(page_table, cache_lens):
+    import torch
+
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    return [_check("page_table", page_table, torch.int32, (B, max_pages)),
+            _check("cache_lens", cache_lens, torch.int32, (B,))], B, max_pages
+
+
+def cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, stream=None):
+    """Writes packed new rows k/v [total,Hkv,d] bf16 into the pages [num_pages,page_size,Hkv,d]: row i of
+    sequence b (rows cu_seqlens[b]..cu_seqlens[b+1]) to place cache_lens[b] + i of the cache, i.e. row
+    place % page_size of page page_table[b, place // page_size].  page_table int32 [B,max_pages],
+    cache_lens int32 [B], cu_seqlens int32 [B+1]."""
+    import torch
+
+    pages, _, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, False)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total = k.shape[0]
+    dev = _same_device(_check("k", k, torch.bfloat16, (total, Hkv, d)), _check("v", v, torch.bfloat16, (total, Hkv, d)),
+                       *pages, *table, _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens)
+    if total == 0:
+        return
+    st = fa_cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, B, max_pages, num_pages,
+                         page_size, total, Hkv, d)
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_append")
+
+
+def attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask=None, scale=None,
+                        out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens q [total,H,d] bf16 (sequence b: rows cu_seqlens[b]..cu_seqlens[b+1], at most
+    max_new <= 256 of them) over the cache, which already holds their own keys and values
+    (:func:`cache_append`) -> (o bf16 [total,H,d], lse fp32 [H,total]).  Token i sees the cache_lens[b]
+    places before the new ones and, of the new ones, those up to itself, or with tree_mask (int64
+    [total, ceil(max_new / 64)]) those whose bits are set in its words.  A token that sees nothing gets
+    o = 0 and lse = -inf."""
+    import torch
+
+    pages, _, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, False)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, H, d]")
+    total, H, _ = q.shape
+    max_new = int(max_new)
+    c = [_check("q", q, torch.bfloat16, (total, H, d)), *pages, *table,
+         _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))]
+    words = 0
+    if tree_mask is not None:
+        words = (max_new + 63) // 64
+        c.append(_check("tree_mask", tree_mask, torch.int64, (total, words)))
+    if out is not None:
+        c.append(_check("out", out, torch.bfloat16, (total, H, d)))
+    if lse is not None:
+        c.append(_check("lse", lse, torch.float32, (H, total)))
+    if workspace is not None:
+        c.append(("workspace", workspace))
+    dev = _same_device(*c)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask,
+                                       scale, out, lse, workspace)
+    o = torch.empty_like(q) if out is None else out
+    if lse is None:
+        lse = torch.empty((H, total), dtype=torch.float32, device=dev)
+    if total == 0:
+        return o, lse
+    if workspace is None:
+        workspace = torch.empty(max(fa_fwd_paged_workspace_bytes(B, max_new, H, Hkv, d), 1), dtype=torch.uint8,
+                                device=dev)
+    st = fa_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, tree_mask, words, o, lse, B, max_pages,
+                      num_pages, page_size, max_new, total, H, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
+                      workspace, workspace.numel() * workspace.element_size())
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_paged")
+    return o, lse
+
+
+def cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, stream=None):
+    """Moves the accepted path of each sequence's drafted tokens together, in every layer (k/v_pages
+    [num_pages,page_size,Hkv,d], or with a leading [layers]): the rows of place cache_lens[b] +
+    accepted[b, i] go to place cache_lens[b] + i for i < n_accepted[b] -> new lengths int32 [B].
+    accepted int32 [B,max_accepted] ascends along each path; a path ends before the first entry that
+    does not."""
+    import torch
+
+    pages, layers, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, True)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be [B, max_accepted]")
+    most = accepted.shape[1]
+    dev = _same_device(*pages, *table, _check("accepted", accepted, torch.int32, (B, most)),
+                       _check("n_accepted", n_accepted, torch.int32, (B,)))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted)
+    lens = torch.empty_like(cache_lens)
+    st = fa_cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, lens, B, most, max_pages,
+                          num_pages, page_size, layers, Hkv, d)
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_compact")
+    return lens
+
+
+def cache_fork(page_refs, page_table, cache_lens, parents, page_size, stream=None):
+    """Row b of page_table becomes what row parents[b] was before the call, sharing its pages (-1 empties
+    the row; b leaves it alone) -> new lengths int32 [B].  page_refs int32 [num_pages] counts the rows
+    that hold each page and is kept in step; no key or value moves."""
+    import torch
+
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if page_refs.dim() != 1:
+        raise ValueError("page_refs must be [num_pages]")
+    num_pages = page_refs.shape[0]
+    dev = _same_device(_check("page_refs", page_refs, torch.int32, (num_pages,)), *table,
+                       _check("parents", parents, torch.int32, (B,)))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cache_fork(page_refs, page_table, cache_lens, parents, page_size)
+    lens = torch.empty_like(cache_lens)
+    st = fa_cache_fork(page_refs, page_table, cache_lens, parents, lens, B, max_pages, num_pages, int(page_size))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_fork")
+    return lens
+
+
+def cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace=None, stream=None):
+    """Makes every row of page_table hold new_lens[b] places: shrinking rows give pages back, growing rows
+    take free ones (count 0 in page_refs), lowest first, and a growing row's shared, partly filled last
+    page is first copied into one of its own, in every layer -> (lengths int32 [B], status int32 [2]).
+    status[0] is the number of pages that were missing (then no row has grown), status[1] the number of
+    rows left alone because a length was negative or past the table."""
+    import torch
+
+    pages, layers, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, True)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    c = [_check("page_refs", page_refs, torch.int32, (num_pages,)), *pages, *table,
+         _check("new_lens", new_lens, torch.int32, (B,))]
+    if workspace is not None:
+        c.append(("workspace", workspace))
+    dev = _same_device(*c)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace)
+    lens = torch.empty_like(cache_lens)
+    status = torch.empty(2, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(fa_cache_resize_workspace_bytes(B), 1), dtype=torch.uint8, device=dev)
+    st = fa_cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, lens, status, B, max_pages,
+                         num_pages, page_size, layers, Hkv, d, workspace,
+                         workspace.numel() * workspace.element_size())
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_resize")
+    return lens, status

@@ -28,6 +28,8 @@ int current_device(int *dev) {
   return FA_OK;
 }
 
+}  // namespace
+
 // Once per device: compute capability must be 10.3 (GB300, sm_103a).
 int check_device() {
   int dev;
@@ -42,6 +44,8 @@ int check_device() {
   }
   return g_dev_ok[dev] == 1 ? FA_OK : FA_ERR_UNSUPPORTED;
 }
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

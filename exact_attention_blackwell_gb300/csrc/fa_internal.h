@@ -140,6 +140,45 @@ struct Fp8Params {
   int sched_chunk;
 };
 
+// A paged key/value cache (fa_cache.cu, fa_paged.cu): pages [num_pages,
+// page_size, Hkv, d] bf16, place p of sequence b in row p % page_size of page
+// page_table[b][p / page_size].
+struct PageGeom {
+  const int *page_table;  // [B, max_pages]
+  const int *cache_lens;  // [B]
+  int B, max_pages, num_pages, page_size;
+};
+
+inline bool ptr_aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Argument checks of the page table's and the pages' sizes (FA_OK or the error).
+int check_page_table(int B, int max_pages, int num_pages, int page_size);
+int check_page_rows(int layers, int num_pages, int page_size, int Hkv, int d);
+
+#ifdef __CUDACC__
+// Page of place `pos` of sequence b, or -1 where there is none: outside the
+// table, or an entry that names no page.
+__device__ __forceinline__ int page_of(const PageGeom &g, int b, long long pos) {
+  if (pos < 0 || pos >= (long long)g.max_pages * g.page_size) return -1;
+  const int page = g.page_table[(size_t)b * g.max_pages + (int)(pos / g.page_size)];
+  return page >= 0 && page < g.num_pages ? page : -1;
+}
+
+// Sequence of packed token t: the last b with cu[b] <= t, found by a whole warp
+// 32 offsets at a time (two dependent loads for up to 1024 sequences).  Always
+// in [0, B); a table that does not ascend gives some such value.
+__device__ __forceinline__ int seq_of_token(const int *cu, int B, int t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + (int)(threadIdx.x & 31) * step;
+    const unsigned seen = __ballot_sync(0xffffffffu, at < hi && (at == lo || cu[at] <= t));
+    lo += (31 - __clz(seen)) * step;
+    hi = min(lo + step, hi);
+  }
+  return lo;
+}
+#endif
+
 int launch_fp8_prepare(const Fp8PrepParams &p, cudaStream_t stream);
 int launch_fwd_fp8(const Fp8Params &p, bool causal, cudaStream_t stream);
 
@@ -147,6 +186,9 @@ int launch_fwd_fp8(const Fp8Params &p, bool causal, cudaStream_t stream);
 // bytes for dims 1..3, box extents per dim (box[0] <= 128 bytes), 128-byte swizzle.
 int encode_u8_tile_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                        const uint32_t box[4]);
+
+// FA_OK on a GB300 (compute capability 10.3), else FA_ERR_UNSUPPORTED or FA_ERR_CUDA.
+int check_device();
 
 // Device status word of the current device (a small static device array).
 unsigned *device_status_ptr();

@@ -206,6 +206,99 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
                    const void *dO, void *dq, void *dk, void *dv,
                    int B, int H, int Hkv, int N, int d, float scale, int causal, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key/value cache, and the attention of new tokens over it.  Nothing on
+ * the pages describes serving from a cache; these entry points are what a
+ * decoding loop needs next to fa_fwd_varlen, which computes its prompts.
+ *
+ *   k_pages, v_pages : bf16 [num_pages, page_size, Hkv, d], page_size in {16,
+ *                      32, 64, 128, 256}; the entry points that take `layers`
+ *                      see bf16 [layers, num_pages, page_size, Hkv, d] with one
+ *                      page table for all layers
+ *   page_table       : int32 [B, max_pages]; place p of sequence b is row
+ *                      p % page_size of page page_table[b][p / page_size].  An
+ *                      entry outside [0, num_pages) names no page: its places
+ *                      are never seen, read or written.  max_pages * page_size
+ *                      at most 2^30
+ *   cache_lens       : int32 [B], places in use before the call (a negative
+ *                      length counts as none)
+ *   page_refs        : int32 [num_pages], how many rows of the page table hold
+ *                      each page; 0 = free.  A row of length n holds its first
+ *                      ceil(n / page_size) entries
+ * The tables are read only on the device, so every call is asynchronous and can
+ * be captured in a graph; contents outside these contracts give unspecified
+ * values but no out-of-bounds access.  Sequences in one call must not share the
+ * pages that the call writes (fa_cache_resize sees to that).  B at most 65535
+ * (4096 for fa_cache_fork and fa_cache_resize).  Other rules as above.
+ * ------------------------------------------------------------------------ */
+
+/* New keys and values into the cache: packed rows k, v bf16 [total, Hkv, d],
+ * sequence b being rows [cu_seqlens[b], cu_seqlens[b+1]) (DEVICE int32 [B + 1],
+ * as for fa_fwd_varlen); row i of sequence b goes to place cache_lens[b] + i.
+ * Rows past the table, or whose page entry names no page, are dropped. */
+int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, const int *page_table,
+                    const int *cache_lens, const int *cu_seqlens, int B, int max_pages, int num_pages,
+                    int page_size, int total, int Hkv, int d, void *stream);
+
+/* Attention of the new tokens (one, a chain, or a drafted tree for each
+ * sequence) over the cache, which already holds their own keys and values at
+ * places cache_lens[b] + i (fa_cache_append).  With n_b = cu_seqlens[b+1] -
+ * cu_seqlens[b] new tokens, token i of sequence b sees place p iff
+ *     p < cache_lens[b],  or  p = cache_lens[b] + j, 0 <= j < n_b, and
+ *     tree_mask == NULL ?  j <= i  :  bit j % 64 of word j / 64 of its mask is set
+ * (a token's own bit is not implied).  O and LSE as for fa_fwd over the places
+ * seen; what a token does not see contributes nothing, whatever it holds; a
+ * token that sees nothing gets O = 0 and LSE = -infinity.
+ *   q, o : bf16 [total, H, d];  lse : fp32 [H, total] or NULL;
+ *   tree_mask : DEVICE int64 [total, mask_words], 8-byte aligned, mask_words *
+ *     64 >= max_new, or NULL;
+ *   max_new : no sequence has more new tokens (rows past it are not written),
+ *     at most 256.
+ *   H / Hkv at most 128.  workspace : caller-owned, 256-byte aligned, of at least
+ *     fa_fwd_paged_workspace_bytes() bytes (0 for sizes that would be rejected).
+ * No atomics: the result is bitwise reproducible. */
+size_t fa_fwd_paged_workspace_bytes(int B, int max_new, int H, int Hkv, int d);
+int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
+                 const int *cache_lens, const int *cu_seqlens, const long long *tree_mask, int mask_words, void *o,
+                 float *lse, int B, int max_pages, int num_pages, int page_size, int max_new, int total, int H,
+                 int Hkv, int d, float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Moves an accepted path of drafted tokens together, in every layer: for i <
+ * n_accepted[b] the k and v rows of place cache_lens[b] + accepted[b][i] go to
+ * place cache_lens[b] + i.  accepted : int32 [B, max_accepted], ascending (a
+ * path's tokens follow their parents); n_accepted : int32 [B].  The path ends
+ * before the first entry that does not ascend or lies past the table.
+ * lens_out[b] = cache_lens[b] + the tokens kept. */
+int fa_cache_compact(void *k_pages, void *v_pages, const int *page_table, const int *cache_lens, const int *accepted,
+                     const int *n_accepted, int *lens_out, int B, int max_accepted, int max_pages, int num_pages,
+                     int page_size, int layers, int Hkv, int d, void *stream);
+
+/* Rows of the page table become what other rows were before the call: row b
+ * takes row parents[b]'s pages and length (sharing the pages: no key or value
+ * moves); parents[b] = b, or a value outside [-1, B), leaves the row alone;
+ * parents[b] = -1 empties it.  A changed row gives up the pages it held, its
+ * unused entries become -1, and page_refs is kept in step.  parents : int32 [B]. */
+int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const int *parents, int *lens_out, int B,
+                  int max_pages, int num_pages, int page_size, void *stream);
+
+/* Makes every row of the page table hold new_lens[b] places (int32 [B]).
+ * Shrinking rows give up the pages past ceil(new_lens[b] / page_size) (entries
+ * become -1).  Then growing rows take free pages (count 0), the lowest number
+ * first, in row order; a growing row whose last page is partly filled and also
+ * held by another row first takes a page of its own and copies the filled rows
+ * of that page, in every layer (of several such rows the later ones copy no
+ * more than needed: the last holder keeps the page).  If the free pages do not
+ * suffice for all growing rows, none grows.
+ *   lens_out : int32 [B], new_lens[b], or cache_lens[b] where the row did not change;
+ *   status   : int32 [2]: pages missing (0: every row grew), and how many rows
+ *              were left alone because a length was negative or past the table.
+ *   workspace : 256-byte aligned, at least fa_cache_resize_workspace_bytes(). */
+size_t fa_cache_resize_workspace_bytes(int B);
+int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_table, const int *cache_lens,
+                    const int *new_lens, int *lens_out, int *status, int B, int max_pages, int num_pages,
+                    int page_size, int layers, int Hkv, int d, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
 /* The software 2^x the kernels evaluate on the FMA pipe (FlashAttention-4
  * paper summary, section 2.B: 2^x emulated with FMA instructions, a polynomial
  * of degree 3 to 5 for the fractional part).  Range reduction x = j + f with
