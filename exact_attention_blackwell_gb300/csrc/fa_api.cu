@@ -111,6 +111,19 @@ int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int H
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                        const uint32_t box_dims[4]) {
+  if (get_encoder() != FA_OK) return FA_ERR_CUDA;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t box[4] = {box_dims[0], box_dims[1], box_dims[2], box_dims[3]};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), d, st, box, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 int encode_u8_tile_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                        const uint32_t box_dims[4]) {
   if (get_encoder() != FA_OK) return FA_ERR_CUDA;

@@ -197,6 +197,10 @@ unsigned *device_status_ptr();
 // `box_rows` rows of one head, 128-byte swizzle.  Returns 0 on success.
 int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int Hx, int d, int box_rows);
 
+// Encodes a 4-D bf16 tensor map, box[0] = 64 columns, 128-byte swizzle; strides in bytes for dims 1..3.
+int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                        const uint32_t box[4]);
+
 // Test builds only (-DFA_TEST_STALL): block 0 of the chosen kernel skips one
 // barrier arrival (1: the forward's first P, 2: the dK/dV kernels' first P,
 // 3: the dQ kernels' first dS), so that a bounded wait runs out and the kernel

@@ -10,70 +10,698 @@
 #include <cmath>
 
 #include "fa_internal.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
 
+// Work.  A unit is one key tile (BN places) of one item; an item is one (sequence,
+// kv head, row group), a row group being QT tiles of TB * G rows (TB tokens with
+// the G query heads that share the kv head).  The units of all items stand in one
+// line, cut into equal stretches for the blocks, so that ragged batches keep all
+// SMs busy; the lengths are known on the device only, so every block sums them up
+// itself.  A block that gets only a part of an item writes its unnormalised O with
+// the row maxima and sums; paged_combine_kernel joins the parts.
 struct PagedParams {
-  const __nv_bfloat16 *q, *k_pages, *v_pages;
+  CUtensorMap tm_q;  // [total, Hkv, G, d]: box 64 columns x G heads x TB tokens
+  CUtensorMap tm_k, tm_v;  // [num_pages, page_size, Hkv, d]: box 64 columns x min(page_size, BN) rows of one head
+  const __nv_bfloat16 *v_pages;
   const int *cu;
-  const long long *mask;  // [total, words] or nullptr: a chain
+  const unsigned long long *mask;  // [total, words] or nullptr: a chain
   __nv_bfloat16 *o;
   float *lse;
+  float *part_o;      // [2 * blocks, rows, d] fp32
+  float2 *part_ml;    // [2 * blocks, rows]: row maximum (scaled log2 units) and sum
+  long long *prefix;  // [B + 1] units before each sequence
+  unsigned *status;
   PageGeom g;
-  int words, max_new, total, H, Hkv;
-  float scale;
+  int words, max_new, total, H, Hkv, G, TB;
+  float scale_log2;
 };
 
-// One block per (token, head); each warp takes every fourth visible key, the
-// lanes share the head dimension.
-template <int D>
-__global__ void __launch_bounds__(128) paged_simple_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x / p.H, h = blockIdx.x % p.H, kh = h / (p.H / p.Hkv);
-  const int b = seq_of_token(p.cu, p.g.B, t);
-  const int start = p.cu[b], n = min(min(p.cu[b + 1], p.total) - start, p.max_new), i = t - start;
-  const int len = max(p.g.cache_lens[b], 0);
-  if (i < 0 || i >= n) return;
-  float q[E], acc[E] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(p.q[((size_t)t * p.H + h) * D + lane + 32 * e]) * p.scale;
-  for (int pos = warp; pos < len + n; pos += 4) {
-    if (pos >= len) {
-      const int j = pos - len;
-      const bool sees = p.mask ? (p.mask[(size_t)t * p.words + j / 64] >> (j % 64)) & 1 : j <= i;
-      if (!sees) continue;
+template <int D, int BN_, int QT_>
+struct PagedCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kQBytes = 128 * D * 2;     // one row tile: kBoxes boxes of 128 rows
+  static constexpr int kTileBytes = BN_ * D * 2;  // one tile of K or V
+  static constexpr int kBoxBytes = BN_ * 128;     // its 64-column box
+  static constexpr int kMinBlocks = (QT_ == 1 && D <= 128) ? 2 : 1;
+  static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
+  static constexpr int kStages = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
+  static_assert(kStages >= 2, "ring");
+  static constexpr int kThreads = 128 * QT_ + 64;
+  static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 4 * QT_ + 1;
+  static constexpr int kOCol = BN_ * QT_;
+  static constexpr int kTmemNeed = QT_ * (BN_ + D);
+  static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
+  static_assert(kTmemNeed <= 512 && kMinBlocks * kTmemCols <= 512, "TMEM budget");
+  static constexpr int kOffQ = 0, kOffRing = QT_ * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
+  // barriers: full[S], empty[S], q_full, q_free, s_full[QT], p_full[QT], o_full[QT], drain
+  static constexpr int kNumBars = 2 * kStages + 3 + 3 * QT_;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
+  static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
+};
+
+enum PagedSite : int {
+  kPSiteQ = 31, kPSiteKFull = 32, kPSiteVFull = 33, kPSitePFull = 34, kPSiteEmpty = 35,
+  kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39, kPSiteVTail = 40
+};
+
+// Sequence b: its first new token, their number, places cached, places in all.
+struct PagedSeq {
+  int start, n, len, keys;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
+  PagedSeq s;
+  const long long cap = (long long)p.g.max_pages * p.g.page_size;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  s.start = max(0, min(c0, p.total));
+  s.n = max(0, min(min(c1, p.total) - s.start, p.max_new));
+  s.len = (int)max(0ll, min((long long)p.g.cache_lens[b], cap));
+  s.keys = (int)min((long long)s.len + s.n, cap);
+  return s;
+}
+template <int BN, int QT>
+__device__ __forceinline__ void paged_units(const PagedParams &p, const PagedSeq &s, int &tiles, int &groups) {
+  tiles = (s.keys + BN - 1) / BN;
+  groups = (s.n + p.TB * QT - 1) / (p.TB * QT);
+}
+
+// A stretch of units, item by item; every warp of a block walks its own copy.
+template <int BN, int QT>
+struct PagedWalk {
+  long long u, end, base;
+  int b, tiles, groups;
+  PagedSeq s;
+  // the current item
+  int kh, rg, j0, j1;
+  bool whole, first;
+
+  __device__ void load(const PagedParams &p) {
+    for (; b < p.g.B; ++b) {
+      s = paged_seq(p, b);
+      if (s.n > 0) break;
     }
-    const int page = page_of(p.g, b, pos);
+    if (b < p.g.B) paged_units<BN, QT>(p, s, tiles, groups);
+  }
+  __device__ bool next(const PagedParams &p, long long begin) {
+    if (u >= end) return false;
+    if (u - base >= (long long)tiles * groups * p.Hkv) {
+      base = u;
+      ++b;
+      load(p);
+      if (b >= p.g.B) return false;
+    }
+    const long long r = u - base;
+    const int item = (int)(r / tiles);
+    j0 = (int)(r - (long long)item * tiles);
+    j1 = (int)min((long long)tiles, j0 + (end - u));
+    kh = item / groups;
+    rg = item - kh * groups;
+    whole = j0 == 0 && j1 == tiles;
+    first = u == begin;
+    u += j1 - j0;
+    return true;
+  }
+};
+
+// Which of the 32 new tokens from j0 on (j0 may be negative) token i of the sequence sees.
+__device__ __forceinline__ unsigned seen_bits(const unsigned long long *words, int i, int n, int j0) {
+  if (j0 >= n || j0 <= -32) return 0;
+  unsigned bits;
+  if (words == nullptr) {
+    const int m = i - j0;  // the last one seen
+    bits = m < 0 ? 0u : m >= 31 ? 0xffffffffu : (2u << m) - 1u;
+  } else {
+    const int a = max(j0, 0);
+    unsigned long long w = words[a >> 6] >> (a & 63);
+    if ((a & 63) > 32 && (a >> 6) + 1 <= (n - 1) >> 6) w |= words[(a >> 6) + 1] << (64 - (a & 63));
+    bits = (unsigned)w;
+    if (j0 < 0) bits <<= -j0;
+  }
+  if (n - j0 < 32) bits &= (1u << (n - j0)) - 1u;
+  if (j0 < 0) bits &= 0xffffffffu << -j0;
+  return bits;
+}
+
+// The V rows of a tile that not every row of S sees.  Past the sequence's end
+// they hold anything, and 0 * NaN is NaN: cleared.  Among the new tokens
+// non-finite values are cleared too, and the epilogue adds them to the rows that
+// see them.  By the whole MMA warp, before the tile's P V; returns whether a new
+// token's value was cleared.  Rows from the last page's end on are zeros already.
+template <int D, int BN>
+__device__ __forceinline__ bool clear_unseen(uint8_t *tile, const PagedSeq &s, int kv0, int page_size) {
+  const int r0 = max(s.len - kv0, 0), r1 = min((s.keys + page_size - 1) / page_size * page_size - kv0, BN);
+  const int lane = threadIdx.x & 31, chunk = lane & 7;
+  bool any = false;
+#pragma unroll 1
+  for (int bx = 0; bx < D / 64; ++bx) {
+#pragma unroll 4
+    for (int r = r0 + (lane >> 3); r < r1; r += 4) {
+      uint4 *at = reinterpret_cast<uint4 *>(tile + bx * (BN * 128) + r * 128 + ((chunk ^ (r & 7)) * 16));
+      if (kv0 + r >= s.keys) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint4 x = *at;
+      const uint4 was = x;
+      auto keep = [](uint32_t w) {
+        if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+        if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+        return w;
+      };
+      x = make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
+      if (x.x != was.x || x.y != was.y || x.z != was.z || x.w != was.w) {
+        *at = x;
+        any = true;
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  return __any_sync(0xffffffffu, any);
+}
+
+// Adds to 32 columns of one row's O the non-finite values of the new tokens that
+// it sees at places [p0, p1): their weights are positive, so the sum is theirs.
+__device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &s, int b, int kh,
+                                          const unsigned long long *words, int i, int p0, int p1, int D, int col,
+                                          uint32_t (&o)[32]) {
+  for (int j = max(p0 - s.len, 0); j < min(p1, s.keys) - s.len; ++j) {
+    if (!(seen_bits(words, i, s.keys - s.len, j) & 1u)) continue;
+    const int page = page_of(p.g, b, (long long)s.len + j);
     if (page < 0) continue;
-    const size_t row = ((size_t)page * p.g.page_size + pos % p.g.page_size) * p.Hkv + kh;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += q[e] * __bfloat162float(p.k_pages[row * D + lane + 32 * e]);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float m_new = fmaxf(m, s);
-    const float a = __expf(m - m_new), w = __expf(s - m_new);
-    l = l * a + w;
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * __bfloat162float(p.v_pages[row * D + lane + 32 * e]);
-    m = m_new;
+    const __nv_bfloat16 *v =
+        p.v_pages + (((size_t)page * p.g.page_size + (s.len + j) % p.g.page_size) * p.Hkv + kh) * D + col;
+    for (int e = 0; e < 32; ++e) {
+      const float x = __bfloat162float(v[e]);
+      if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+    }
   }
-  __shared__ float s_m[4], s_l[4], s_acc[4][D];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+}
+
+template <int D, int BN, int QT>
+__global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
+    paged_fwd_kernel(const __grid_constant__ PagedParams p) {
+  using C = PagedCfg<D, BN, QT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
+  const uint32_t q_bar = bar0 + 8u * (2 * C::kStages), qfree_bar = q_bar + 8u;
+  auto s_bar = [&](int t) { return q_bar + 8u * (2 + t); };
+  auto p_bar = [&](int t) { return q_bar + 8u * (2 + QT + t); };
+  auto o_bar = [&](int t) { return q_bar + 8u * (2 + 2 * QT + t); };
+  const uint32_t drain_bar = q_bar + 8u * (2 + 3 * QT);
+  uint8_t *misc = smem + C::kOffMisc;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
+  int *s_b = reinterpret_cast<int *>(misc + 8);
+  volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
+  long long *s_base = reinterpret_cast<long long *>(misc + 16);
+  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
+  long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32 + 1] <= 11
+  const WaitCtx wctx{abort_flag, p.status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const uint32_t bar = bar0 + 8u * i;
+      mbar_init(bar, bar >= p_bar(0) && bar < p_bar(0) + 8u * QT ? 4u : 1u);
+    }
+    *abort_flag = 0;
+    odd[0] = odd[1] = 0;
+    *s_b = -1;
+    fence_mbar_init();
   }
-  for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == C::kLoadWarp && lane == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // ----------------------------------------------------- this block's stretch of the units
+  auto units_of = [&](int b) -> long long {
+    if (b >= p.g.B) return 0;
+    const PagedSeq s = paged_seq(p, b);
+    if (s.n == 0) return 0;
+    int tiles, groups;
+    paged_units<BN, QT>(p, s, tiles, groups);
+    return (long long)tiles * groups * p.Hkv;
+  };
+  constexpr int kWarps = C::kThreads / 32;
+  auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
+    long long sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sums[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sums[w];
+      total += s_sums[w];
+    }
+    return before + sum - x;
+  };
+  long long total_units = 0, mine = units_of(threadIdx.x), first_sum, first_before;
+  first_before = block_scan(mine, first_sum);
+  total_units = first_sum;
+  for (int b0 = C::kThreads; b0 < p.g.B; b0 += C::kThreads) {
+    long long sum;
+    block_scan(units_of(b0 + (int)threadIdx.x), sum);
+    total_units += sum;
+  }
+  const long long per = (total_units + gridDim.x - 1) / gridDim.x;
+  const long long begin = min(per * blockIdx.x, total_units), stop = min(begin + per, total_units);
+  {
+    long long done = 0;
+    for (int b0 = 0; b0 < p.g.B; b0 += C::kThreads) {
+      const int b = b0 + (int)threadIdx.x;
+      long long before = first_before, sum = first_sum, x = mine;
+      if (b0 > 0) {
+        x = units_of(b);
+        before = block_scan(x, sum);
+      }
+      before += done;
+      if (b < p.g.B && begin >= before && begin < before + x) {
+        *s_b = b;
+        *s_base = before;
+      }
+      if (blockIdx.x == 0 && b < p.g.B) p.prefix[b] = before;
+      done += sum;
+      if (blockIdx.x != 0 && done > begin) break;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[p.g.B] = total_units;
+  }
+  tc_fence_before();
   __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float sum = 0.f;
-  for (int w = 0; w < 4; ++w)
-    if (s_l[w] > 0.f) sum += s_l[w] * __expf(s_m[w] - top);
-  for (int c = threadIdx.x; c < D; c += 128) {
-    float x = 0.f;
-    for (int w = 0; w < 4; ++w)
-      if (s_l[w] > 0.f) x += s_acc[w][c] * __expf(s_m[w] - top);
-    p.o[((size_t)t * p.H + h) * D + c] = __float2bfloat16(sum > 0.f ? x / sum : 0.f);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PagedWalk<BN, QT> walk;
+  walk.u = begin;
+  walk.end = *s_b < 0 ? begin : stop;
+  walk.base = *s_base;
+  walk.b = max(*s_b, 0);
+  if (walk.u < walk.end) walk.load(p);
+
+  auto tile_tokens = [&](int t) { return max(0, min(p.TB, walk.s.n - (walk.rg * QT + t) * p.TB)); };
+
+  if (warp < 4 * QT) {
+    // ===================================================== softmax warpgroups
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + (uint32_t)(BN * t);
+    const uint32_t o_tm = tmem + lane_off + C::kOCol + (uint32_t)(D * t);
+    const float c2 = p.scale_log2;
+    const int tok = r / p.G, head = r - tok * p.G;
+    int tile_no = 0, o_no = 0, fill = 0, item = 0;  // tiles and items of this row tile, ring slots, items so far
+    bool ok = true;
+    while (ok && walk.next(p, begin)) {
+      ++item;
+      const int tokens = tile_tokens(t), nt = walk.j1 - walk.j0;
+      const int i = (walk.rg * QT + t) * p.TB + tok;  // this row's token in its sequence
+      const bool live = (warp & 3) * 32 < tokens * p.G;
+      const bool row = r < tokens * p.G;
+      if (tokens > 0) {
+        const unsigned long long *words =
+            p.mask && row ? p.mask + (size_t)(walk.s.start + i) * p.words : nullptr;
+        float m_ref = -INFINITY, l_sum = 0.f;
+        for (int j = 0; j < nt && ok; ++j, ++tile_no) {
+          ok = mbar_wait_warp(s_bar(t), tile_no & 1, wctx, kPSiteSFull);
+          if (!ok) break;
+          tc_fence_after();
+          const int kv0 = (walk.j0 + j) * BN;
+          const bool tail = kv0 + BN > walk.s.len;
+          if (live) {
+            float s[BN];
+            {
+              uint32_t sr[BN / 32][32];
+#pragma unroll
+              for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32(s_tm + 32 * c, sr[c]);
+              tmem_wait_ld(sr[0]);
+#pragma unroll
+              for (int c = 1; c < BN / 32; ++c) reg_tie(sr[c]);
+#pragma unroll
+              for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
+            }
+            const unsigned gone = bad[(fill / 2 + j) & 15];
+            if (tail || gone) {
+#pragma unroll
+              for (int w = 0; w < BN / 32; ++w) {
+                const int at = kv0 + 32 * w;  // place of the word's first column
+                const int pre = walk.s.len - at;
+                unsigned see = pre >= 32 ? 0xffffffffu : pre <= 0 ? 0u : (1u << pre) - 1u;
+                if (pre < 32) see |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
+                if ((gone >> (2 * w)) & 1) see &= 0xffff0000u;
+                if ((gone >> (2 * w)) & 2) see &= 0x0000ffffu;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((see >> c) & 1)) s[32 * w + c] = -INFINITY;
+              }
+            }
+            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+            for (int c = 4; c < BN - 4; c += 8) {
+              mx0 = fmax3(mx0, s[c], s[c + 1]);
+              mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+              mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+              mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+            }
+            mx0 = fmax3(mx0, s[BN - 4], s[BN - 3]);
+            mx1 = fmax3(mx1, s[BN - 2], s[BN - 1]);
+            const float m_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3)) * c2;
+            if (j == 0) {
+              m_ref = m_blk;
+            } else if (__any_sync(0xffffffffu, row && (m_blk - m_ref) > kRescaleTau)) {
+              const float m_new = fmaxf(m_ref, m_blk);
+              const float alpha = m_ref == m_new ? 1.f : ex2_mufu(m_ref - m_new);
+              m_ref = m_new;
+              l_sum *= alpha;
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_tm + 32 * c, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st_32x32b_x32(o_tm + 32 * c, o);
+              }
+            }
+            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: all weights 0
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+            for (int half = 0; half < BN / 64; ++half) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int c = 0; c < 64; c += 4) {
+                float x[4], e[4];
+                ffma2(x[0], x[1], s[64 * half + c], s[64 * half + c + 1], c2, c2, neg_m, neg_m);
+                ffma2(x[2], x[3], s[64 * half + c + 2], s[64 * half + c + 3], c2, c2, neg_m, neg_m);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) e[u] = ex2_mufu(x[u]);
+                fadd2(l0, l1, l0, l1, e[0], e[1]);
+                fadd2(l2, l3, l2, l3, e[2], e[3]);
+                pk[c >> 1] = pack_bf16x2(e[0], e[1]);
+                pk[(c >> 1) + 1] = pack_bf16x2(e[2], e[3]);
+              }
+              tmem_st_32x32b_x32(s_tm + 32 * half, pk);
+            }
+            l_sum += (l0 + l1) + (l2 + l3);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          mbar_arrive_warp(p_bar(t));
+        }
+        // ----------------------------------------------------- epilogue
+        if (ok) ok = mbar_wait_warp(o_bar(t), o_no & 1, wctx, kPSiteOFull);
+        ++o_no;
+        tc_fence_after();
+        if (ok && live) {
+          const int odd_item = odd[t];
+          const int q_row = walk.s.start + i, h = walk.kh * p.G + head;
+          const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * (QT * p.TB * p.G) + t * p.TB * p.G + r;
+          const float inv_l = walk.whole ? (l_sum == 0.f ? 0.f : 1.0f / l_sum) : 1.0f;
+          uint4 *orow = reinterpret_cast<uint4 *>(p.o + ((size_t)q_row * p.H + h) * D);
+          float4 *prow = reinterpret_cast<float4 *>(p.part_o + slot * D);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_tm + 32 * c, o);
+            tmem_wait_ld(o);
+            if (row && odd_item == item) {
+              uint32_t x[32];
+              for (int e = 0; e < 32; ++e) x[e] = o[e];
+              add_unfinite(p, walk.s, walk.b, walk.kh, words, i, walk.j0 * BN, walk.j1 * BN, D, 32 * c, x);
+              for (int e = 0; e < 32; ++e) o[e] = x[e];
+            }
+            if (row && walk.whole) {
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(o[8 * k4 + 2 * e]) * inv_l, __uint_as_float(o[8 * k4 + 2 * e + 1]) * inv_l);
+                orow[4 * c + k4] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else if (row) {
+#pragma unroll
+              for (int k4 = 0; k4 < 8; ++k4)
+                prow[8 * c + k4] = make_float4(__uint_as_float(o[4 * k4]), __uint_as_float(o[4 * k4 + 1]),
+                                               __uint_as_float(o[4 * k4 + 2]), __uint_as_float(o[4 * k4 + 3]));
+            }
+            __syncwarp();
+          }
+          if (row && walk.whole) {
+            if (p.lse != nullptr)
+              p.lse[(size_t)h * p.total + q_row] = (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
+          } else if (row) {
+            p.part_ml[slot] = make_float2(m_ref, l_sum);
+          }
+          tc_fence_before();
+        }
+      }
+      fill += 2 * nt;
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ===================================================== MMA issue (whole warp; the elected lane issues)
+    constexpr uint32_t idesc_s = make_idesc_bf16(128, BN, false, false);
+    constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, false, true);
+    auto slot_of = [&](int f) { return f % C::kStages; };
+    auto par_of = [&](int f) { return (uint32_t)((f / C::kStages) & 1); };
+    uint64_t q_desc[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) q_desc[t] = make_sdesc_sw128(sbase + C::kOffQ + t * C::kQBytes, 0, 1024);
+    const uint64_t ring_desc_k = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
+    const uint64_t ring_desc_v = make_sdesc_sw128(sbase + C::kOffRing, C::kBoxBytes, 1024);
+    auto issue_s = [&](int t, int slot) {
+      const uint64_t kd = ring_desc_k + (uint64_t)((slot * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(tmem + (uint32_t)(BN * t), q_desc[t] + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+               kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+    };
+    auto issue_pv = [&](int t, int slot, bool acc) {
+      const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+        mma_ts(tmem + C::kOCol + (uint32_t)(D * t), tmem + (uint32_t)(BN * t) + 8u * kk, vd + (uint64_t)(kk * 128), idesc_pv,
+               (acc || kk > 0));
+    };
+    int fill = 0, seg = 0;
+    int p_no[QT] = {};
+    bool ok = true, any = false;
+    while (ok && walk.next(p, begin)) {
+      any = true;
+      const int nt = walk.j1 - walk.j0;
+      bool act[QT];
+#pragma unroll
+      for (int t = 0; t < QT; ++t) act[t] = tile_tokens(t) > 0;
+      ok = mbar_wait_warp(q_bar, seg & 1, wctx, kPSiteQ);
+      if (ok) ok = mbar_wait_warp(full_bar(slot_of(fill)), par_of(fill), wctx, kPSiteKFull);
+      if (!ok) break;
+      ++seg;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          if (act[t]) {
+            issue_s(t, slot_of(fill));
+            tc_commit(s_bar(t));
+          }
+        tc_commit(empty_bar(slot_of(fill)));
+        if (nt == 1) tc_commit(qfree_bar);
+      }
+      __syncwarp();
+      for (int j = 0; j < nt && ok; ++j) {
+        const int fv = fill + 2 * j + 1, fk = fv + 1;
+        ok = mbar_wait_warp(full_bar(slot_of(fv)), par_of(fv), wctx, kPSiteVFull);
+        if (!ok) break;
+        const int kv0 = (walk.j0 + j) * BN;
+        bool cleared = false;
+        if (kv0 + BN > walk.s.len)
+          cleared = clear_unseen<D, BN>(smem + C::kOffRing + slot_of(fv) * C::kTileBytes, walk.s, kv0, p.g.page_size);
+        tc_fence_after();
+        bool k_next = false;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          if (!act[t] || !ok) continue;
+          ok = mbar_wait_warp(p_bar(t), p_no[t] & 1, wctx, kPSitePFull);
+          if (!ok) break;
+          ++p_no[t];
+          tc_fence_after();
+          // this row tile's warps have left the epilogue of every earlier item
+          if (cleared && lane == 0) odd[t] = seg;
+          __syncwarp();
+          if (elect_one()) issue_pv(t, slot_of(fv), j > 0);
+          __syncwarp();
+          if (j + 1 < nt) {
+            if (!k_next) {
+              ok = mbar_wait_warp(full_bar(slot_of(fk)), par_of(fk), wctx, kPSiteKFull);
+              if (!ok) break;
+              tc_fence_after();
+              k_next = true;
+            }
+            if (elect_one()) {
+              issue_s(t, slot_of(fk));
+              tc_commit(s_bar(t));
+            }
+            __syncwarp();
+          } else {
+            if (elect_one()) tc_commit(o_bar(t));
+            __syncwarp();
+          }
+        }
+        if (elect_one()) {
+          tc_commit(empty_bar(slot_of(fv)));
+          if (k_next) tc_commit(empty_bar(slot_of(fk)));
+          if (j + 2 == nt) tc_commit(qfree_bar);
+        }
+        __syncwarp();
+      }
+      fill += 2 * nt;
+    }
+    // Drain: every MMA this warp issued completes before TMEM is released.
+    if (any) {
+      if (elect_one()) tc_commit(drain_bar);
+      __syncwarp();
+      if (!mbar_wait_warp(drain_bar, 0, wctx, kPSiteDrain) && *abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test(drain_bar, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      }
+    }
+  } else {
+    // ===================================================== TMA producer (whole warp; one lane per page of a tile)
+    const uint64_t once = policy_evict_first();
+    const int box_rows = min(p.g.page_size, BN), boxes = BN / box_rows;
+    const int shift = 31 - __clz(p.g.page_size);
+    const uint32_t ring = sbase + C::kOffRing;
+    int fill = 0, seg = 0, tile = 0;
+    bool ok = true;
+    while (ok && walk.next(p, begin)) {
+      const int nt = walk.j1 - walk.j0;
+      const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
+      auto page_at = [&](int j) {  // this lane's page of tile j: -2 where the sequence has ended, -1 where there is none
+        const int pos = j * BN + lane * box_rows;
+        if (lane >= boxes || pos >= walk.s.keys) return -2;
+        const int page = row[pos >> shift];
+        return page >= 0 && page < p.g.num_pages ? page : -1;
+      };
+      int page = page_at(walk.j0);
+      for (int j = 0; j < nt && ok; ++j, ++tile) {
+        const int page_next = j + 1 < nt ? page_at(walk.j0 + j + 1) : -2;
+        unsigned gone = page == -1 ? ((1u << (box_rows / 16)) - 1u) << (lane * (box_rows / 16)) : 0u;
+        gone = __reduce_or_sync(0xffffffffu, gone);
+        if (lane == 0) bad[tile & 15] = gone;
+        const int r0 = ((walk.j0 + j) * BN + lane * box_rows) & (p.g.page_size - 1);
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && ok; ++kv, ++fill) {
+          const int s = fill % C::kStages;
+          ok = mbar_wait_warp(empty_bar(s), ((fill / C::kStages) & 1) ^ 1, wctx, kPSiteEmpty);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(full_bar(s), C::kTileBytes);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_4d_hint(ring + s * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, kv ? &p.tm_v : &p.tm_k,
+                               full_bar(s), bx * 64, walk.kh, r0, max(page, -1), once);
+          }
+          if (j == 0 && kv == 0) {
+            // Q after the first K tile: it may have to wait for the previous item's last S
+            if (seg > 0) ok = mbar_wait_warp(qfree_bar, (seg - 1) & 1, wctx, kPSiteQFree);
+            if (!ok) { ++fill; break; }
+            if (lane == 0) {
+              int active = 0;
+              for (int t = 0; t < QT; ++t) active += tile_tokens(t) > 0;
+              mbar_arrive_expect_tx(q_bar, active * C::kBoxes * p.TB * p.G * 128);
+              for (int t = 0; t < QT; ++t)
+                if (tile_tokens(t) > 0)
+                  for (int bx = 0; bx < C::kBoxes; ++bx)
+                    tma_load_4d_hint(sbase + C::kOffQ + t * C::kQBytes + bx * 16384, &p.tm_q, q_bar, bx * 64, 0, walk.kh,
+                                     walk.s.start + (walk.rg * QT + t) * p.TB, once);
+            }
+            ++seg;
+            __syncwarp();
+          }
+        }
+        page = page_next;
+      }
+    }
+    // Every copy issued lands before the block exits (normally they already have).
+    const uint64_t t0 = global_timer_ns();
+    for (int f = max(0, fill - C::kStages); f < fill; ++f)
+      while (!mbar_test(full_bar(f % C::kStages), (f / C::kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+    if (seg > 0)
+      while (!mbar_test(q_bar, (seg - 1) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[(size_t)h * p.total + t] = sum > 0.f ? top + logf(sum) : -INFINITY;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the parts of the items that were cut: one warp per (token, head).
+template <int D, int BN, int QT>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int id = (int)(blockIdx.x * 4 + (threadIdx.x >> 5));
+  if (id >= p.total * p.H) return;
+  const int tok = id / p.H, h = id - tok * p.H;
+  const int b = seq_of_token(p.cu, p.g.B, tok);
+  const PagedSeq s = paged_seq(p, b);
+  const int i = tok - s.start;
+  if (i < 0 || i >= s.n) return;
+  int tiles, groups;
+  paged_units<BN, QT>(p, s, tiles, groups);
+  const int kh = h / p.G, rt = i / p.TB, rg = rt / QT;
+  const int rows = p.TB * p.G;
+  const int row = (rt - rg * QT) * rows + (i - rt * p.TB) * p.G + (h - kh * p.G);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long u0 = p.prefix[b] + (long long)(kh * groups + rg) * tiles;
+  const long long per = (p.prefix[p.g.B] + blocks - 1) / blocks;
+  const int c0 = (int)(u0 / per), c1 = (int)((u0 + tiles - 1) / per);
+  if (c0 == c1) return;  // one block had it all and has written the result
+  auto slot = [&](int c) { return ((size_t)c * 2 + (u0 > c * per ? 1 : 0)) * (QT * rows) + row; };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float top = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[E] = {};
+  for (int c = c0; c <= c1; ++c) {
+    const size_t at = slot(c);
+    const float2 ml = p.part_ml[at];
+    const float w = ex2_mufu(ml.x - top);
+    l += ml.y * w;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 x = *reinterpret_cast<const float2 *>(p.part_o + at * D + 64 * e + 2 * lane);
+      acc[2 * e] += x.x * w;
+      acc[2 * e + 1] += x.y * w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e)
+    *reinterpret_cast<uint32_t *>(p.o + ((size_t)tok * p.H + h) * D + 64 * e + 2 * lane) =
+        pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[(size_t)h * p.total + tok] = (top + __log2f(l)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxNew = 256;
@@ -88,6 +716,62 @@ int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new,
   return FA_OK;
 }
 
+// Blocks of the main kernel: as many as run at once.  (The SM count of a GB300;
+// the result does not depend on it.)
+constexpr int kSMs = 152;
+
+struct PagedPlan {
+  int QT, TB, blocks;
+  size_t part_o, part_ml, prefix, bytes;
+};
+
+PagedPlan paged_plan(int B, int max_new, int G, int d) {
+  PagedPlan w;
+  w.TB = 128 / G < max_new ? 128 / G : max_new;
+  w.QT = max_new > w.TB && d <= 128 ? 2 : 1;
+  w.blocks = kSMs * (w.QT == 1 && d <= 128 ? 2 : 1);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t rows = (size_t)2 * w.blocks * w.QT * w.TB * G;
+  w.part_o = 0;
+  w.part_ml = up(rows * d * 4);
+  w.prefix = w.part_ml + up(rows * 8);
+  w.bytes = w.prefix + up(((size_t)B + 1) * 8);
+  return w;
+}
+
+template <int D, int BN, int QT>
+int launch_paged(PagedParams &p, const PagedPlan &w, const void *q, const void *k_pages, const void *v_pages,
+                 cudaStream_t stream) {
+  using C = PagedCfg<D, BN, QT>;
+  const int box_rows = p.g.page_size < BN ? p.g.page_size : BN;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.total};
+  const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
+  const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
+  if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) ||
+      encode_bf16_tile_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, D, box_rows) ||
+      encode_bf16_tile_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, D, box_rows))
+    return FA_ERR_CUDA;
+  auto kern = paged_fwd_kernel<D, BN, QT>;
+  // on every launch: the attribute belongs to the function on the current device
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+    return FA_ERR_CUDA;
+  kern<<<(unsigned)w.blocks, C::kThreads, C::kSmemBytes, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  // the join starts while the main kernel still runs and waits for its end on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)p.total * p.H + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, BN, QT>, (const PagedParams)p, w.blocks) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -97,7 +781,7 @@ extern "C" {
 
 size_t fa_fwd_paged_workspace_bytes(int B, int max_new, int H, int Hkv, int d) {
   if (check_paged(B, 1, 1, 16, max_new, 0, H, Hkv, d) != FA_OK) return 0;
-  return 256;
+  return paged_plan(B, max_new, H / Hkv, d).bytes;
 }
 
 int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
@@ -118,27 +802,36 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
     return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   if (total == 0) return FA_OK;
+  const PagedPlan w = paged_plan(B, max_new, H / Hkv, d);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
-  p.q = static_cast<const __nv_bfloat16 *>(q);
-  p.k_pages = static_cast<const __nv_bfloat16 *>(k_pages);
   p.v_pages = static_cast<const __nv_bfloat16 *>(v_pages);
   p.cu = cu_seqlens;
-  p.mask = tree_mask;
+  p.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.lse = lse;
+  p.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  p.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
+  p.prefix = reinterpret_cast<long long *>(ws + w.prefix);
+  p.status = device_status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
   p.g = PageGeom{page_table, cache_lens, B, max_pages, num_pages, page_size};
   p.words = mask_words;
   p.max_new = max_new;
   p.total = total;
   p.H = H;
   p.Hkv = Hkv;
-  p.scale = scale;
-  const unsigned grid = (unsigned)total * (unsigned)H;
+  p.G = H / Hkv;
+  p.TB = w.TB;
+  p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64) paged_simple_kernel<64><<<grid, 128, 0, s>>>(p);
-  else if (d == 128) paged_simple_kernel<128><<<grid, 128, 0, s>>>(p);
-  else paged_simple_kernel<256><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  if (d == 64)
+    return w.QT == 2 ? launch_paged<64, 64, 2>(p, w, q, k_pages, v_pages, s)
+                     : launch_paged<64, 64, 1>(p, w, q, k_pages, v_pages, s);
+  if (d == 128)
+    return w.QT == 2 ? launch_paged<128, 64, 2>(p, w, q, k_pages, v_pages, s)
+                     : launch_paged<128, 64, 1>(p, w, q, k_pages, v_pages, s);
+  return launch_paged<256, 64, 1>(p, w, q, k_pages, v_pages, s);
 }
 
 }  // extern "C"
