@@ -15,9 +15,9 @@
 namespace fa {
 namespace {
 
-// Work.  A unit is one key tile (BN places) of one item; an item is one (sequence,
-// kv head, row group), a row group being QT tiles of TB * G rows (TB tokens with
-// the G query heads that share the kv head).  The units of all items stand in one
+// Work.  A unit is one key tile (bn places) of one item; an item is one (sequence,
+// HB adjacent kv heads, row group), a row group being QT tiles of TB * G rows (TB
+// tokens with the G query heads that share a kv head).  The units of all items stand in one
 // line, cut into equal stretches for the blocks, so that ragged batches keep all
 // SMs busy; the lengths are known on the device only, so every block sums them up
 // itself.  A block that gets only a part of an item writes its unnormalised O with
@@ -25,7 +25,7 @@ namespace {
 struct PagedParams {
   CUtensorMap tm_q;  // [total, Hkv, G, d]: box 64 columns x G heads x TB tokens
   CUtensorMap tm_k, tm_v;  // [num_pages, page_size, Hkv, d]: box 64 columns x min(page_size, BN) rows of one head
-  const __nv_bfloat16 *v_pages;
+  const __nv_bfloat16 *q, *v_pages;
   const int *cu;
   const unsigned long long *mask;  // [total, words] or nullptr: a chain
   __nv_bfloat16 *o;
@@ -36,6 +36,7 @@ struct PagedParams {
   unsigned *status;
   PageGeom g;
   int words, max_new, total, H, Hkv, G, TB;
+  int bn, QT, HB;  // places in a tile; row tiles and kv heads of an item
   float scale_log2;
 };
 
@@ -82,14 +83,84 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
   s.keys = (int)min((long long)s.len + s.n, cap);
   return s;
 }
-template <int BN, int QT>
 __device__ __forceinline__ void paged_units(const PagedParams &p, const PagedSeq &s, int &tiles, int &groups) {
-  tiles = (s.keys + BN - 1) / BN;
-  groups = (s.n + p.TB * QT - 1) / (p.TB * QT);
+  tiles = (s.keys + p.bn - 1) / p.bn;
+  groups = (s.n + p.TB * p.QT - 1) / (p.TB * p.QT);
+}
+
+// This block's stretch [begin, end) of all units; *s_b (-1 on entry, for the
+// whole block to see) and *s_base get the sequence it begins in and that one's
+// first unit, after the caller's next barrier.  By all threads of the block.
+// Block 0 also leaves every sequence's first unit in p.prefix for the join.
+struct PagedStretch {
+  long long begin, end;
+};
+template <int THREADS>
+__device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long long *s_sums, int *s_b,
+                                                      long long *s_base) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto units_of = [&](int b) -> long long {
+    if (b >= p.g.B) return 0;
+    const PagedSeq s = paged_seq(p, b);
+    if (s.n == 0) return 0;
+    int tiles, groups;
+    paged_units(p, s, tiles, groups);
+    return (long long)tiles * groups * (p.Hkv / p.HB);
+  };
+  auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
+    long long sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sums[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const long long x = s_sums[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+    return before + sum - x;
+  };
+  long long first_sum;
+  const long long mine = units_of(threadIdx.x), first_before = block_scan(mine, first_sum);
+  long long total_units = first_sum;
+  for (int b0 = THREADS; b0 < p.g.B; b0 += THREADS) {
+    long long sum;
+    block_scan(units_of(b0 + (int)threadIdx.x), sum);
+    total_units += sum;
+  }
+  const long long per = (total_units + gridDim.x - 1) / gridDim.x;
+  PagedStretch r;
+  r.begin = min(per * blockIdx.x, total_units);
+  r.end = min(r.begin + per, total_units);
+  long long done = 0;
+  for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
+    const int b = b0 + (int)threadIdx.x;
+    long long before = first_before, sum = first_sum, x = mine;
+    if (b0 > 0) {
+      x = units_of(b);
+      before = block_scan(x, sum);
+    }
+    before += done;
+    if (b < p.g.B && r.begin >= before && r.begin < before + x) {
+      *s_b = b;
+      *s_base = before;
+    }
+    if (blockIdx.x == 0 && b < p.g.B) p.prefix[b] = before;
+    done += sum;
+    if (blockIdx.x != 0 && done > r.begin) break;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[p.g.B] = total_units;
+  return r;
 }
 
 // A stretch of units, item by item; every warp of a block walks its own copy.
-template <int BN, int QT>
 struct PagedWalk {
   long long u, end, base;
   int b, tiles, groups;
@@ -98,16 +169,23 @@ struct PagedWalk {
   int kh, rg, j0, j1;
   bool whole, first;
 
+  __device__ void start(const PagedParams &p, const PagedStretch &r, int b0, long long base0) {
+    u = r.begin;
+    end = b0 < 0 ? r.begin : r.end;
+    base = base0;
+    b = max(b0, 0);
+    if (u < end) load(p);
+  }
   __device__ void load(const PagedParams &p) {
     for (; b < p.g.B; ++b) {
       s = paged_seq(p, b);
       if (s.n > 0) break;
     }
-    if (b < p.g.B) paged_units<BN, QT>(p, s, tiles, groups);
+    if (b < p.g.B) paged_units(p, s, tiles, groups);
   }
   __device__ bool next(const PagedParams &p, long long begin) {
     if (u >= end) return false;
-    if (u - base >= (long long)tiles * groups * p.Hkv) {
+    if (u - base >= (long long)tiles * groups * (p.Hkv / p.HB)) {
       base = u;
       ++b;
       load(p);
@@ -182,20 +260,22 @@ __device__ __forceinline__ bool clear_unseen(uint8_t *tile, const PagedSeq &s, i
   return __any_sync(0xffffffffu, any);
 }
 
-// Adds to 32 columns of one row's O the non-finite values of the new tokens that
-// it sees at places [p0, p1): their weights are positive, so the sum is theirs.
+// Sums into x the non-finite values, in columns [col, col + count), of the new
+// tokens that a row sees at places [p0, p1): their weights are positive, so the
+// sum belongs to that row's O.
 __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &s, int b, int kh,
                                           const unsigned long long *words, int i, int p0, int p1, int D, int col,
-                                          uint32_t (&o)[32]) {
+                                          int count, float *x) {
+  for (int e = 0; e < count; ++e) x[e] = 0.f;
   for (int j = max(p0 - s.len, 0); j < min(p1, s.keys) - s.len; ++j) {
     if (!(seen_bits(words, i, s.keys - s.len, j) & 1u)) continue;
     const int page = page_of(p.g, b, (long long)s.len + j);
     if (page < 0) continue;
     const __nv_bfloat16 *v =
         p.v_pages + (((size_t)page * p.g.page_size + (s.len + j) % p.g.page_size) * p.Hkv + kh) * D + col;
-    for (int e = 0; e < 32; ++e) {
-      const float x = __bfloat162float(v[e]);
-      if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+    for (int e = 0; e < count; ++e) {
+      const float y = __bfloat162float(v[e]);
+      if (!isfinite(y)) x[e] += y;
     }
   }
 }
@@ -246,74 +326,14 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     prefetch_tmap(&p.tm_v);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ----------------------------------------------------- this block's stretch of the units
-  auto units_of = [&](int b) -> long long {
-    if (b >= p.g.B) return 0;
-    const PagedSeq s = paged_seq(p, b);
-    if (s.n == 0) return 0;
-    int tiles, groups;
-    paged_units<BN, QT>(p, s, tiles, groups);
-    return (long long)tiles * groups * p.Hkv;
-  };
-  constexpr int kWarps = C::kThreads / 32;
-  auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
-    long long sum = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sums[warp] = sum;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_sums[w];
-      total += s_sums[w];
-    }
-    return before + sum - x;
-  };
-  long long total_units = 0, mine = units_of(threadIdx.x), first_sum, first_before;
-  first_before = block_scan(mine, first_sum);
-  total_units = first_sum;
-  for (int b0 = C::kThreads; b0 < p.g.B; b0 += C::kThreads) {
-    long long sum;
-    block_scan(units_of(b0 + (int)threadIdx.x), sum);
-    total_units += sum;
-  }
-  const long long per = (total_units + gridDim.x - 1) / gridDim.x;
-  const long long begin = min(per * blockIdx.x, total_units), stop = min(begin + per, total_units);
-  {
-    long long done = 0;
-    for (int b0 = 0; b0 < p.g.B; b0 += C::kThreads) {
-      const int b = b0 + (int)threadIdx.x;
-      long long before = first_before, sum = first_sum, x = mine;
-      if (b0 > 0) {
-        x = units_of(b);
-        before = block_scan(x, sum);
-      }
-      before += done;
-      if (b < p.g.B && begin >= before && begin < before + x) {
-        *s_b = b;
-        *s_base = before;
-      }
-      if (blockIdx.x == 0 && b < p.g.B) p.prefix[b] = before;
-      done += sum;
-      if (blockIdx.x != 0 && done > begin) break;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[p.g.B] = total_units;
-  }
+  const PagedStretch stretch = block_stretch<C::kThreads>(p, s_sums, s_b, s_base);
+  const long long begin = stretch.begin;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PagedWalk<BN, QT> walk;
-  walk.u = begin;
-  walk.end = *s_b < 0 ? begin : stop;
-  walk.base = *s_base;
-  walk.b = max(*s_b, 0);
-  if (walk.u < walk.end) walk.load(p);
+  PagedWalk walk;
+  walk.start(p, stretch, *s_b, *s_base);
 
   auto tile_tokens = [&](int t) { return max(0, min(p.TB, walk.s.n - (walk.rg * QT + t) * p.TB)); };
 
@@ -441,10 +461,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             tmem_ld_32x32b_x32(o_tm + 32 * c, o);
             tmem_wait_ld(o);
             if (row && odd_item == item) {
-              uint32_t x[32];
-              for (int e = 0; e < 32; ++e) x[e] = o[e];
-              add_unfinite(p, walk.s, walk.b, walk.kh, words, i, walk.j0 * BN, walk.j1 * BN, D, 32 * c, x);
-              for (int e = 0; e < 32; ++e) o[e] = x[e];
+              float x[32];
+              add_unfinite(p, walk.s, walk.b, walk.kh, words, i, walk.j0 * BN, walk.j1 * BN, D, 32 * c, 32, x);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + x[e]);
             }
             if (row && walk.whole) {
 #pragma unroll
@@ -655,53 +674,494 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   }
 }
 
-// Joins the parts of the items that were cut: one warp per (token, head).
-template <int D, int BN, int QT>
+
+// ------------------------------------------------------------------ few rows
+// All rows of a kv head (new tokens x G heads) in one or two 16-row fragments:
+// a decoding step, a short chain.  The cache is read once and each byte of it
+// meets few multiplications, so HBM is the bound and the work around the tiles is
+// what has to be small.  mma.sync.m16n8k16 fits: a warp takes 16 places of a
+// tile through S, softmax and P V in its own registers (running maximum, sum and O
+// of all rows over its own places), so warps only meet in the ring's barriers and,
+// where several of them share a kv head, at an item's end.  The tcgen05 kernel pads
+// the rows to 128 and passes S and P between warps for every tile.
+//
+// A tile is 64 / HB places of HB adjacent kv heads, four warps' work in any case.
+// A head's row is only 128 to 512 bytes of the cache; fetching adjacent heads
+// together keeps DRAM pages and 256-byte L2 lines whole, and with HB = 4 each warp
+// has a head to itself and nothing to join.
+template <int D, int MT>
+struct FewCfg {
+  static constexpr int kWarps = 4, kBoxes = D / 64;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kTileBytes = 16 * kWarps * D * 2;  // K or V of a tile
+  static constexpr int kMinBlocks = D * MT <= 128 ? 2 : 1;
+  static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
+  static constexpr int kJoinBytes = (kWarps / 2) * 16 * MT * D * 4;
+  static constexpr int kStages = (kSmemMax - 1024 - 1024 - kJoinBytes) / (2 * kTileBytes);
+  static_assert(kStages >= 2, "ring");
+  static constexpr int kOffRing = 0, kOffJoin = 2 * kStages * kTileBytes, kOffBar = kOffJoin + kJoinBytes;
+  static constexpr int kOffMisc = kOffBar + 16 * kStages;
+  static constexpr int kOffML = kOffMisc + 64;  // [kWarps][16 * MT] float2
+  static constexpr int kOffSums = kOffML + kWarps * 16 * MT * 8;
+  static constexpr int kSmemBytes = kOffSums + 8 * (kWarps + 1) + 1024;
+  static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// bf16 pairs: infinities and NaNs made zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+enum FewSite : int { kFSiteFull = 41, kFSiteEmpty = 42 };
+
+template <int D, int MT>
+__global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBlocks)
+    paged_few_kernel(const __grid_constant__ PagedParams p) {
+  using C = FewCfg<D, MT>;
+  constexpr int W = C::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto full_bar = [&](int s) { return sbase + C::kOffBar + 8u * s; };
+  auto empty_bar = [&](int s) { return sbase + C::kOffBar + 8u * (C::kStages + s); };
+  uint8_t *misc = smem + C::kOffMisc;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(misc);
+  int *s_b = reinterpret_cast<int *>(misc + 4);
+  long long *s_base = reinterpret_cast<long long *>(misc + 8);
+  volatile int *odd = reinterpret_cast<volatile int *>(misc + 16);             // the last item with cleared V values
+  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 20);   // [kStages] granules without a page
+  static_assert(20 + 4 * C::kStages <= 64, "");
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + C::kOffML);
+  const WaitCtx wctx{abort_flag, p.status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bn = p.bn, box_bytes = bn * 128, head_bytes = bn * D * 2;  // a 64-column box, a head's part of a tile
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), W);
+    }
+    *abort_flag = 0;
+    *odd = 0;
+    *s_b = -1;
+    fence_mbar_init();
+  }
+  if (warp == W && lane == 0) {
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const PagedStretch stretch =
+      block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), s_b, s_base);
+  __syncthreads();
+  PagedWalk walk;
+  walk.start(p, stretch, *s_b, *s_base);
+  bool ok = true;
+
+  if (warp < W) {
+    const int q4 = lane >> 2, c4 = (lane & 3) * 2;
+    const int sharers = W / p.HB, hb = warp / sharers, sub = warp - hb * sharers;  // warps of a kv head
+    const float c2 = p.scale_log2;
+    int fill = 0, item = 0;
+    while (walk.next(p, stretch.begin)) {
+      ++item;
+      const int nt = walk.j1 - walk.j0, rows = walk.s.n * p.G, kh = walk.kh * p.HB + hb;
+      // this thread's rows: 16 m + q4 and + 8
+      uint32_t qf[MT][D / 16][4];
+      int tok[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int r = 16 * m + 8 * hf + q4;
+          tok[m][hf] = r / p.G;
+          const uint32_t *qr = reinterpret_cast<const uint32_t *>(
+              p.q + ((size_t)(walk.s.start + tok[m][hf]) * p.H + kh * p.G + (r - tok[m][hf] * p.G)) * D);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            qf[m][k][hf] = r < rows ? qr[8 * k + (lane & 3)] : 0u;
+            qf[m][k][hf + 2] = r < rows ? qr[8 * k + 4 + (lane & 3)] : 0u;
+          }
+        }
+      auto words = [&](int m, int hf) {
+        return p.mask && 16 * m + 8 * hf + q4 < rows ? p.mask + (size_t)(walk.s.start + tok[m][hf]) * p.words : nullptr;
+      };
+      float o[MT][D / 8][4], m_ref[MT][2], l_sum[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        m_ref[m][0] = m_ref[m][1] = -INFINITY;
+        l_sum[m][0] = l_sum[m][1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+      }
+      bool cleared = false;
+      for (int j = 0; j < nt; ++j, ++fill) {
+        const int slot = fill % C::kStages;
+        if (ok) ok = mbar_wait_warp(full_bar(slot), (fill / C::kStages) & 1, wctx, kFSiteFull);
+        const int kv0 = (walk.j0 + j) * bn + 16 * sub;
+        if (ok && kv0 < walk.s.keys && !((bad[slot] >> sub) & 1)) {
+          const uint32_t kt = sbase + C::kOffRing + 2 * slot * C::kTileBytes + hb * head_bytes + 16 * sub * 128;
+          const uint32_t vt = kt + C::kTileBytes;
+          float s[MT][2][4] = {};
+          {
+            const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t kf[4];
+              ldsm4(kf, kt + (k >> 2) * box_bytes + key * 128 + (((2 * (k & 3) + half) ^ (key & 7)) << 4));
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816(s[m][0], qf[m][k], kf[0], kf[1]);
+                mma16816(s[m][1], qf[m][k], kf[2], kf[3]);
+              }
+            }
+          }
+          const bool tail = kv0 + 16 > walk.s.len;
+          if (tail) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int pre = walk.s.len - kv0;
+                const unsigned see = (pre <= 0 ? 0u : (1u << pre) - 1u) |
+                                     seen_bits(words(m, hf), tok[m][hf], walk.s.keys - walk.s.len, kv0 - walk.s.len);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (!((see >> (8 * n + c4 + e)) & 1)) s[m][n][2 * hf + e] = -INFINITY;
+              }
+          }
+          uint32_t pf[MT][4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            float top[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              top[hf] = fmaxf(fmaxf(s[m][0][2 * hf], s[m][0][2 * hf + 1]), fmaxf(s[m][1][2 * hf], s[m][1][2 * hf + 1])) * c2;
+            // the maximum moves only where a score is more than kRescaleTau above it (at first: above -inf)
+            if (__any_sync(0xffffffffu, top[0] - m_ref[m][0] > kRescaleTau || top[1] - m_ref[m][1] > kRescaleTau)) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                float t = top[hf];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                t = fmaxf(t, m_ref[m][hf]);
+                const float alpha = t == m_ref[m][hf] ? 1.f : ex2_mufu(m_ref[m][hf] - t);
+                m_ref[m][hf] = t;
+                l_sum[m][hf] *= alpha;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                  o[m][n][2 * hf] *= alpha;
+                  o[m][n][2 * hf + 1] *= alpha;
+                }
+              }
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float neg = m_ref[m][hf] == -INFINITY ? 0.f : -m_ref[m][hf];
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const float e0 = ex2_mufu(fmaf(s[m][n][2 * hf], c2, neg)), e1 = ex2_mufu(fmaf(s[m][n][2 * hf + 1], c2, neg));
+                l_sum[m][hf] += e0 + e1;
+                pf[m][2 * n + hf] = pack_bf16x2(e0, e1);
+              }
+            }
+          }
+          const int key = lane & 15, part = lane >> 4;
+          if (!tail) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t vf[4];
+              ldsm4_t(vf, vt + (n >> 2) * box_bytes + key * 128 + (((2 * (n & 3) + part) ^ (key & 7)) << 4));
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816(o[m][2 * n], pf[m], vf[0], vf[1]);
+                mma16816(o[m][2 * n + 1], pf[m], vf[2], vf[3]);
+              }
+            }
+          } else {
+            // Values that not every row sees: past the end they hold anything, and 0 * NaN is NaN; among
+            // the new tokens non-finite ones are left out and added at the item's end to the rows that
+            // see them.  vf[0], vf[2] hold places c4, c4 + 1; vf[1], vf[3] the ones 8 further.
+            const int left = walk.s.keys - kv0 - c4, fresh = walk.s.len - kv0 - c4;
+            auto cut = [&](uint32_t w, int at) {
+              const uint32_t was = w;
+              const uint32_t f = finite_pair(w);
+              if (fresh <= at) w = (w & 0xffff0000u) | (f & 0xffffu);
+              if (fresh <= at + 1) w = (w & 0x0000ffffu) | (f & 0xffff0000u);
+              cleared |= w != was && left > at;
+              if (left <= at) w &= 0xffff0000u;
+              if (left <= at + 1) w &= 0x0000ffffu;
+              return w;
+            };
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t vf[4];
+              ldsm4_t(vf, vt + (n >> 2) * box_bytes + key * 128 + (((2 * (n & 3) + part) ^ (key & 7)) << 4));
+              vf[0] = cut(vf[0], 0);
+              vf[1] = cut(vf[1], 8);
+              vf[2] = cut(vf[2], 0);
+              vf[3] = cut(vf[3], 8);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816(o[m][2 * n], pf[m], vf[0], vf[1]);
+                mma16816(o[m][2 * n + 1], pf[m], vf[2], vf[3]);
+              }
+            }
+          }
+        }
+        mbar_arrive_warp(empty_bar(slot));
+      }
+      float row_l[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float l = l_sum[m][hf];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          row_l[m][hf] = l;  // m_ref is the row's already: its lanes moved it together
+        }
+      bool is_odd = __any_sync(0xffffffffu, cleared);
+      if (sharers > 1) {
+        // ----------------------------------------------------- join the warps of a kv head
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            if ((lane & 3) == 0)
+              s_ml[warp * 16 * MT + 16 * m + 8 * hf + q4] = make_float2(m_ref[m][hf], row_l[m][hf]);
+        if (is_odd && lane == 0) *odd = item;
+        named_bar_sync(1, 32 * W);
+        is_odd = *odd == item;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float2 *ml = s_ml + hb * sharers * 16 * MT + 16 * m + 8 * hf + q4;
+            float top = -INFINITY, l = 0.f;
+            for (int w = 0; w < sharers; ++w) top = fmaxf(top, ml[w * 16 * MT].x);
+            const float base = top == -INFINITY ? 0.f : top;
+            for (int w = 0; w < sharers; ++w) {
+              const float2 x = ml[w * 16 * MT];
+              l += x.y * ex2_mufu(x.x - base);
+            }
+            const float a = ex2_mufu(m_ref[m][hf] - base);
+            m_ref[m][hf] = top;
+            row_l[m][hf] = l;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[m][n][2 * hf] *= a;
+              o[m][n][2 * hf + 1] *= a;
+            }
+          }
+        float4 *join = reinterpret_cast<float4 *>(smem + C::kOffJoin);  // [W / 2][MT * D / 8][32 lanes]
+        for (int step = sharers / 2; step >= 1; step >>= 1) {
+          if (sub >= step && sub < 2 * step) {
+            float4 *to = join + (hb * step + sub - step) * MT * (D / 8) * 32 + lane;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n)
+                to[(m * (D / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+          }
+          named_bar_sync(1, 32 * W);
+          if (sub < step) {
+            const float4 *from = join + (hb * step + sub) * MT * (D / 8) * 32 + lane;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                const float4 x = from[(m * (D / 8) + n) * 32];
+                o[m][n][0] += x.x;
+                o[m][n][1] += x.y;
+                o[m][n][2] += x.z;
+                o[m][n][3] += x.w;
+              }
+          }
+          named_bar_sync(1, 32 * W);
+        }
+      }
+      if (sub == 0 && ok) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int r = 16 * m + 8 * hf + q4;
+            if (r >= rows) continue;
+            const int q_row = walk.s.start + tok[m][hf], h = kh * p.G + (r - tok[m][hf] * p.G);
+            const float l = row_l[m][hf];
+            const size_t slot = (((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * p.HB + hb) * (p.TB * p.G) + r;
+            const float inv = walk.whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;
+            float add[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              if (is_odd) add_unfinite(p, walk.s, walk.b, kh, words(m, hf), tok[m][hf], walk.j0 * bn, walk.j1 * bn, D, 8 * n + c4, 2, add);
+              const float x = (o[m][n][2 * hf] + add[0]) * inv, y = (o[m][n][2 * hf + 1] + add[1]) * inv;
+              if (walk.whole)
+                *reinterpret_cast<uint32_t *>(p.o + ((size_t)q_row * p.H + h) * D + 8 * n + c4) = pack_bf16x2(x, y);
+              else
+                *reinterpret_cast<float2 *>(p.part_o + slot * D + 8 * n + c4) = make_float2(x, y);
+            }
+            if ((lane & 3) == 0) {
+              if (!walk.whole) p.part_ml[slot] = make_float2(m_ref[m][hf], l);
+              else if (p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[m][hf] + __log2f(l)) * 0.69314718055994531f;
+            }
+          }
+      }
+    }
+  } else {
+    // ===================================================== TMA producer: one lane per page, head, and K or V
+    const uint64_t once = policy_evict_first();
+    const int box_rows = min(p.g.page_size, bn), boxes = bn / box_rows;
+    const int shift = 31 - __clz(p.g.page_size);
+    // lane = (kv * HB + head) * boxes + box: at most 2 * HB * (64 / HB) / 16 = 8 lanes
+    const int box = lane % boxes, head = lane / boxes % p.HB, kv = lane / (boxes * p.HB);
+    int fill = 0;
+    while (ok && walk.next(p, stretch.begin)) {
+      const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
+      auto page_at = [&](int j) {  // -2 where the sequence has ended, -1 where there is no page
+        const int pos = j * bn + box * box_rows;
+        if (kv > 1 || pos >= walk.s.keys) return -2;
+        const int page = row[pos >> shift];
+        return page >= 0 && page < p.g.num_pages ? page : -1;
+      };
+      int page = page_at(walk.j0);
+      for (int j = walk.j0; j < walk.j1 && ok; ++j, ++fill) {
+        const int page_next = j + 1 < walk.j1 ? page_at(j + 1) : -2;
+        const int s = fill % C::kStages;
+        ok = mbar_wait_warp(empty_bar(s), ((fill / C::kStages) & 1) ^ 1, wctx, kFSiteEmpty);
+        if (!ok) break;
+        unsigned gone = page == -1 ? ((1u << (box_rows / 16)) - 1u) << (box * (box_rows / 16)) : 0u;
+        gone = __reduce_or_sync(0xffffffffu, gone);
+        if (lane == 0) {
+          bad[s] = gone;
+          mbar_arrive_expect_tx(full_bar(s), 2 * C::kTileBytes);
+        }
+        __syncwarp();
+        if (kv < 2) {
+          const int r0 = (j * bn + box * box_rows) & (p.g.page_size - 1);
+          const uint32_t to = sbase + C::kOffRing + (2 * s + kv) * C::kTileBytes + head * head_bytes + box * box_rows * 128;
+#pragma unroll
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_4d_hint(to + bx * box_bytes, kv ? &p.tm_v : &p.tm_k, full_bar(s), bx * 64, walk.kh * p.HB + head, r0,
+                             max(page, -1), once);
+        }
+        page = page_next;
+      }
+    }
+    const uint64_t t0 = global_timer_ns();
+    for (int f = max(0, fill - C::kStages); f < fill; ++f)
+      while (!mbar_test(full_bar(f % C::kStages), (f / C::kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  }
+}
+
+// Joins the parts of the items that were cut: one block per (token, head), its
+// warps taking every fourth part, four of them in flight each.  Everything that
+// depends on the call's inputs alone is done before the wait for the main kernel.
+template <int D>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int id = (int)(blockIdx.x * 4 + (threadIdx.x >> 5));
-  if (id >= p.total * p.H) return;
-  const int tok = id / p.H, h = id - tok * p.H;
+  __shared__ float s_acc[4][D];
+  __shared__ float s_m[4], s_l[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tok = blockIdx.x / p.H, h = blockIdx.x - tok * p.H;
   const int b = seq_of_token(p.cu, p.g.B, tok);
   const PagedSeq s = paged_seq(p, b);
   const int i = tok - s.start;
   if (i < 0 || i >= s.n) return;
   int tiles, groups;
-  paged_units<BN, QT>(p, s, tiles, groups);
-  const int kh = h / p.G, rt = i / p.TB, rg = rt / QT;
+  paged_units(p, s, tiles, groups);
+  const int kh = h / p.G, rt = i / p.TB, rg = rt / p.QT;
   const int rows = p.TB * p.G;
-  const int row = (rt - rg * QT) * rows + (i - rt * p.TB) * p.G + (h - kh * p.G);
+  const int row = ((kh % p.HB) * p.QT + rt - rg * p.QT) * rows + (i - rt * p.TB) * p.G + (h - kh * p.G);
+  const int item = kh / p.HB * groups + rg;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long u0 = p.prefix[b] + (long long)(kh * groups + rg) * tiles;
+  const long long u0 = p.prefix[b] + (long long)item * tiles;
   const long long per = (p.prefix[p.g.B] + blocks - 1) / blocks;
   const int c0 = (int)(u0 / per), c1 = (int)((u0 + tiles - 1) / per);
   if (c0 == c1) return;  // one block had it all and has written the result
-  auto slot = [&](int c) { return ((size_t)c * 2 + (u0 > c * per ? 1 : 0)) * (QT * rows) + row; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+  // only the first block can have had another item before this one: then it is its second part
+  const bool second = u0 > c0 * per;
+  auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 && second ? 1 : 0)) * (p.HB * p.QT * rows) + row; };
+  float m = -INFINITY, l = 0.f, acc[E] = {};
+  for (int c = c0 + warp; c <= c1; c += 16) {
+    float2 ml[4];
+    float x[4][E];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float top = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[E] = {};
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = slot(c);
-    const float2 ml = p.part_ml[at];
-    const float w = ex2_mufu(ml.x - top);
-    l += ml.y * w;
+    for (int u = 0; u < 4; ++u) {
+      const int cc = c + 4 * u;
+      ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 x = *reinterpret_cast<const float2 *>(p.part_o + at * D + 64 * e + 2 * lane);
-      acc[2 * e] += x.x * w;
-      acc[2 * e + 1] += x.y * w;
+      for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+      if (cc <= c1) {
+        const size_t at = slot(cc);
+        ml[u] = p.part_ml[at];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          *reinterpret_cast<float2 *>(&x[u][e]) = *reinterpret_cast<const float2 *>(p.part_o + at * D + 32 * e + 2 * lane);
+      }
+    }
+    const float m_new = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    const float top = m_new == -INFINITY ? 0.f : m_new;
+    const float a = ex2_mufu(m - top);
+    m = m_new;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = ex2_mufu(ml[u].x - top);
+      l += ml[u].y * w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += x[u][e] * w;
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e)
-    *reinterpret_cast<uint32_t *>(p.o + ((size_t)tok * p.H + h) * D + 64 * e + 2 * lane) =
-        pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[(size_t)h * p.total + tok] = (top + __log2f(l)) * 0.69314718055994531f;
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<float2 *>(&s_acc[warp][32 * e + 2 * lane]) = make_float2(acc[e], acc[e + 1]);
+  __syncthreads();
+  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  if (top == -INFINITY) top = 0.f;
+  float w[4], sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    w[u] = ex2_mufu(s_m[u] - top);
+    sum += s_l[u] * w[u];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  for (int c = 2 * threadIdx.x; c < D; c += 256) {
+    float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      y.x += s_acc[u][c] * w[u];
+      y.y += s_acc[u][c + 1] * w[u];
+    }
+    *reinterpret_cast<uint32_t *>(p.o + ((size_t)tok * p.H + h) * D + c) = pack_bf16x2(y.x * inv, y.y * inv);
+  }
+  if (threadIdx.x == 0 && p.lse) p.lse[(size_t)h * p.total + tok] = (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxNew = 256;
@@ -721,45 +1181,39 @@ int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new,
 constexpr int kSMs = 152;
 
 struct PagedPlan {
-  int QT, TB, blocks;
+  int MT;  // 16-row fragments of the few-rows kernel, 0: the tcgen05 kernel
+  int QT, HB, bn, TB, blocks;
   size_t part_o, part_ml, prefix, bytes;
 };
 
-PagedPlan paged_plan(int B, int max_new, int G, int d) {
+PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
   PagedPlan w;
+  const int rows = max_new * G;
+  w.MT = rows <= 16 ? 1 : rows <= 32 && d <= 128 ? 2 : 0;
   w.TB = 128 / G < max_new ? 128 / G : max_new;
   w.QT = max_new > w.TB && d <= 128 ? 2 : 1;
-  w.blocks = kSMs * (w.QT == 1 && d <= 128 ? 2 : 1);
+  w.HB = !w.MT ? 1 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+  w.bn = 64 / w.HB;
+  w.blocks = kSMs * (w.MT ? (d * w.MT <= 128 ? 2 : 1) : (w.QT == 1 && d <= 128 ? 2 : 1));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t rows = (size_t)2 * w.blocks * w.QT * w.TB * G;
+  const size_t slots = (size_t)2 * w.blocks * w.HB * w.QT * w.TB * G;
   w.part_o = 0;
-  w.part_ml = up(rows * d * 4);
-  w.prefix = w.part_ml + up(rows * 8);
+  w.part_ml = up(slots * d * 4);
+  w.prefix = w.part_ml + up(slots * 8);
   w.bytes = w.prefix + up(((size_t)B + 1) * 8);
   return w;
 }
 
-template <int D, int BN, int QT>
-int launch_paged(PagedParams &p, const PagedPlan &w, const void *q, const void *k_pages, const void *v_pages,
-                 cudaStream_t stream) {
-  using C = PagedCfg<D, BN, QT>;
-  const int box_rows = p.g.page_size < BN ? p.g.page_size : BN;
-  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.total};
-  const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
-  const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
-  if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) ||
-      encode_bf16_tile_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, D, box_rows) ||
-      encode_bf16_tile_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, D, box_rows))
-    return FA_ERR_CUDA;
-  auto kern = paged_fwd_kernel<D, BN, QT>;
+// The main kernel, then the join, which starts while the main kernel still runs
+// and waits for its end on the device.
+int launch_two(const PagedParams &p, int blocks, int threads, int smem, void (*main)(PagedParams),
+               void (*join)(PagedParams, int), cudaStream_t stream) {
   // on every launch: the attribute belongs to the function on the current device
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-    return FA_ERR_CUDA;
-  kern<<<(unsigned)w.blocks, C::kThreads, C::kSmemBytes, stream>>>(p);
+  if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
+  main<<<(unsigned)blocks, threads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  // the join starts while the main kernel still runs and waits for its end on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)p.total * p.H + 3) / 4));
+  cfg.gridDim = dim3((unsigned)((long long)p.total * p.H));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at;
@@ -767,9 +1221,35 @@ int launch_paged(PagedParams &p, const PagedPlan &w, const void *q, const void *
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, BN, QT>, (const PagedParams)p, w.blocks) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, join, p, blocks) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int page_maps(PagedParams &p, const void *k_pages, const void *v_pages, int d) {
+  const int box_rows = p.g.page_size < p.bn ? p.g.page_size : p.bn;
+  return encode_bf16_tile_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows) ||
+                 encode_bf16_tile_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows)
+             ? FA_ERR_CUDA
+             : FA_OK;
+}
+
+template <int D, int BN, int QT>
+int launch_paged(PagedParams &p, int blocks, const void *q, const void *k_pages, const void *v_pages,
+                 cudaStream_t stream) {
+  using C = PagedCfg<D, BN, QT>;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.total};
+  const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
+  const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
+  if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) || page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
+  return launch_two(p, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, paged_combine_kernel<D>,
+                    stream);
+}
+
+template <int D, int MT>
+int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pages, cudaStream_t stream) {
+  using C = FewCfg<D, MT>;
+  if (page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
+  return launch_two(p, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D, MT>, paged_combine_kernel<D>,
+                    stream);
 }
 
 }  // namespace
@@ -781,7 +1261,7 @@ extern "C" {
 
 size_t fa_fwd_paged_workspace_bytes(int B, int max_new, int H, int Hkv, int d) {
   if (check_paged(B, 1, 1, 16, max_new, 0, H, Hkv, d) != FA_OK) return 0;
-  return paged_plan(B, max_new, H / Hkv, d).bytes;
+  return paged_plan(B, max_new, Hkv, H / Hkv, d).bytes;
 }
 
 int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
@@ -802,9 +1282,10 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
     return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   if (total == 0) return FA_OK;
-  const PagedPlan w = paged_plan(B, max_new, H / Hkv, d);
+  const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
   p.v_pages = static_cast<const __nv_bfloat16 *>(v_pages);
   p.cu = cu_seqlens;
   p.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
@@ -823,15 +1304,26 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.TB = w.TB;
+  p.bn = w.bn;
+  p.QT = w.QT;
+  p.HB = w.HB;
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (w.MT == 1) {
+    if (d == 64) return launch_few<64, 1>(p, w.blocks, k_pages, v_pages, s);
+    if (d == 128) return launch_few<128, 1>(p, w.blocks, k_pages, v_pages, s);
+    return launch_few<256, 1>(p, w.blocks, k_pages, v_pages, s);
+  }
+  if (w.MT == 2)
+    return d == 64 ? launch_few<64, 2>(p, w.blocks, k_pages, v_pages, s)
+                   : launch_few<128, 2>(p, w.blocks, k_pages, v_pages, s);
   if (d == 64)
-    return w.QT == 2 ? launch_paged<64, 64, 2>(p, w, q, k_pages, v_pages, s)
-                     : launch_paged<64, 64, 1>(p, w, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<64, 64, 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<64, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
   if (d == 128)
-    return w.QT == 2 ? launch_paged<128, 64, 2>(p, w, q, k_pages, v_pages, s)
-                     : launch_paged<128, 64, 1>(p, w, q, k_pages, v_pages, s);
-  return launch_paged<256, 64, 1>(p, w, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<128, 64, 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<128, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
+  return launch_paged<256, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
 }
 
 }  // extern "C"
