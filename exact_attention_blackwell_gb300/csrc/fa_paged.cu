@@ -30,13 +30,16 @@ struct PagedParams {
   const unsigned long long *mask;  // [total, words] or nullptr: a chain
   __nv_bfloat16 *o;
   float *lse;
-  float *part_o;      // [2 * blocks, rows, d] fp32
+  float *part_o;      // [2 * blocks, d, rows] fp32
   float2 *part_ml;    // [2 * blocks, rows]: row maximum (scaled log2 units) and sum
   long long *prefix;  // [B + 1] units before each sequence
   unsigned *status;
   PageGeom g;
   int words, max_new, total, H, Hkv, G, TB;
-  int bn, QT, HB;  // places in a tile; row tiles and kv heads of an item
+  int bn_log2, QT, HB;  // places in a tile; row tiles and kv heads of an item
+  int heads;            // Hkv / HB
+  int min_units;        // a block's stretch is no shorter
+  int join;             // warps that share a task of the join
   float scale_log2;
 };
 
@@ -84,28 +87,42 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
   return s;
 }
 __device__ __forceinline__ void paged_units(const PagedParams &p, const PagedSeq &s, int &tiles, int &groups) {
-  tiles = (s.keys + p.bn - 1) / p.bn;
-  groups = (s.n + p.TB * p.QT - 1) / (p.TB * p.QT);
+  tiles = (s.keys + (1 << p.bn_log2) - 1) >> p.bn_log2;
+  groups = p.max_new <= p.TB * p.QT ? 1 : (s.n + p.TB * p.QT - 1) / (p.TB * p.QT);
+}
+// a / b for a >= 0, b > 0, in 32 bits where both fit (nearly always)
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
+}
+// Units of a block's stretch.
+__device__ __forceinline__ long long stretch_units(const PagedParams &p, long long total, int blocks) {
+  return max(quot(total + blocks - 1, blocks), (long long)p.min_units);
 }
 
-// This block's stretch [begin, end) of all units; *s_b (-1 on entry, for the
-// whole block to see) and *s_base get the sequence it begins in and that one's
-// first unit, after the caller's next barrier.  By all threads of the block.
-// Block 0 also leaves every sequence's first unit in p.prefix for the join.
+// This block's stretch [begin, end) of all units; *at gets the sequence it begins
+// in (b stays -1 where there is none) and that one's first unit, after the caller's
+// next barrier.  By all threads of the block.  Block 0 also leaves every sequence's
+// first unit in p.prefix for the join.
 struct PagedStretch {
   long long begin, end;
 };
+struct PagedStart {
+  long long base;
+  PagedSeq s;
+  int b;
+};
 template <int THREADS>
-__device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long long *s_sums, int *s_b,
-                                                      long long *s_base) {
+__device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long long *s_sums, PagedStart *at) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PagedSeq s;
   auto units_of = [&](int b) -> long long {
     if (b >= p.g.B) return 0;
-    const PagedSeq s = paged_seq(p, b);
+    s = paged_seq(p, b);
     if (s.n == 0) return 0;
     int tiles, groups;
     paged_units(p, s, tiles, groups);
-    return (long long)tiles * groups * (p.Hkv / p.HB);
+    return (long long)tiles * groups * p.heads;
   };
   auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
     long long sum = x;
@@ -135,7 +152,7 @@ __device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long
     block_scan(units_of(b0 + (int)threadIdx.x), sum);
     total_units += sum;
   }
-  const long long per = (total_units + gridDim.x - 1) / gridDim.x;
+  const long long per = stretch_units(p, total_units, gridDim.x);
   PagedStretch r;
   r.begin = min(per * blockIdx.x, total_units);
   r.end = min(r.begin + per, total_units);
@@ -143,14 +160,15 @@ __device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long
   for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
     const int b = b0 + (int)threadIdx.x;
     long long before = first_before, sum = first_sum, x = mine;
-    if (b0 > 0) {
+    if (p.g.B > THREADS) {
       x = units_of(b);
       before = block_scan(x, sum);
     }
     before += done;
     if (b < p.g.B && r.begin >= before && r.begin < before + x) {
-      *s_b = b;
-      *s_base = before;
+      at->base = before;
+      at->s = s;
+      at->b = b;
     }
     if (blockIdx.x == 0 && b < p.g.B) p.prefix[b] = before;
     done += sum;
@@ -169,12 +187,13 @@ struct PagedWalk {
   int kh, rg, j0, j1;
   bool whole, first;
 
-  __device__ void start(const PagedParams &p, const PagedStretch &r, int b0, long long base0) {
+  __device__ void start(const PagedParams &p, const PagedStretch &r, const PagedStart &at) {
     u = r.begin;
-    end = b0 < 0 ? r.begin : r.end;
-    base = base0;
-    b = max(b0, 0);
-    if (u < end) load(p);
+    end = at.b < 0 ? r.begin : r.end;
+    base = at.base;
+    b = at.b;
+    s = at.s;
+    paged_units(p, s, tiles, groups);
   }
   __device__ void load(const PagedParams &p) {
     for (; b < p.g.B; ++b) {
@@ -185,17 +204,17 @@ struct PagedWalk {
   }
   __device__ bool next(const PagedParams &p, long long begin) {
     if (u >= end) return false;
-    if (u - base >= (long long)tiles * groups * (p.Hkv / p.HB)) {
+    if ((unsigned)(u - base) >= (unsigned)tiles * groups * p.heads) {
       base = u;
       ++b;
       load(p);
       if (b >= p.g.B) return false;
     }
-    const long long r = u - base;
-    const int item = (int)(r / tiles);
-    j0 = (int)(r - (long long)item * tiles);
-    j1 = (int)min((long long)tiles, j0 + (end - u));
-    kh = item / groups;
+    const unsigned r = (unsigned)(u - base);  // a sequence's units fit 31 bits (checked by the host)
+    const int item = (int)(r / (unsigned)tiles);
+    j0 = (int)(r - (unsigned)item * (unsigned)tiles);
+    j1 = end - u < tiles - j0 ? j0 + (int)(end - u) : tiles;
+    kh = groups == 1 ? item : item / groups;
     rg = item - kh * groups;
     whole = j0 == 0 && j1 == tiles;
     first = u == begin;
@@ -298,9 +317,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   uint8_t *misc = smem + C::kOffMisc;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
-  int *s_b = reinterpret_cast<int *>(misc + 8);
+  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 176);  // 32 bytes
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
-  long long *s_base = reinterpret_cast<long long *>(misc + 16);
   volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
   long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32 + 1] <= 11
   const WaitCtx wctx{abort_flag, p.status};
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     }
     *abort_flag = 0;
     odd[0] = odd[1] = 0;
-    *s_b = -1;
+    at->b = -1;
     fence_mbar_init();
   }
   if (warp == C::kMmaWarp) {
@@ -326,14 +344,14 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     prefetch_tmap(&p.tm_v);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const PagedStretch stretch = block_stretch<C::kThreads>(p, s_sums, s_b, s_base);
+  const PagedStretch stretch = block_stretch<C::kThreads>(p, s_sums, at);
   const long long begin = stretch.begin;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PagedWalk walk;
-  walk.start(p, stretch, *s_b, *s_base);
+  walk.start(p, stretch, *at);
 
   auto tile_tokens = [&](int t) { return max(0, min(p.TB, walk.s.n - (walk.rg * QT + t) * p.TB)); };
 
@@ -359,11 +377,21 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             p.mask && row ? p.mask + (size_t)(walk.s.start + i) * p.words : nullptr;
         float m_ref = -INFINITY, l_sum = 0.f;
         for (int j = 0; j < nt && ok; ++j, ++tile_no) {
+          const int kv0 = (walk.j0 + j) * BN;
+          const bool tail = kv0 + BN > walk.s.len;
+          unsigned see[BN / 32];  // the places this row sees, while the tile is being multiplied
+#pragma unroll
+          for (int w = 0; w < BN / 32; ++w) {
+            see[w] = 0xffffffffu;
+            if (tail) {
+              const int at = kv0 + 32 * w, pre = walk.s.len - at;
+              see[w] = pre >= 32 ? 0xffffffffu : pre <= 0 ? 0u : (1u << pre) - 1u;
+              if (pre < 32) see[w] |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
+            }
+          }
           ok = mbar_wait_warp(s_bar(t), tile_no & 1, wctx, kPSiteSFull);
           if (!ok) break;
           tc_fence_after();
-          const int kv0 = (walk.j0 + j) * BN;
-          const bool tail = kv0 + BN > walk.s.len;
           if (live) {
             float s[BN];
             {
@@ -380,15 +408,11 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             if (tail || gone) {
 #pragma unroll
               for (int w = 0; w < BN / 32; ++w) {
-                const int at = kv0 + 32 * w;  // place of the word's first column
-                const int pre = walk.s.len - at;
-                unsigned see = pre >= 32 ? 0xffffffffu : pre <= 0 ? 0u : (1u << pre) - 1u;
-                if (pre < 32) see |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
-                if ((gone >> (2 * w)) & 1) see &= 0xffff0000u;
-                if ((gone >> (2 * w)) & 2) see &= 0x0000ffffu;
+                if ((gone >> (2 * w)) & 1) see[w] &= 0xffff0000u;
+                if ((gone >> (2 * w)) & 2) see[w] &= 0x0000ffffu;
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                  if (!((see >> c) & 1)) s[32 * w + c] = -INFINITY;
+                  if (!((see[w] >> c) & 1)) s[32 * w + c] = -INFINITY;
               }
             }
             float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
@@ -451,10 +475,11 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         if (ok && live) {
           const int odd_item = odd[t];
           const int q_row = walk.s.start + i, h = walk.kh * p.G + head;
-          const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * (QT * p.TB * p.G) + t * p.TB * p.G + r;
+          const int all = QT * p.TB * p.G;
+          const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * all;
           const float inv_l = walk.whole ? (l_sum == 0.f ? 0.f : 1.0f / l_sum) : 1.0f;
           uint4 *orow = reinterpret_cast<uint4 *>(p.o + ((size_t)q_row * p.H + h) * D);
-          float4 *prow = reinterpret_cast<float4 *>(p.part_o + slot * D);
+          float *part = p.part_o + slot * D + t * p.TB * p.G + r;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -476,9 +501,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
               }
             } else if (row) {
 #pragma unroll
-              for (int k4 = 0; k4 < 8; ++k4)
-                prow[8 * c + k4] = make_float4(__uint_as_float(o[4 * k4]), __uint_as_float(o[4 * k4 + 1]),
-                                               __uint_as_float(o[4 * k4 + 2]), __uint_as_float(o[4 * k4 + 3]));
+              for (int e = 0; e < 32; ++e) part[(size_t)(32 * c + e) * all] = __uint_as_float(o[e]);
             }
             __syncwarp();
           }
@@ -486,7 +509,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             if (p.lse != nullptr)
               p.lse[(size_t)h * p.total + q_row] = (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
           } else if (row) {
-            p.part_ml[slot] = make_float2(m_ref, l_sum);
+            p.part_ml[slot + t * p.TB * p.G + r] = make_float2(m_ref, l_sum);
           }
           tc_fence_before();
         }
@@ -701,7 +724,7 @@ struct FewCfg {
   static_assert(kStages >= 2, "ring");
   static constexpr int kOffRing = 0, kOffJoin = 2 * kStages * kTileBytes, kOffBar = kOffJoin + kJoinBytes;
   static constexpr int kOffMisc = kOffBar + 16 * kStages;
-  static constexpr int kOffML = kOffMisc + 64;  // [kWarps][16 * MT] float2
+  static constexpr int kOffML = kOffMisc + 80;  // [kWarps][16 * MT] float2
   static constexpr int kOffSums = kOffML + kWarps * 16 * MT * 8;
   static constexpr int kSmemBytes = kOffSums + 8 * (kWarps + 1) + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
@@ -744,15 +767,14 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
   auto empty_bar = [&](int s) { return sbase + C::kOffBar + 8u * (C::kStages + s); };
   uint8_t *misc = smem + C::kOffMisc;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc);
-  int *s_b = reinterpret_cast<int *>(misc + 4);
-  long long *s_base = reinterpret_cast<long long *>(misc + 8);
-  volatile int *odd = reinterpret_cast<volatile int *>(misc + 16);             // the last item with cleared V values
-  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 20);   // [kStages] granules without a page
-  static_assert(20 + 4 * C::kStages <= 64, "");
+  volatile int *odd = reinterpret_cast<volatile int *>(misc + 4);             // the last item with cleared V values
+  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 8);                  // 32 bytes
+  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 40);  // [kStages] granules without a page
+  static_assert(sizeof(PagedStart) <= 32 && 40 + 4 * C::kStages <= 80, "");
   float2 *s_ml = reinterpret_cast<float2 *>(smem + C::kOffML);
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bn = p.bn, box_bytes = bn * 128, head_bytes = bn * D * 2;  // a 64-column box, a head's part of a tile
+  const int bn = 1 << p.bn_log2, box_bytes = bn * 128, head_bytes = bn * D * 2;  // a 64-column box, a head's part of a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -760,7 +782,7 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
     }
     *abort_flag = 0;
     *odd = 0;
-    *s_b = -1;
+    at->b = -1;
     fence_mbar_init();
   }
   if (warp == W && lane == 0) {
@@ -769,10 +791,10 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const PagedStretch stretch =
-      block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), s_b, s_base);
+      block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), at);
   __syncthreads();
   PagedWalk walk;
-  walk.start(p, stretch, *s_b, *s_base);
+  walk.start(p, stretch, *at);
   bool ok = true;
 
   if (warp < W) {
@@ -1001,29 +1023,45 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
         }
       }
       if (sub == 0 && ok) {
+        if (is_odd) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                if (16 * m + 8 * hf + q4 >= rows) continue;
+                float add[2];
+                add_unfinite(p, walk.s, walk.b, kh, words(m, hf), tok[m][hf], walk.j0 * bn, walk.j1 * bn, D, 8 * n + c4, 2, add);
+                o[m][n][2 * hf] += add[0];
+                o[m][n][2 * hf + 1] += add[1];
+              }
+        }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int r = 16 * m + 8 * hf + q4;
             if (r >= rows) continue;
-            const int q_row = walk.s.start + tok[m][hf], h = kh * p.G + (r - tok[m][hf] * p.G);
             const float l = row_l[m][hf];
-            const size_t slot = (((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * p.HB + hb) * (p.TB * p.G) + r;
-            const float inv = walk.whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.0f;
-            float add[2] = {0.f, 0.f};
+            if (walk.whole) {
+              const int h = kh * p.G + (r - tok[m][hf] * p.G);
+              const size_t q_row = (size_t)walk.s.start + tok[m][hf];
+              const float inv = l == 0.f ? 0.f : 1.0f / l;
+              uint32_t *to = reinterpret_cast<uint32_t *>(p.o + (q_row * p.H + h) * D + c4);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              if (is_odd) add_unfinite(p, walk.s, walk.b, kh, words(m, hf), tok[m][hf], walk.j0 * bn, walk.j1 * bn, D, 8 * n + c4, 2, add);
-              const float x = (o[m][n][2 * hf] + add[0]) * inv, y = (o[m][n][2 * hf + 1] + add[1]) * inv;
-              if (walk.whole)
-                *reinterpret_cast<uint32_t *>(p.o + ((size_t)q_row * p.H + h) * D + 8 * n + c4) = pack_bf16x2(x, y);
-              else
-                *reinterpret_cast<float2 *>(p.part_o + slot * D + 8 * n + c4) = make_float2(x, y);
-            }
-            if ((lane & 3) == 0) {
-              if (!walk.whole) p.part_ml[slot] = make_float2(m_ref[m][hf], l);
-              else if (p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[m][hf] + __log2f(l)) * 0.69314718055994531f;
+              for (int n = 0; n < D / 8; ++n) to[4 * n] = pack_bf16x2(o[m][n][2 * hf] * inv, o[m][n][2 * hf + 1] * inv);
+              if ((lane & 3) == 0 && p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[m][hf] + __log2f(l)) * 0.69314718055994531f;
+            } else {
+              const int all = p.HB * p.TB * p.G, row = hb * p.TB * p.G + r;
+              const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * all;
+              float *to = p.part_o + slot * D + c4 * all + row;
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n, to += 8 * all) {
+                to[0] = o[m][n][2 * hf];
+                to[all] = o[m][n][2 * hf + 1];
+              }
+              if ((lane & 3) == 0) p.part_ml[slot + row] = make_float2(m_ref[m][hf], l);
             }
           }
       }
@@ -1074,94 +1112,117 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
   }
 }
 
-// Joins the parts of the items that were cut: one block per (token, head), its
-// warps taking every fourth part, four of them in flight each.  Everything that
-// depends on the call's inputs alone is done before the wait for the main kernel.
+// Joins the parts of the items that were cut.  A task is eight columns of one row;
+// the p.join warps (1 to 8) that share 32 tasks take every join-th part each, four
+// of them in flight.  Parts are stored column by column, so that the rows of a row
+// tile (neighbouring tasks) are contiguous for the kernels' stores and the loads
+// here.  Everything that depends on the call's inputs alone is done before the wait
+// for the main kernel.
+constexpr int kJoinWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
-  constexpr int E = D / 32;
-  __shared__ float s_acc[4][D];
-  __shared__ float s_m[4], s_l[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok = blockIdx.x / p.H, h = blockIdx.x - tok * p.H;
-  const int b = seq_of_token(p.cu, p.g.B, tok);
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
+  __shared__ float s_part[kJoinWarps][10][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % p.join;
+  const long long id = ((long long)blockIdx.x * (kJoinWarps / p.join) + warp / p.join) * 32 + lane;
+  int tok, h, cg;
+  if (p.HB > 1) {  // neighbours: the heads of a token
+    const long long r = quot(id, p.H);
+    h = (int)(id - r * p.H);
+    tok = (int)(r / (D / 8));
+    cg = (int)(r % (D / 8));
+  } else {  // the rows of a kv head
+    const long long r = quot(id, (long long)p.total * p.G), tg = id - r * p.total * p.G;
+    tok = (int)quot(tg, p.G);
+    cg = (int)(r % (D / 8));
+    h = (int)(r / (D / 8)) * p.G + (int)(tg - (long long)tok * p.G);
+  }
+  bool mine = tok < p.total && h < p.H;
+  if (!mine) tok = h = 0;
+  int b = 0;
+  for (int hi = p.g.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (p.cu[mid] <= tok) b = mid;
+    else hi = mid;
+  }
   const PagedSeq s = paged_seq(p, b);
   const int i = tok - s.start;
-  if (i < 0 || i >= s.n) return;
+  mine = mine && i >= 0 && i < s.n;
   int tiles, groups;
   paged_units(p, s, tiles, groups);
   const int kh = h / p.G, rt = i / p.TB, rg = rt / p.QT;
   const int rows = p.TB * p.G;
   const int row = ((kh % p.HB) * p.QT + rt - rg * p.QT) * rows + (i - rt * p.TB) * p.G + (h - kh * p.G);
-  const int item = kh / p.HB * groups + rg;
+  const int item = kh / p.HB * groups + rg, all = p.HB * p.QT * rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long u0 = p.prefix[b] + (long long)item * tiles;
-  const long long per = (p.prefix[p.g.B] + blocks - 1) / blocks;
-  const int c0 = (int)(u0 / per), c1 = (int)((u0 + tiles - 1) / per);
-  if (c0 == c1) return;  // one block had it all and has written the result
-  // only the first block can have had another item before this one: then it is its second part
-  const bool second = u0 > c0 * per;
-  auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 && second ? 1 : 0)) * (p.HB * p.QT * rows) + row; };
-  float m = -INFINITY, l = 0.f, acc[E] = {};
-  for (int c = c0 + warp; c <= c1; c += 16) {
+  int parts = 0, c0 = 0;
+  long long first = 0;
+  if (mine) {
+    const long long u0 = p.prefix[b] + (long long)item * tiles;
+    const long long per = stretch_units(p, p.prefix[p.g.B], blocks);
+    c0 = (int)quot(u0, per);
+    parts = (int)quot(u0 + tiles - 1, per) - c0 + 1;
+    // only the first block can have had another item before this one: then it is its second part
+    first = (long long)c0 * 2 + (u0 > c0 * per ? 1 : 0);
+    mine = parts > 1;  // else one block had it all and has written the result
+    if (!mine) parts = 0;
+  }
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+  for (int k0 = share; k0 < parts; k0 += 4 * p.join) {
     float2 ml[4];
-    float x[4][E];
+    float x[4][8];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int cc = c + 4 * u;
+      const int k = k0 + u * p.join;
       ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[u][e] = 0.f;
-      if (cc <= c1) {
-        const size_t at = slot(cc);
-        ml[u] = p.part_ml[at];
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+      if (k < parts) {
+        const size_t at = (size_t)(k == 0 ? first : (long long)(c0 + k) * 2) * all;
+        ml[u] = p.part_ml[at + row];
+        const float *from = p.part_o + at * D + (size_t)(8 * cg) * all + row;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-          *reinterpret_cast<float2 *>(&x[u][e]) = *reinterpret_cast<const float2 *>(p.part_o + at * D + 32 * e + 2 * lane);
+        for (int e = 0; e < 8; ++e) x[u][e] = from[(size_t)e * all];
       }
     }
     const float m_new = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-    const float top = m_new == -INFINITY ? 0.f : m_new;
-    const float a = ex2_mufu(m - top);
+    const float top = m_new == -INFINITY ? 0.f : m_new, a = ex2_mufu(m - top);
     m = m_new;
     l *= a;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= a;
+    for (int e = 0; e < 8; ++e) acc[e] *= a;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float w = ex2_mufu(ml[u].x - top);
       l += ml[u].y * w;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += x[u][e] * w;
+      for (int e = 0; e < 8; ++e) acc[e] += x[u][e] * w;
     }
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  if (p.join > 1) {
+    s_part[warp][8][lane] = m;
+    s_part[warp][9][lane] = l;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<float2 *>(&s_acc[warp][32 * e + 2 * lane]) = make_float2(acc[e], acc[e + 1]);
-  __syncthreads();
-  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  if (top == -INFINITY) top = 0.f;
-  float w[4], sum = 0.f;
+    for (int e = 0; e < 8; ++e) s_part[warp][e][lane] = acc[e];
+    __syncthreads();
+    if (share != 0) return;
+    for (int w = warp + 1; w < warp + p.join; ++w) {
+      const float mw = s_part[w][8][lane], m_new = fmaxf(m, mw), top = m_new == -INFINITY ? 0.f : m_new;
+      const float a = ex2_mufu(m - top), aw = ex2_mufu(mw - top);
+      m = m_new;
+      l = l * a + s_part[w][9][lane] * aw;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    w[u] = ex2_mufu(s_m[u] - top);
-    sum += s_l[u] * w[u];
-  }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  for (int c = 2 * threadIdx.x; c < D; c += 256) {
-    float2 y = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      y.x += s_acc[u][c] * w[u];
-      y.y += s_acc[u][c + 1] * w[u];
+      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + s_part[w][e][lane] * aw;
     }
-    *reinterpret_cast<uint32_t *>(p.o + ((size_t)tok * p.H + h) * D + c) = pack_bf16x2(y.x * inv, y.y * inv);
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[(size_t)h * p.total + tok] = (top + __log2f(sum)) * 0.69314718055994531f;
+  if (!mine) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  uint32_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  *reinterpret_cast<uint4 *>(p.o + ((size_t)tok * p.H + h) * D + 8 * cg) = make_uint4(y[0], y[1], y[2], y[3]);
+  if (cg == 0 && p.lse)
+    p.lse[(size_t)h * p.total + tok] = ((m == -INFINITY ? 0.f : m) + __log2f(l)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxNew = 256;
@@ -1180,6 +1241,8 @@ int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new,
 // the result does not depend on it.)
 constexpr int kSMs = 152;
 
+constexpr int kTileKeys = 64;  // places in a tile of the tcgen05 kernel
+
 struct PagedPlan {
   int MT;  // 16-row fragments of the few-rows kernel, 0: the tcgen05 kernel
   int QT, HB, bn, TB, blocks;
@@ -1193,7 +1256,7 @@ PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
   w.TB = 128 / G < max_new ? 128 / G : max_new;
   w.QT = max_new > w.TB && d <= 128 ? 2 : 1;
   w.HB = !w.MT ? 1 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-  w.bn = 64 / w.HB;
+  w.bn = w.MT ? 64 / w.HB : kTileKeys;
   w.blocks = kSMs * (w.MT ? (d * w.MT <= 128 ? 2 : 1) : (w.QT == 1 && d <= 128 ? 2 : 1));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)2 * w.blocks * w.HB * w.QT * w.TB * G;
@@ -1206,15 +1269,16 @@ PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
 
 // The main kernel, then the join, which starts while the main kernel still runs
 // and waits for its end on the device.
-int launch_two(const PagedParams &p, int blocks, int threads, int smem, void (*main)(PagedParams),
+int launch_two(const PagedParams &p, int d, int blocks, int threads, int smem, void (*main)(PagedParams),
                void (*join)(PagedParams, int), cudaStream_t stream) {
   // on every launch: the attribute belongs to the function on the current device
   if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
   main<<<(unsigned)blocks, threads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.total * p.H));
-  cfg.blockDim = dim3(128);
+  const long long tasks = 32 * (kJoinWarps / p.join);
+  cfg.gridDim = dim3((unsigned)(((long long)p.total * p.H * (d / 8) + tasks - 1) / tasks));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1225,7 +1289,7 @@ int launch_two(const PagedParams &p, int blocks, int threads, int smem, void (*m
 }
 
 int page_maps(PagedParams &p, const void *k_pages, const void *v_pages, int d) {
-  const int box_rows = p.g.page_size < p.bn ? p.g.page_size : p.bn;
+  const int bn = 1 << p.bn_log2, box_rows = p.g.page_size < bn ? p.g.page_size : bn;
   return encode_bf16_tile_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows) ||
                  encode_bf16_tile_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows)
              ? FA_ERR_CUDA
@@ -1240,7 +1304,7 @@ int launch_paged(PagedParams &p, int blocks, const void *q, const void *k_pages,
   const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
   const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
   if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) || page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, paged_combine_kernel<D>,
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, paged_combine_kernel<D>,
                     stream);
 }
 
@@ -1248,7 +1312,7 @@ template <int D, int MT>
 int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pages, cudaStream_t stream) {
   using C = FewCfg<D, MT>;
   if (page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D, MT>, paged_combine_kernel<D>,
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D, MT>, paged_combine_kernel<D>,
                     stream);
 }
 
@@ -1283,6 +1347,8 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   if ((rc = check_device()) != FA_OK) return rc;
   if (total == 0) return FA_OK;
   const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
+  // the units of one sequence are counted in 31 bits
+  if ((double)max_pages * page_size / w.bn * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB) >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1304,7 +1370,12 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.TB = w.TB;
-  p.bn = w.bn;
+  p.bn_log2 = w.bn == 128 ? 7 : w.bn == 64 ? 6 : w.bn == 32 ? 5 : 4;
+  p.heads = Hkv / w.HB;
+  p.min_units = w.MT ? 2 : 1;
+  // parts an item is cut into on average, two a warp and four in flight
+  const long long items = (long long)B * p.heads * (w.TB * w.QT >= max_new ? 1 : (max_new + w.TB * w.QT - 1) / (w.TB * w.QT));
+  p.join = w.blocks / items >= 16 ? 8 : w.blocks / items >= 8 ? 4 : 1;
   p.QT = w.QT;
   p.HB = w.HB;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1318,12 +1389,12 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
     return d == 64 ? launch_few<64, 2>(p, w.blocks, k_pages, v_pages, s)
                    : launch_few<128, 2>(p, w.blocks, k_pages, v_pages, s);
   if (d == 64)
-    return w.QT == 2 ? launch_paged<64, 64, 2>(p, w.blocks, q, k_pages, v_pages, s)
-                     : launch_paged<64, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<64, kTileKeys, 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<64, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
   if (d == 128)
-    return w.QT == 2 ? launch_paged<128, 64, 2>(p, w.blocks, q, k_pages, v_pages, s)
-                     : launch_paged<128, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
-  return launch_paged<256, 64, 1>(p, w.blocks, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<128, kTileKeys, 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<128, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
+  return launch_paged<256, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
 }
 
 }  // extern "C"
