@@ -52,20 +52,25 @@ struct PagedCfg {
   static constexpr int kMinBlocks = (QT_ == 1 && D <= 128) ? 2 : 1;
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
   static constexpr int kStages = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
-  static_assert(kStages >= 2, "ring");
+  static_assert(kStages >= 4, "ring");
   static constexpr int kThreads = 128 * QT_ + 64;
   static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 4 * QT_ + 1;
-  static constexpr int kOCol = BN_ * QT_;
-  static constexpr int kTmemNeed = QT_ * (BN_ + D);
+  static constexpr int kOCol = 2 * BN_ * QT_;  // S of row tile t in two buffers at (2 t + tile % 2) BN, then O
+  static constexpr int kTmemNeed = QT_ * (2 * BN_ + D);
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static_assert(kTmemNeed <= 512 && kMinBlocks * kTmemCols <= 512, "TMEM budget");
   static constexpr int kOffQ = 0, kOffRing = QT_ * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
-  // barriers: full[S], empty[S], q_full, q_free, s_full[QT], p_full[QT], o_full[QT], drain
-  static constexpr int kNumBars = 2 * kStages + 3 + 3 * QT_;
+  // barriers: full[S], empty[S], q_full, q_free, s_full[QT][2], p_full[QT][2], pv[QT], o_full[QT], drain.
+  // S runs a tile ahead, so warps of a row tile may be a tile apart: two barriers each, by tile.
+  static constexpr int kNumBars = 2 * kStages + 3 + 6 * QT_;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
 };
+
+// Ring slots of tile j's K and V within an item of nt tiles (K_0 K_1 V_0 K_2 V_1 ... V_last).
+__device__ __forceinline__ int k_fill(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_fill(int j, int nt) { return j + 1 < nt ? 2 * j + 2 : 2 * nt - 1; }
 
 enum PagedSite : int {
   kPSiteQ = 31, kPSiteKFull = 32, kPSiteVFull = 33, kPSitePFull = 34, kPSiteEmpty = 35,
@@ -310,10 +315,11 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
   const uint32_t q_bar = bar0 + 8u * (2 * C::kStages), qfree_bar = q_bar + 8u;
-  auto s_bar = [&](int t) { return q_bar + 8u * (2 + t); };
-  auto p_bar = [&](int t) { return q_bar + 8u * (2 + QT + t); };
-  auto o_bar = [&](int t) { return q_bar + 8u * (2 + 2 * QT + t); };
-  const uint32_t drain_bar = q_bar + 8u * (2 + 3 * QT);
+  auto s_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * t + buf); };
+  auto p_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * QT + 2 * t + buf); };
+  auto pv_bar = [&](int t) { return q_bar + 8u * (2 + 4 * QT + t); };
+  auto o_bar = [&](int t) { return q_bar + 8u * (2 + 5 * QT + t); };
+  const uint32_t drain_bar = q_bar + 8u * (2 + 6 * QT);
   uint8_t *misc = smem + C::kOffMisc;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const uint32_t bar = bar0 + 8u * i;
-      mbar_init(bar, bar >= p_bar(0) && bar < p_bar(0) + 8u * QT ? 4u : 1u);
+      mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : 1u);
     }
     *abort_flag = 0;
     odd[0] = odd[1] = 0;
@@ -360,11 +366,10 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + (uint32_t)(BN * t);
     const uint32_t o_tm = tmem + lane_off + C::kOCol + (uint32_t)(D * t);
     const float c2 = p.scale_log2;
     const int tok = r / p.G, head = r - tok * p.G;
-    int tile_no = 0, o_no = 0, fill = 0, item = 0;  // tiles and items of this row tile, ring slots, items so far
+    int tile_no = 0, o_no = 0, tiles = 0, item = 0;  // tiles and items of this row tile, tiles and items of the block so far
     bool ok = true;
     while (ok && walk.next(p, begin)) {
       ++item;
@@ -389,7 +394,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
               if (pre < 32) see[w] |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
             }
           }
-          ok = mbar_wait_warp(s_bar(t), tile_no & 1, wctx, kPSiteSFull);
+          const uint32_t s_tm = tmem + lane_off + (uint32_t)(BN * (2 * t + (tile_no & 1)));
+          ok = mbar_wait_warp(s_bar(t, tile_no & 1), (tile_no >> 1) & 1, wctx, kPSiteSFull);
           if (!ok) break;
           tc_fence_after();
           if (live) {
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 #pragma unroll
               for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
             }
-            const unsigned gone = bad[(fill / 2 + j) & 15];
+            const unsigned gone = bad[(tiles + j) & 15];
             if (tail || gone) {
 #pragma unroll
               for (int w = 0; w < BN / 32; ++w) {
@@ -429,6 +435,11 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             if (j == 0) {
               m_ref = m_blk;
             } else if (__any_sync(0xffffffffu, row && (m_blk - m_ref) > kRescaleTau)) {
+              // S of this tile was multiplied before P V of the last one: O is read once that is done
+              // (the one before it is: it preceded this tile's S, so the parity is not ambiguous)
+              ok = mbar_wait_warp(pv_bar(t), (tile_no - 1) & 1, wctx, kPSiteOFull);
+              if (!ok) break;
+              tc_fence_after();
               const float m_new = fmaxf(m_ref, m_blk);
               const float alpha = m_ref == m_new ? 1.f : ex2_mufu(m_ref - m_new);
               m_ref = m_new;
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             tmem_wait_st();
             tc_fence_before();
           }
-          mbar_arrive_warp(p_bar(t));
+          mbar_arrive_warp(p_bar(t, tile_no & 1));
         }
         // ----------------------------------------------------- epilogue
         if (ok) ok = mbar_wait_warp(o_bar(t), o_no & 1, wctx, kPSiteOFull);
@@ -514,7 +525,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
           tc_fence_before();
         }
       }
-      fill += 2 * nt;
+      tiles += nt;
     }
   } else if (warp == C::kMmaWarp) {
     // ===================================================== MMA issue (whole warp; the elected lane issues)
@@ -527,22 +538,23 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     for (int t = 0; t < QT; ++t) q_desc[t] = make_sdesc_sw128(sbase + C::kOffQ + t * C::kQBytes, 0, 1024);
     const uint64_t ring_desc_k = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
     const uint64_t ring_desc_v = make_sdesc_sw128(sbase + C::kOffRing, C::kBoxBytes, 1024);
-    auto issue_s = [&](int t, int slot) {
+    auto issue_s = [&](int t, int buf, int slot) {
       const uint64_t kd = ring_desc_k + (uint64_t)((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(tmem + (uint32_t)(BN * t), q_desc[t] + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+        mma_ss(tmem + (uint32_t)(BN * (2 * t + buf)), q_desc[t] + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
     };
-    auto issue_pv = [&](int t, int slot, bool acc) {
+    auto issue_pv = [&](int t, int buf, int slot, bool acc) {
       const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts(tmem + C::kOCol + (uint32_t)(D * t), tmem + (uint32_t)(BN * t) + 8u * kk, vd + (uint64_t)(kk * 128), idesc_pv,
-               (acc || kk > 0));
+        mma_ts(tmem + C::kOCol + (uint32_t)(D * t), tmem + (uint32_t)(BN * (2 * t + buf)) + 8u * kk, vd + (uint64_t)(kk * 128),
+               idesc_pv, (acc || kk > 0));
     };
+    // S runs one tile ahead of the softmax: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
     int fill = 0, seg = 0;
-    int p_no[QT] = {};
+    int s_no[QT] = {}, p_no[QT] = {};  // tiles multiplied so far, by row tile
     bool ok = true, any = false;
     while (ok && walk.next(p, begin)) {
       any = true;
@@ -551,44 +563,56 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 #pragma unroll
       for (int t = 0; t < QT; ++t) act[t] = tile_tokens(t) > 0;
       ok = mbar_wait_warp(q_bar, seg & 1, wctx, kPSiteQ);
-      if (ok) ok = mbar_wait_warp(full_bar(slot_of(fill)), par_of(fill), wctx, kPSiteKFull);
       if (!ok) break;
       ++seg;
-      tc_fence_after();
-      if (elect_one()) {
+      auto multiply_s = [&](int j) {  // S of tile j for the active row tiles
+        const int f = fill + k_fill(j);
+        ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int t = 0; t < QT; ++t)
-          if (act[t]) {
-            issue_s(t, slot_of(fill));
-            tc_commit(s_bar(t));
-          }
-        tc_commit(empty_bar(slot_of(fill)));
-        if (nt == 1) tc_commit(qfree_bar);
-      }
-      __syncwarp();
+          for (int t = 0; t < QT; ++t)
+            if (act[t]) {
+              issue_s(t, s_no[t] & 1, slot_of(f));
+              tc_commit(s_bar(t, s_no[t] & 1));
+            }
+          tc_commit(empty_bar(slot_of(f)));
+          if (j == nt - 1) tc_commit(qfree_bar);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < QT; ++t) s_no[t] += act[t];
+      };
+      multiply_s(0);
+      if (ok && nt > 1) multiply_s(1);
       for (int j = 0; j < nt && ok; ++j) {
-        const int fv = fill + 2 * j + 1, fk = fv + 1;
+        const int fv = fill + v_fill(j, nt);
         ok = mbar_wait_warp(full_bar(slot_of(fv)), par_of(fv), wctx, kPSiteVFull);
         if (!ok) break;
         const int kv0 = (walk.j0 + j) * BN;
         bool cleared = false;
         if (kv0 + BN > walk.s.len)
           cleared = clear_unseen<D, BN>(smem + C::kOffRing + slot_of(fv) * C::kTileBytes, walk.s, kv0, p.g.page_size);
-        tc_fence_after();
         bool k_next = false;
+        const int fk = fill + k_fill(j + 2);
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
           if (!act[t] || !ok) continue;
-          ok = mbar_wait_warp(p_bar(t), p_no[t] & 1, wctx, kPSitePFull);
+          ok = mbar_wait_warp(p_bar(t, p_no[t] & 1), (p_no[t] >> 1) & 1, wctx, kPSitePFull);
           if (!ok) break;
-          ++p_no[t];
           tc_fence_after();
           // this row tile's warps have left the epilogue of every earlier item
           if (cleared && lane == 0) odd[t] = seg;
           __syncwarp();
-          if (elect_one()) issue_pv(t, slot_of(fv), j > 0);
+          if (elect_one()) {
+            issue_pv(t, p_no[t] & 1, slot_of(fv), j > 0);
+            tc_commit(pv_bar(t));
+            if (j == nt - 1) tc_commit(o_bar(t));
+          }
           __syncwarp();
-          if (j + 1 < nt) {
+          ++p_no[t];
+          if (j + 2 < nt) {  // into the buffer that this tile's P just left (the tensor pipe runs in order)
             if (!k_next) {
               ok = mbar_wait_warp(full_bar(slot_of(fk)), par_of(fk), wctx, kPSiteKFull);
               if (!ok) break;
@@ -596,19 +620,17 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
               k_next = true;
             }
             if (elect_one()) {
-              issue_s(t, slot_of(fk));
-              tc_commit(s_bar(t));
+              issue_s(t, s_no[t] & 1, slot_of(fk));
+              tc_commit(s_bar(t, s_no[t] & 1));
             }
             __syncwarp();
-          } else {
-            if (elect_one()) tc_commit(o_bar(t));
-            __syncwarp();
+            ++s_no[t];
           }
         }
         if (elect_one()) {
           tc_commit(empty_bar(slot_of(fv)));
           if (k_next) tc_commit(empty_bar(slot_of(fk)));
-          if (j + 2 == nt) tc_commit(qfree_bar);
+          if (k_next && j + 3 == nt) tc_commit(qfree_bar);
         }
         __syncwarp();
       }
@@ -640,44 +662,53 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         const int page = row[pos >> shift];
         return page >= 0 && page < p.g.num_pages ? page : -1;
       };
-      int page = page_at(walk.j0);
-      for (int j = 0; j < nt && ok; ++j, ++tile) {
-        const int page_next = j + 1 < nt ? page_at(walk.j0 + j + 1) : -2;
-        unsigned gone = page == -1 ? ((1u << (box_rows / 16)) - 1u) << (lane * (box_rows / 16)) : 0u;
-        gone = __reduce_or_sync(0xffffffffu, gone);
-        if (lane == 0) bad[tile & 15] = gone;
-        const int r0 = ((walk.j0 + j) * BN + lane * box_rows) & (p.g.page_size - 1);
-#pragma unroll 1
-        for (int kv = 0; kv < 2 && ok; ++kv, ++fill) {
-          const int s = fill % C::kStages;
-          ok = mbar_wait_warp(empty_bar(s), ((fill / C::kStages) & 1) ^ 1, wctx, kPSiteEmpty);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full_bar(s), C::kTileBytes);
-          __syncwarp();
-          if (lane < boxes) {
+      // in the order the MMA warp takes them: K_0 K_1 V_0 K_2 V_1 ... V_last
+      auto load = [&](const CUtensorMap *map, int j, int page) {
+        const int s = fill % C::kStages;
+        ok = mbar_wait_warp(empty_bar(s), ((fill / C::kStages) & 1) ^ 1, wctx, kPSiteEmpty);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(s), C::kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int r0 = ((walk.j0 + j) * BN + lane * box_rows) & (p.g.page_size - 1);
 #pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_4d_hint(ring + s * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, kv ? &p.tm_v : &p.tm_k,
-                               full_bar(s), bx * 64, walk.kh, r0, max(page, -1), once);
-          }
-          if (j == 0 && kv == 0) {
-            // Q after the first K tile: it may have to wait for the previous item's last S
-            if (seg > 0) ok = mbar_wait_warp(qfree_bar, (seg - 1) & 1, wctx, kPSiteQFree);
-            if (!ok) { ++fill; break; }
-            if (lane == 0) {
-              int active = 0;
-              for (int t = 0; t < QT; ++t) active += tile_tokens(t) > 0;
-              mbar_arrive_expect_tx(q_bar, active * C::kBoxes * p.TB * p.G * 128);
-              for (int t = 0; t < QT; ++t)
-                if (tile_tokens(t) > 0)
-                  for (int bx = 0; bx < C::kBoxes; ++bx)
-                    tma_load_4d_hint(sbase + C::kOffQ + t * C::kQBytes + bx * 16384, &p.tm_q, q_bar, bx * 64, 0, walk.kh,
-                                     walk.s.start + (walk.rg * QT + t) * p.TB, once);
-            }
-            ++seg;
-            __syncwarp();
-          }
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_4d_hint(ring + s * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, map, full_bar(s), bx * 64,
+                             walk.kh, r0, max(page, -1), once);
         }
+        ++fill;
+      };
+      int page = page_at(walk.j0), page_v = -2;
+      for (int j = 0; j <= nt && ok; ++j) {
+        const int page_next = j + 1 < nt ? page_at(walk.j0 + j + 1) : -2;
+        if (j < nt) {
+          unsigned gone = page == -1 ? ((1u << (box_rows / 16)) - 1u) << (lane * (box_rows / 16)) : 0u;
+          gone = __reduce_or_sync(0xffffffffu, gone);
+          if (lane == 0) bad[tile & 15] = gone;
+          ++tile;
+          load(&p.tm_k, j, page);
+          if (!ok) break;
+        }
+        if (j == 0) {
+          // Q after the first K tile: it may have to wait for the previous item's last S
+          if (seg > 0) ok = mbar_wait_warp(qfree_bar, (seg - 1) & 1, wctx, kPSiteQFree);
+          if (!ok) break;
+          if (lane == 0) {
+            int active = 0;
+            for (int t = 0; t < QT; ++t) active += tile_tokens(t) > 0;
+            mbar_arrive_expect_tx(q_bar, active * C::kBoxes * p.TB * p.G * 128);
+            for (int t = 0; t < QT; ++t)
+              if (tile_tokens(t) > 0)
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                  tma_load_4d_hint(sbase + C::kOffQ + t * C::kQBytes + bx * 16384, &p.tm_q, q_bar, bx * 64, 0, walk.kh,
+                                   walk.s.start + (walk.rg * QT + t) * p.TB, once);
+          }
+          ++seg;
+          __syncwarp();
+        } else {
+          load(&p.tm_v, j - 1, page_v);
+        }
+        page_v = page;
         page = page_next;
       }
     }
