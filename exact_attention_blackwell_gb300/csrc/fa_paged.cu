@@ -53,16 +53,16 @@ struct PagedCfg {
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
   static constexpr int kStages = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
   static_assert(kStages >= 4, "ring");
-  static constexpr int kThreads = 128 * QT_ + 64;
-  static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 4 * QT_ + 1;
+  static constexpr int kThreads = 128 * QT_ + 32 * QT_ + 32;  // softmax warps, an MMA warp for each row tile, TMA warp
+  static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 5 * QT_;
   static constexpr int kOCol = 2 * BN_ * QT_;  // S of row tile t in two buffers at (2 t + tile % 2) BN, then O
   static constexpr int kTmemNeed = QT_ * (2 * BN_ + D);
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static_assert(kTmemNeed <= 512 && kMinBlocks * kTmemCols <= 512, "TMEM budget");
   static constexpr int kOffQ = 0, kOffRing = QT_ * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
-  // barriers: full[S], empty[S], q_full, q_free, s_full[QT][2], p_full[QT][2], pv[QT], o_full[QT], drain.
+  // barriers: full[S], empty[S], ready[S], q_full, q_free, s_full[QT][2], p_full[QT][2], pv[QT], o_full[QT], drain[QT].
   // S runs a tile ahead, so warps of a row tile may be a tile apart: two barriers each, by tile.
-  static constexpr int kNumBars = 2 * kStages + 3 + 6 * QT_;
+  static constexpr int kNumBars = 3 * kStages + 2 + 7 * QT_;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
@@ -314,29 +314,33 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   const uint32_t bar0 = sbase + C::kOffBar;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
-  const uint32_t q_bar = bar0 + 8u * (2 * C::kStages), qfree_bar = q_bar + 8u;
+  auto ready_bar = [&](int s) { return bar0 + 8u * (2 * C::kStages + s); };
+  const uint32_t q_bar = bar0 + 8u * (3 * C::kStages), qfree_bar = q_bar + 8u;
   auto s_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * t + buf); };
   auto p_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * QT + 2 * t + buf); };
   auto pv_bar = [&](int t) { return q_bar + 8u * (2 + 4 * QT + t); };
   auto o_bar = [&](int t) { return q_bar + 8u * (2 + 5 * QT + t); };
-  const uint32_t drain_bar = q_bar + 8u * (2 + 6 * QT);
+  auto drain_bar = [&](int t) { return q_bar + 8u * (2 + 6 * QT + t); };
   uint8_t *misc = smem + C::kOffMisc;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
-  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 176);  // 32 bytes
+  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 192);  // 32 bytes
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
+  volatile unsigned *hit = reinterpret_cast<volatile unsigned *>(misc + 240);  // by ring slot: new tokens' V values were cleared
   volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
-  long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32 + 1] <= 11
+  long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32] <= 11
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const uint32_t bar = bar0 + 8u * i;
-      mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : 1u);
+      const bool per_row_tile = (bar >= empty_bar(0) && bar < ready_bar(0)) || bar == qfree_bar;  // one MMA warp each
+      mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : per_row_tile ? (uint32_t)QT : 1u);
     }
     *abort_flag = 0;
     odd[0] = odd[1] = 0;
+    *hit = 0;
     at->b = -1;
     fence_mbar_init();
   }
@@ -369,7 +373,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     const uint32_t o_tm = tmem + lane_off + C::kOCol + (uint32_t)(D * t);
     const float c2 = p.scale_log2;
     const int tok = r / p.G, head = r - tok * p.G;
-    int tile_no = 0, o_no = 0, tiles = 0, item = 0;  // tiles and items of this row tile, tiles and items of the block so far
+    int tile_no = 0, o_no = 0, pv_no = 0;  // tiles, items, and items of several tiles of this row tile so far
+    int tiles = 0, item = 0;               // tiles and items of the block
     bool ok = true;
     while (ok && walk.next(p, begin)) {
       ++item;
@@ -435,9 +440,10 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             if (j == 0) {
               m_ref = m_blk;
             } else if (__any_sync(0xffffffffu, row && (m_blk - m_ref) > kRescaleTau)) {
-              // S of this tile was multiplied before P V of the last one: O is read once that is done
-              // (the one before it is: it preceded this tile's S, so the parity is not ambiguous)
-              ok = mbar_wait_warp(pv_bar(t), (tile_no - 1) & 1, wctx, kPSiteOFull);
+              // O is read once the last tile's P V is done: S of the next tile follows it in the pipe, and
+              // where there is no next tile it has a barrier of its own.
+              if (j + 1 < nt) ok = mbar_wait_warp(s_bar(t, (tile_no + 1) & 1), ((tile_no + 1) >> 1) & 1, wctx, kPSiteOFull);
+              else ok = mbar_wait_warp(pv_bar(t), pv_no & 1, wctx, kPSiteOFull);
               if (!ok) break;
               tc_fence_after();
               const float m_new = fmaxf(m_ref, m_blk);
@@ -482,6 +488,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         // ----------------------------------------------------- epilogue
         if (ok) ok = mbar_wait_warp(o_bar(t), o_no & 1, wctx, kPSiteOFull);
         ++o_no;
+        pv_no += nt > 1;
         tc_fence_after();
         if (ok && live) {
           const int odd_item = odd[t];
@@ -527,122 +534,113 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
       }
       tiles += nt;
     }
-  } else if (warp == C::kMmaWarp) {
-    // ===================================================== MMA issue (whole warp; the elected lane issues)
+  } else if (warp < C::kLoadWarp) {
+    // ===================================================== MMA issue: a warp for each row tile (the elected lane issues)
+    const int t = warp - C::kMmaWarp;
     constexpr uint32_t idesc_s = make_idesc_bf16(128, BN, false, false);
     constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, false, true);
     auto slot_of = [&](int f) { return f % C::kStages; };
     auto par_of = [&](int f) { return (uint32_t)((f / C::kStages) & 1); };
-    uint64_t q_desc[QT];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) q_desc[t] = make_sdesc_sw128(sbase + C::kOffQ + t * C::kQBytes, 0, 1024);
+    const uint64_t q_desc = make_sdesc_sw128(sbase + C::kOffQ + t * C::kQBytes, 0, 1024);
     const uint64_t ring_desc_k = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
     const uint64_t ring_desc_v = make_sdesc_sw128(sbase + C::kOffRing, C::kBoxBytes, 1024);
-    auto issue_s = [&](int t, int buf, int slot) {
+    const uint32_t s_col = tmem + (uint32_t)(2 * BN * t), o_col = tmem + C::kOCol + (uint32_t)(D * t);
+    auto issue_s = [&](int buf, int slot) {
       const uint64_t kd = ring_desc_k + (uint64_t)((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(tmem + (uint32_t)(BN * (2 * t + buf)), q_desc[t] + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+        mma_ss(s_col + (uint32_t)(BN * buf), q_desc + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
     };
-    auto issue_pv = [&](int t, int buf, int slot, bool acc) {
+    auto issue_pv = [&](int buf, int slot, bool acc) {
       const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts(tmem + C::kOCol + (uint32_t)(D * t), tmem + (uint32_t)(BN * (2 * t + buf)) + 8u * kk, vd + (uint64_t)(kk * 128),
-               idesc_pv, (acc || kk > 0));
+        mma_ts(o_col, s_col + (uint32_t)(BN * buf) + 8u * kk, vd + (uint64_t)(kk * 128), idesc_pv, (acc || kk > 0));
     };
     // S runs one tile ahead of the softmax: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
-    int fill = 0, seg = 0;
-    int s_no[QT] = {}, p_no[QT] = {};  // tiles multiplied so far, by row tile
+    int fill = 0, seg = 0, s_no = 0, p_no = 0;  // ring slots, items; tiles of this row tile through S, through P V
+    uint32_t ready_par = 0;                     // by ring slot: parity of its next clearing
     bool ok = true, any = false;
     while (ok && walk.next(p, begin)) {
-      any = true;
       const int nt = walk.j1 - walk.j0;
-      bool act[QT];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) act[t] = tile_tokens(t) > 0;
       ok = mbar_wait_warp(q_bar, seg & 1, wctx, kPSiteQ);
       if (!ok) break;
       ++seg;
-      auto multiply_s = [&](int j) {  // S of tile j for the active row tiles
+      if (QT > 1 && tile_tokens(t) == 0) {
+        // no rows: let go of Q and of every tile, keeping step with the ring
+        if (lane == 0) mbar_arrive(qfree_bar);
+        for (int f = fill; f < fill + 2 * nt && ok; ++f) {
+          ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
+          if (ok && lane == 0) mbar_arrive(empty_bar(slot_of(f)));
+        }
+        for (int j = 0; j < nt; ++j)
+          if ((walk.j0 + j) * BN + BN > walk.s.len) ready_par ^= 1u << slot_of(fill + v_fill(j, nt));
+        fill += 2 * nt;
+        continue;
+      }
+      any = true;
+      auto multiply_s = [&](int j) {  // S of tile j
         const int f = fill + k_fill(j);
         ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
         if (!ok) return;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
-          for (int t = 0; t < QT; ++t)
-            if (act[t]) {
-              issue_s(t, s_no[t] & 1, slot_of(f));
-              tc_commit(s_bar(t, s_no[t] & 1));
-            }
+          issue_s(s_no & 1, slot_of(f));
+          tc_commit(s_bar(t, s_no & 1));
           tc_commit(empty_bar(slot_of(f)));
           if (j == nt - 1) tc_commit(qfree_bar);
         }
         __syncwarp();
-#pragma unroll
-        for (int t = 0; t < QT; ++t) s_no[t] += act[t];
+        ++s_no;
       };
       multiply_s(0);
       if (ok && nt > 1) multiply_s(1);
       for (int j = 0; j < nt && ok; ++j) {
-        const int fv = fill + v_fill(j, nt);
-        ok = mbar_wait_warp(full_bar(slot_of(fv)), par_of(fv), wctx, kPSiteVFull);
-        if (!ok) break;
+        const int fv = fill + v_fill(j, nt), sv = slot_of(fv);
         const int kv0 = (walk.j0 + j) * BN;
         bool cleared = false;
-        if (kv0 + BN > walk.s.len)
-          cleared = clear_unseen<D, BN>(smem + C::kOffRing + slot_of(fv) * C::kTileBytes, walk.s, kv0, p.g.page_size);
-        bool k_next = false;
-        const int fk = fill + k_fill(j + 2);
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          if (!act[t] || !ok) continue;
-          ok = mbar_wait_warp(p_bar(t, p_no[t] & 1), (p_no[t] >> 1) & 1, wctx, kPSitePFull);
-          if (!ok) break;
-          tc_fence_after();
-          // this row tile's warps have left the epilogue of every earlier item
-          if (cleared && lane == 0) odd[t] = seg;
-          __syncwarp();
-          if (elect_one()) {
-            issue_pv(t, p_no[t] & 1, slot_of(fv), j > 0);
-            tc_commit(pv_bar(t));
-            if (j == nt - 1) tc_commit(o_bar(t));
-          }
-          __syncwarp();
-          ++p_no[t];
-          if (j + 2 < nt) {  // into the buffer that this tile's P just left (the tensor pipe runs in order)
-            if (!k_next) {
-              ok = mbar_wait_warp(full_bar(slot_of(fk)), par_of(fk), wctx, kPSiteKFull);
-              if (!ok) break;
-              tc_fence_after();
-              k_next = true;
+        if (kv0 + BN <= walk.s.len) {
+          ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
+        } else if (t == 0) {  // clear what must not be multiplied, for all row tiles
+          ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
+          if (ok) {
+            cleared = clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, kv0, p.g.page_size);
+            if (QT > 1) {
+              if (lane == 0) *hit = cleared ? *hit | (1u << sv) : *hit & ~(1u << sv);
+              mbar_arrive_warp(ready_bar(sv));
             }
-            if (elect_one()) {
-              issue_s(t, s_no[t] & 1, slot_of(fk));
-              tc_commit(s_bar(t, s_no[t] & 1));
-            }
-            __syncwarp();
-            ++s_no[t];
           }
+        } else {
+          ok = mbar_wait_warp(ready_bar(sv), (ready_par >> sv) & 1, wctx, kPSiteVTail);
+          ready_par ^= 1u << sv;
+          cleared = (*hit >> sv) & 1;
         }
+        if (ok) ok = mbar_wait_warp(p_bar(t, p_no & 1), (p_no >> 1) & 1, wctx, kPSitePFull);
+        if (!ok) break;
+        tc_fence_after();
+        // this row tile's warps have left the epilogue of every earlier item
+        if (cleared && lane == 0) odd[t] = seg;
+        __syncwarp();
         if (elect_one()) {
-          tc_commit(empty_bar(slot_of(fv)));
-          if (k_next) tc_commit(empty_bar(slot_of(fk)));
-          if (k_next && j + 3 == nt) tc_commit(qfree_bar);
+          issue_pv(p_no & 1, sv, j > 0);
+          if (j == nt - 1) tc_commit(o_bar(t));
+          if (j == nt - 2) tc_commit(pv_bar(t));
+          tc_commit(empty_bar(sv));
         }
         __syncwarp();
+        ++p_no;
+        if (j + 2 < nt) multiply_s(j + 2);  // into the buffer that P just left (the tensor pipe runs in order)
       }
       fill += 2 * nt;
     }
     // Drain: every MMA this warp issued completes before TMEM is released.
     if (any) {
-      if (elect_one()) tc_commit(drain_bar);
+      if (elect_one()) tc_commit(drain_bar(t));
       __syncwarp();
-      if (!mbar_wait_warp(drain_bar, 0, wctx, kPSiteDrain) && *abort_flag) {
+      if (!mbar_wait_warp(drain_bar(t), 0, wctx, kPSiteDrain) && *abort_flag) {
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_test(drain_bar, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+        while (!mbar_test(drain_bar(t), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
       }
     }
   } else {
