@@ -30,7 +30,7 @@ struct PagedParams {
   const unsigned long long *mask;  // [total, words] or nullptr: a chain
   __nv_bfloat16 *o;
   float *lse;
-  float *part_o;      // [2 * blocks, d, rows] fp32
+  float *part_o;      // [2 * blocks, d, rows] fp32, rows of an item token by token
   float2 *part_ml;    // [2 * blocks, rows]: row maximum (scaled log2 units) and sum
   long long *prefix;  // [B + 1] units before each sequence
   unsigned *status;
@@ -53,28 +53,39 @@ struct PagedCfg {
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
   static constexpr int kStages = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
   static_assert(kStages >= 4, "ring");
-  static constexpr int kThreads = 128 * QT_ + 32 * QT_ + 32;  // softmax warps, an MMA warp for each row tile, TMA warp
-  static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 5 * QT_;
-  static constexpr int kOCol = 2 * BN_ * QT_;  // S of row tile t in two buffers at (2 t + tile % 2) BN, then O
-  static constexpr int kTmemNeed = QT_ * (2 * BN_ + D);
+  static constexpr int kThreads = 128 * QT_ + 64;  // softmax warps, MMA warp, TMA warp
+  static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 4 * QT_ + 1;
+  // S of row tile t: 128 columns from 128 t (two tiles of 64 places, or one of 128), then O
+  static constexpr int kOCol = 128 * QT_;
+  static constexpr int kTmemNeed = QT_ * (128 + D);
+  static constexpr bool kPair = BN_ == 128;
+  static_assert(BN_ == 64 || BN_ == 128, "");
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static_assert(kTmemNeed <= 512 && kMinBlocks * kTmemCols <= 512, "TMEM budget");
   static constexpr int kOffQ = 0, kOffRing = QT_ * kQBytes, kOffBar = kOffRing + kStages * kTileBytes;
-  // barriers: full[S], empty[S], ready[S], q_full, q_free, s_full[QT][2], p_full[QT][2], pv[QT], o_full[QT], drain[QT].
-  // S runs a tile ahead, so warps of a row tile may be a tile apart: two barriers each, by tile.
-  static constexpr int kNumBars = 3 * kStages + 2 + 7 * QT_;
+  // barriers: full[S], empty[S], q_full, q_free, s_full[QT][2], p_full[QT][2], pv[QT], o_full[QT], drain.
+  // Warps of a row tile may be a buffer apart: two barriers each, by buffer.
+  static constexpr int kNumBars = 2 * kStages + 3 + 6 * QT_;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
 };
 
-// Ring slots of tile j's K and V within an item of nt tiles (K_0 K_1 V_0 K_2 V_1 ... V_last).
-__device__ __forceinline__ int k_fill(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int v_fill(int j, int nt) { return j + 1 < nt ? 2 * j + 2 : 2 * nt - 1; }
+// Ring slots of tile j's K and V within an item of nt tiles, in the order the MMA
+// warp takes them: K_0 V_0 K_1 V_1 ... where a tile is a pair of halves, else (S a
+// tile ahead) K_0 K_1 V_0 K_2 V_1 ... V_last.
+template <bool PAIR>
+__device__ __forceinline__ int k_fill(int j) {
+  return PAIR ? 2 * j : j == 0 ? 0 : 2 * j - 1;
+}
+template <bool PAIR>
+__device__ __forceinline__ int v_fill(int j, int nt) {
+  return PAIR ? 2 * j + 1 : j + 1 < nt ? 2 * j + 2 : 2 * nt - 1;
+}
 
 enum PagedSite : int {
   kPSiteQ = 31, kPSiteKFull = 32, kPSiteVFull = 33, kPSitePFull = 34, kPSiteEmpty = 35,
-  kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39, kPSiteVTail = 40
+  kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39
 };
 
 // Sequence b: its first new token, their number, places cached, places in all.
@@ -314,19 +325,17 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   const uint32_t bar0 = sbase + C::kOffBar;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::kStages + s); };
-  auto ready_bar = [&](int s) { return bar0 + 8u * (2 * C::kStages + s); };
-  const uint32_t q_bar = bar0 + 8u * (3 * C::kStages), qfree_bar = q_bar + 8u;
+  const uint32_t q_bar = bar0 + 8u * (2 * C::kStages), qfree_bar = q_bar + 8u;
   auto s_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * t + buf); };
   auto p_bar = [&](int t, int buf) { return q_bar + 8u * (2 + 2 * QT + 2 * t + buf); };
   auto pv_bar = [&](int t) { return q_bar + 8u * (2 + 4 * QT + t); };
   auto o_bar = [&](int t) { return q_bar + 8u * (2 + 5 * QT + t); };
-  auto drain_bar = [&](int t) { return q_bar + 8u * (2 + 6 * QT + t); };
+  const uint32_t drain_bar = q_bar + 8u * (2 + 6 * QT);
   uint8_t *misc = smem + C::kOffMisc;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
   PagedStart *at = reinterpret_cast<PagedStart *>(misc + 192);  // 32 bytes
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
-  volatile unsigned *hit = reinterpret_cast<volatile unsigned *>(misc + 240);  // by ring slot: new tokens' V values were cleared
   volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
   long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32] <= 11
   const WaitCtx wctx{abort_flag, p.status};
@@ -335,12 +344,10 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const uint32_t bar = bar0 + 8u * i;
-      const bool per_row_tile = (bar >= empty_bar(0) && bar < ready_bar(0)) || bar == qfree_bar;  // one MMA warp each
-      mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : per_row_tile ? (uint32_t)QT : 1u);
+      mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : 1u);
     }
     *abort_flag = 0;
     odd[0] = odd[1] = 0;
-    *hit = 0;
     at->b = -1;
     fence_mbar_init();
   }
@@ -386,12 +393,13 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         const unsigned long long *words =
             p.mask && row ? p.mask + (size_t)(walk.s.start + i) * p.words : nullptr;
         float m_ref = -INFINITY, l_sum = 0.f;
-        for (int j = 0; j < nt && ok; ++j, ++tile_no) {
-          const int kv0 = (walk.j0 + j) * BN;
-          const bool tail = kv0 + BN > walk.s.len;
-          unsigned see[BN / 32];  // the places this row sees, while the tile is being multiplied
+        // 64 columns at a time: a tile, or half of one
+        for (int j = 0; j < nt * (BN / 64) && ok; ++j, ++tile_no) {
+          const int kv0 = walk.j0 * BN + 64 * j;
+          const bool tail = kv0 + 64 > walk.s.len;
+          unsigned see[2];  // the places this row sees, while the tile is being multiplied
 #pragma unroll
-          for (int w = 0; w < BN / 32; ++w) {
+          for (int w = 0; w < 2; ++w) {
             see[w] = 0xffffffffu;
             if (tail) {
               const int at = kv0 + 32 * w, pre = walk.s.len - at;
@@ -399,26 +407,27 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
               if (pre < 32) see[w] |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
             }
           }
-          const uint32_t s_tm = tmem + lane_off + (uint32_t)(BN * (2 * t + (tile_no & 1)));
-          ok = mbar_wait_warp(s_bar(t, tile_no & 1), (tile_no >> 1) & 1, wctx, kPSiteSFull);
+          const int buf = tile_no & 1, par = (tile_no >> 1) & 1;
+          const uint32_t s_tm = tmem + lane_off + (uint32_t)(64 * (2 * t + buf));
+          if (!C::kPair) ok = mbar_wait_warp(s_bar(t, buf), par, wctx, kPSiteSFull);
+          else if (buf == 0) ok = mbar_wait_warp(s_bar(t, 0), par, wctx, kPSiteSFull);
           if (!ok) break;
           tc_fence_after();
           if (live) {
-            float s[BN];
+            float s[64];
             {
-              uint32_t sr[BN / 32][32];
-#pragma unroll
-              for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32(s_tm + 32 * c, sr[c]);
+              uint32_t sr[2][32];
+              tmem_ld_32x32b_x32(s_tm, sr[0]);
+              tmem_ld_32x32b_x32(s_tm + 32, sr[1]);
               tmem_wait_ld(sr[0]);
+              reg_tie(sr[1]);
 #pragma unroll
-              for (int c = 1; c < BN / 32; ++c) reg_tie(sr[c]);
-#pragma unroll
-              for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
+              for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
             }
-            const unsigned gone = bad[(tiles + j) & 15];
+            const unsigned gone = C::kPair ? bad[(tiles + (j >> 1)) & 15] >> (4 * buf) : bad[(tiles + j) & 15];
             if (tail || gone) {
 #pragma unroll
-              for (int w = 0; w < BN / 32; ++w) {
+              for (int w = 0; w < 2; ++w) {
                 if ((gone >> (2 * w)) & 1) see[w] &= 0xffff0000u;
                 if ((gone >> (2 * w)) & 2) see[w] &= 0x0000ffffu;
 #pragma unroll
@@ -428,22 +437,28 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             }
             float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
-            for (int c = 4; c < BN - 4; c += 8) {
+            for (int c = 4; c < 60; c += 8) {
               mx0 = fmax3(mx0, s[c], s[c + 1]);
               mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
               mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
               mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
             }
-            mx0 = fmax3(mx0, s[BN - 4], s[BN - 3]);
-            mx1 = fmax3(mx1, s[BN - 2], s[BN - 1]);
+            mx0 = fmax3(mx0, s[60], s[61]);
+            mx1 = fmax3(mx1, s[62], s[63]);
             const float m_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3)) * c2;
             if (j == 0) {
               m_ref = m_blk;
             } else if (__any_sync(0xffffffffu, row && (m_blk - m_ref) > kRescaleTau)) {
-              // O is read once the last tile's P V is done: S of the next tile follows it in the pipe, and
-              // where there is no next tile it has a barrier of its own.
-              if (j + 1 < nt) ok = mbar_wait_warp(s_bar(t, (tile_no + 1) & 1), ((tile_no + 1) >> 1) & 1, wctx, kPSiteOFull);
-              else ok = mbar_wait_warp(pv_bar(t), pv_no & 1, wctx, kPSiteOFull);
+              // O is read once the P V before is done.  A pair's S follows P V of the pair before it, and
+              // P V of its first half has a barrier; else S of the next tile follows P V of the last one,
+              // and where there is no next tile it has a barrier.
+              if (C::kPair) {
+                if (buf == 1) ok = mbar_wait_warp(pv_bar(t), par, wctx, kPSiteOFull);
+              } else if (j + 1 < nt) {
+                ok = mbar_wait_warp(s_bar(t, buf ^ 1), ((tile_no + 1) >> 1) & 1, wctx, kPSiteOFull);
+              } else {
+                ok = mbar_wait_warp(pv_bar(t), pv_no & 1, wctx, kPSiteOFull);
+              }
               if (!ok) break;
               tc_fence_after();
               const float m_new = fmaxf(m_ref, m_blk);
@@ -462,28 +477,25 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             }
             const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: all weights 0
             float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            uint32_t pk[32];
 #pragma unroll
-            for (int half = 0; half < BN / 64; ++half) {
-              uint32_t pk[32];
+            for (int c = 0; c < 64; c += 4) {
+              float x[4], e[4];
+              ffma2(x[0], x[1], s[c], s[c + 1], c2, c2, neg_m, neg_m);
+              ffma2(x[2], x[3], s[c + 2], s[c + 3], c2, c2, neg_m, neg_m);
 #pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                float x[4], e[4];
-                ffma2(x[0], x[1], s[64 * half + c], s[64 * half + c + 1], c2, c2, neg_m, neg_m);
-                ffma2(x[2], x[3], s[64 * half + c + 2], s[64 * half + c + 3], c2, c2, neg_m, neg_m);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) e[u] = ex2_mufu(x[u]);
-                fadd2(l0, l1, l0, l1, e[0], e[1]);
-                fadd2(l2, l3, l2, l3, e[2], e[3]);
-                pk[c >> 1] = pack_bf16x2(e[0], e[1]);
-                pk[(c >> 1) + 1] = pack_bf16x2(e[2], e[3]);
-              }
-              tmem_st_32x32b_x32(s_tm + 32 * half, pk);
+              for (int u = 0; u < 4; ++u) e[u] = ex2_mufu(x[u]);
+              fadd2(l0, l1, l0, l1, e[0], e[1]);
+              fadd2(l2, l3, l2, l3, e[2], e[3]);
+              pk[c >> 1] = pack_bf16x2(e[0], e[1]);
+              pk[(c >> 1) + 1] = pack_bf16x2(e[2], e[3]);
             }
+            tmem_st_32x32b_x32(s_tm, pk);
             l_sum += (l0 + l1) + (l2 + l3);
             tmem_wait_st();
             tc_fence_before();
           }
-          mbar_arrive_warp(p_bar(t, tile_no & 1));
+          mbar_arrive_warp(p_bar(t, buf));
         }
         // ----------------------------------------------------- epilogue
         if (ok) ok = mbar_wait_warp(o_bar(t), o_no & 1, wctx, kPSiteOFull);
@@ -534,113 +546,132 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
       }
       tiles += nt;
     }
-  } else if (warp < C::kLoadWarp) {
-    // ===================================================== MMA issue: a warp for each row tile (the elected lane issues)
-    const int t = warp - C::kMmaWarp;
+  } else if (warp == C::kMmaWarp) {
+    // ===================================================== MMA issue (whole warp; the elected lane issues)
+    // One warp for both row tiles: their S and P V alternate in the pipe, so that one tile's softmax runs
+    // under the other's products.  (A warp each: both wait for S at once and compute at once, 4100 instead
+    // of 3500 cycles for 128 places of 256 rows.)
     constexpr uint32_t idesc_s = make_idesc_bf16(128, BN, false, false);
     constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, false, true);
     auto slot_of = [&](int f) { return f % C::kStages; };
     auto par_of = [&](int f) { return (uint32_t)((f / C::kStages) & 1); };
-    const uint64_t q_desc = make_sdesc_sw128(sbase + C::kOffQ + t * C::kQBytes, 0, 1024);
+    const uint64_t q_desc = make_sdesc_sw128(sbase + C::kOffQ, 0, 1024);
     const uint64_t ring_desc_k = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
     const uint64_t ring_desc_v = make_sdesc_sw128(sbase + C::kOffRing, C::kBoxBytes, 1024);
-    const uint32_t s_col = tmem + (uint32_t)(2 * BN * t), o_col = tmem + C::kOCol + (uint32_t)(D * t);
-    auto issue_s = [&](int buf, int slot) {
+    auto issue_s = [&](int t, int buf, int slot) {
       const uint64_t kd = ring_desc_k + (uint64_t)((slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss(s_col + (uint32_t)(BN * buf), q_desc + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+        mma_ss(tmem + 128u * t + 64u * buf, q_desc + (uint32_t)((t * C::kQBytes + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
     };
-    auto issue_pv = [&](int buf, int slot, bool acc) {
-      const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes) >> 4);
+    // P V of the 64 places whose P is in buffer `buf`, rows 64 * half on of the tile
+    auto issue_pv = [&](int t, int buf, int half, int slot, bool acc) {
+      const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes + half * 64 * 128) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts(o_col, s_col + (uint32_t)(BN * buf) + 8u * kk, vd + (uint64_t)(kk * 128), idesc_pv, (acc || kk > 0));
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts(tmem + C::kOCol + (uint32_t)(D * t), tmem + 128u * t + 64u * buf + 8u * kk, vd + (uint64_t)(kk * 128),
+               idesc_pv, (acc || kk > 0));
     };
-    // S runs one tile ahead of the softmax: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
-    int fill = 0, seg = 0, s_no = 0, p_no = 0;  // ring slots, items; tiles of this row tile through S, through P V
-    uint32_t ready_par = 0;                     // by ring slot: parity of its next clearing
-    bool ok = true, any = false;
+    // Two row tiles: a tile's S fills both buffers at once (128 columns an instruction),
+    //   S_0 | PV_0a PV_0b S_1 | ... for each;
+    // one row tile: S runs one tile ahead of the softmax, S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
+    constexpr int kAhead = C::kPair ? 1 : 2;
+    int fill = 0, seg = 0;      // ring slots, items
+    int s_no[QT] = {}, p_no[QT] = {};  // tiles through S and through P V, by row tile
+    bool ok = true;
     while (ok && walk.next(p, begin)) {
       const int nt = walk.j1 - walk.j0;
+      bool act[QT];
+#pragma unroll
+      for (int t = 0; t < QT; ++t) act[t] = tile_tokens(t) > 0;
       ok = mbar_wait_warp(q_bar, seg & 1, wctx, kPSiteQ);
       if (!ok) break;
       ++seg;
-      if (QT > 1 && tile_tokens(t) == 0) {
-        // no rows: let go of Q and of every tile, keeping step with the ring
-        if (lane == 0) mbar_arrive(qfree_bar);
-        for (int f = fill; f < fill + 2 * nt && ok; ++f) {
-          ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
-          if (ok && lane == 0) mbar_arrive(empty_bar(slot_of(f)));
-        }
-        for (int j = 0; j < nt; ++j)
-          if ((walk.j0 + j) * BN + BN > walk.s.len) ready_par ^= 1u << slot_of(fill + v_fill(j, nt));
-        fill += 2 * nt;
-        continue;
-      }
-      any = true;
-      auto multiply_s = [&](int j) {  // S of tile j
-        const int f = fill + k_fill(j);
-        ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
-        if (!ok) return;
-        tc_fence_after();
+      auto multiply_s = [&](int t, int slot) {
+        const int buf = C::kPair ? 0 : s_no[t] & 1;
         if (elect_one()) {
-          issue_s(s_no & 1, slot_of(f));
-          tc_commit(s_bar(t, s_no & 1));
-          tc_commit(empty_bar(slot_of(f)));
+          issue_s(t, buf, slot);
+          tc_commit(s_bar(t, buf));
+        }
+        __syncwarp();
+        ++s_no[t];
+      };
+      auto wait_k = [&](int j) {
+        const int f = fill + k_fill<C::kPair>(j);
+        ok = mbar_wait_warp(full_bar(slot_of(f)), par_of(f), wctx, kPSiteKFull);
+        tc_fence_after();
+        return slot_of(f);
+      };
+      for (int j = 0; j < kAhead && j < nt && ok; ++j) {
+        const int sk = wait_k(j);
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          if (act[t]) multiply_s(t, sk);
+        if (elect_one()) {
+          tc_commit(empty_bar(sk));
           if (j == nt - 1) tc_commit(qfree_bar);
         }
         __syncwarp();
-        ++s_no;
-      };
-      multiply_s(0);
-      if (ok && nt > 1) multiply_s(1);
+      }
       for (int j = 0; j < nt && ok; ++j) {
-        const int fv = fill + v_fill(j, nt), sv = slot_of(fv);
+        const int fv = fill + v_fill<C::kPair>(j, nt), sv = slot_of(fv);
+        ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
+        if (!ok) break;
         const int kv0 = (walk.j0 + j) * BN;
         bool cleared = false;
-        if (kv0 + BN <= walk.s.len) {
-          ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
-        } else if (t == 0) {  // clear what must not be multiplied, for all row tiles
-          ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
-          if (ok) {
-            cleared = clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, kv0, p.g.page_size);
-            if (QT > 1) {
-              if (lane == 0) *hit = cleared ? *hit | (1u << sv) : *hit & ~(1u << sv);
-              mbar_arrive_warp(ready_bar(sv));
-            }
+        if (kv0 + BN > walk.s.len)
+          cleared = clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, kv0, p.g.page_size);
+        int sk = -1;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          if (!act[t] || !ok) continue;
+          const int buf = C::kPair ? 0 : p_no[t] & 1, par = C::kPair ? p_no[t] & 1 : (p_no[t] >> 1) & 1;
+          ok = mbar_wait_warp(p_bar(t, buf), par, wctx, kPSitePFull);
+          if (!ok) break;
+          tc_fence_after();
+          // this row tile's warps have left the epilogue of every earlier item
+          if (cleared && lane == 0) odd[t] = seg;
+          __syncwarp();
+          if (elect_one()) {
+            issue_pv(t, buf, 0, sv, j > 0);
+            if (C::kPair || j == nt - 2) tc_commit(pv_bar(t));
           }
-        } else {
-          ok = mbar_wait_warp(ready_bar(sv), (ready_par >> sv) & 1, wctx, kPSiteVTail);
-          ready_par ^= 1u << sv;
-          cleared = (*hit >> sv) & 1;
+          __syncwarp();
+          if (C::kPair) {
+            ok = mbar_wait_warp(p_bar(t, 1), par, wctx, kPSitePFull);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) issue_pv(t, 1, 1, sv, true);
+            __syncwarp();
+          }
+          ++p_no[t];
+          if (j == nt - 1) {
+            if (elect_one()) tc_commit(o_bar(t));
+            __syncwarp();
+          } else if (j + kAhead < nt) {  // into the columns that P just left (the tensor pipe runs in order)
+            if (sk < 0) sk = wait_k(j + kAhead);
+            if (!ok) break;
+            multiply_s(t, sk);
+          }
         }
-        if (ok) ok = mbar_wait_warp(p_bar(t, p_no & 1), (p_no >> 1) & 1, wctx, kPSitePFull);
-        if (!ok) break;
-        tc_fence_after();
-        // this row tile's warps have left the epilogue of every earlier item
-        if (cleared && lane == 0) odd[t] = seg;
-        __syncwarp();
         if (elect_one()) {
-          issue_pv(p_no & 1, sv, j > 0);
-          if (j == nt - 1) tc_commit(o_bar(t));
-          if (j == nt - 2) tc_commit(pv_bar(t));
           tc_commit(empty_bar(sv));
+          if (sk >= 0) tc_commit(empty_bar(sk));
+          if (sk >= 0 && j + kAhead == nt - 1) tc_commit(qfree_bar);
         }
         __syncwarp();
-        ++p_no;
-        if (j + 2 < nt) multiply_s(j + 2);  // into the buffer that P just left (the tensor pipe runs in order)
       }
       fill += 2 * nt;
     }
     // Drain: every MMA this warp issued completes before TMEM is released.
-    if (any) {
-      if (elect_one()) tc_commit(drain_bar(t));
+    if (seg > 0) {
+      if (elect_one()) tc_commit(drain_bar);
       __syncwarp();
-      if (!mbar_wait_warp(drain_bar(t), 0, wctx, kPSiteDrain) && *abort_flag) {
+      if (!mbar_wait_warp(drain_bar, 0, wctx, kPSiteDrain) && *abort_flag) {
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_test(drain_bar(t), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+        while (!mbar_test(drain_bar, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
       }
     }
   } else {
@@ -660,7 +691,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         const int page = row[pos >> shift];
         return page >= 0 && page < p.g.num_pages ? page : -1;
       };
-      // in the order the MMA warp takes them: K_0 K_1 V_0 K_2 V_1 ... V_last
+      // in the order of k_fill and v_fill
       auto load = [&](const CUtensorMap *map, int j, int page) {
         const int s = fill % C::kStages;
         ok = mbar_wait_warp(empty_bar(s), ((fill / C::kStages) & 1) ^ 1, wctx, kPSiteEmpty);
@@ -677,7 +708,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         ++fill;
       };
       int page = page_at(walk.j0), page_v = -2;
-      for (int j = 0; j <= nt && ok; ++j) {
+      for (int j = 0; j < nt + !C::kPair && ok; ++j) {
         const int page_next = j + 1 < nt ? page_at(walk.j0 + j + 1) : -2;
         if (j < nt) {
           unsigned gone = page == -1 ? ((1u << (box_rows / 16)) - 1u) << (lane * (box_rows / 16)) : 0u;
@@ -703,9 +734,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
           }
           ++seg;
           __syncwarp();
-        } else {
-          load(&p.tm_v, j - 1, page_v);
         }
+        if (C::kPair) load(&p.tm_v, j, page);
+        else if (j > 0) load(&p.tm_v, j - 1, page_v);
         page_v = page;
         page = page_next;
       }
@@ -1082,7 +1113,7 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
               for (int n = 0; n < D / 8; ++n) to[4 * n] = pack_bf16x2(o[m][n][2 * hf] * inv, o[m][n][2 * hf + 1] * inv);
               if ((lane & 3) == 0 && p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[m][hf] + __log2f(l)) * 0.69314718055994531f;
             } else {
-              const int all = p.HB * p.TB * p.G, row = hb * p.TB * p.G + r;
+              const int GG = p.HB * p.G, all = p.TB * GG, row = tok[m][hf] * GG + hb * p.G + (r - tok[m][hf] * p.G);
               const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * all;
               float *to = p.part_o + slot * D + c4 * all + row;
 #pragma unroll
@@ -1153,21 +1184,15 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
   __shared__ float s_part[kJoinWarps][10][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % p.join;
-  const long long id = ((long long)blockIdx.x * (kJoinWarps / p.join) + warp / p.join) * 32 + lane;
-  int tok, h, cg;
-  if (p.HB > 1) {  // neighbours: the heads of a token
-    const long long r = quot(id, p.H);
-    h = (int)(id - r * p.H);
-    tok = (int)(r / (D / 8));
-    cg = (int)(r % (D / 8));
-  } else {  // the rows of a kv head
-    const long long r = quot(id, (long long)p.total * p.G), tg = id - r * p.total * p.G;
-    tok = (int)quot(tg, p.G);
-    cg = (int)(r % (D / 8));
-    h = (int)(r / (D / 8)) * p.G + (int)(tg - (long long)tok * p.G);
-  }
-  bool mine = tok < p.total && h < p.H;
-  if (!mine) tok = h = 0;
+  const long long id = ((long long)blockIdx.x * (blockDim.x / 32 / p.join) + warp / p.join) * 32 + lane;
+  // neighbours: the rows of an item (token by token, its heads together)
+  const int GG = p.HB * p.G;
+  const long long r = quot(id, (long long)p.total * GG), tg = id - r * p.total * GG;
+  int tok = (int)quot(tg, GG);
+  const int cg = (int)(r % (D / 8)), group = (int)(r / (D / 8)), hg = (int)(tg - (long long)tok * GG);
+  bool mine = group < p.heads;
+  const int h = mine ? group * GG + hg : 0;
+  if (!mine) tok = 0;
   int b = 0;
   for (int hi = p.g.B; hi - b > 1;) {
     const int mid = (b + hi) >> 1;
@@ -1179,10 +1204,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
   mine = mine && i >= 0 && i < s.n;
   int tiles, groups;
   paged_units(p, s, tiles, groups);
-  const int kh = h / p.G, rt = i / p.TB, rg = rt / p.QT;
-  const int rows = p.TB * p.G;
-  const int row = ((kh % p.HB) * p.QT + rt - rg * p.QT) * rows + (i - rt * p.TB) * p.G + (h - kh * p.G);
-  const int item = kh / p.HB * groups + rg, all = p.HB * p.QT * rows;
+  const int rt = i / p.TB, rg = rt / p.QT, rows = p.TB * GG;
+  const int row = (rt - rg * p.QT) * rows + (i - rt * p.TB) * GG + hg;
+  const int item = group * groups + rg, all = p.QT * rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int parts = 0, c0 = 0;
   long long first = 0;
@@ -1270,7 +1294,8 @@ int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new,
 // the result does not depend on it.)
 constexpr int kSMs = 152;
 
-constexpr int kTileKeys = 64;  // places in a tile of the tcgen05 kernel
+// Places in a tile of the tcgen05 kernel: a pair of halves where a block has two row tiles.
+constexpr int tile_keys(int QT) { return QT == 2 ? 128 : 64; }
 
 struct PagedPlan {
   int MT;  // 16-row fragments of the few-rows kernel, 0: the tcgen05 kernel
@@ -1281,11 +1306,11 @@ struct PagedPlan {
 PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
   PagedPlan w;
   const int rows = max_new * G;
-  w.MT = rows <= 16 ? 1 : rows <= 32 && d <= 128 ? 2 : 0;
+  w.MT = rows <= 16 ? 1 : 0;
   w.TB = 128 / G < max_new ? 128 / G : max_new;
   w.QT = max_new > w.TB && d <= 128 ? 2 : 1;
   w.HB = !w.MT ? 1 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-  w.bn = w.MT ? 64 / w.HB : kTileKeys;
+  w.bn = w.MT ? 64 / w.HB : tile_keys(w.QT);
   w.blocks = kSMs * (w.MT ? (d * w.MT <= 128 ? 2 : 1) : (w.QT == 1 && d <= 128 ? 2 : 1));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)2 * w.blocks * w.HB * w.QT * w.TB * G;
@@ -1305,9 +1330,10 @@ int launch_two(const PagedParams &p, int d, int blocks, int threads, int smem, v
   main<<<(unsigned)blocks, threads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  const long long tasks = 32 * (kJoinWarps / p.join);
+  const int warps = p.join > 4 ? p.join : 4;
+  const long long tasks = 32 * (warps / p.join);
   cfg.gridDim = dim3((unsigned)(((long long)p.total * p.H * (d / 8) + tasks - 1) / tasks));
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.blockDim = dim3(32 * warps);
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1414,16 +1440,13 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
     if (d == 128) return launch_few<128, 1>(p, w.blocks, k_pages, v_pages, s);
     return launch_few<256, 1>(p, w.blocks, k_pages, v_pages, s);
   }
-  if (w.MT == 2)
-    return d == 64 ? launch_few<64, 2>(p, w.blocks, k_pages, v_pages, s)
-                   : launch_few<128, 2>(p, w.blocks, k_pages, v_pages, s);
   if (d == 64)
-    return w.QT == 2 ? launch_paged<64, kTileKeys, 2>(p, w.blocks, q, k_pages, v_pages, s)
-                     : launch_paged<64, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<64, tile_keys(2), 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<64, tile_keys(1), 1>(p, w.blocks, q, k_pages, v_pages, s);
   if (d == 128)
-    return w.QT == 2 ? launch_paged<128, kTileKeys, 2>(p, w.blocks, q, k_pages, v_pages, s)
-                     : launch_paged<128, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
-  return launch_paged<256, kTileKeys, 1>(p, w.blocks, q, k_pages, v_pages, s);
+    return w.QT == 2 ? launch_paged<128, tile_keys(2), 2>(p, w.blocks, q, k_pages, v_pages, s)
+                     : launch_paged<128, tile_keys(1), 1>(p, w.blocks, q, k_pages, v_pages, s);
+  return launch_paged<256, tile_keys(1), 1>(p, w.blocks, q, k_pages, v_pages, s);
 }
 
 }  // extern "C"
