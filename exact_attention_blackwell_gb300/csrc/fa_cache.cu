@@ -22,6 +22,8 @@ __global__ void __launch_bounds__(128)
     cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, uint4 *__restrict__ k_pages,
                         uint4 *__restrict__ v_pages, const __grid_constant__ PageGeom g, const int *__restrict__ cu,
                         int total, int chunks) {
+  grid_go();
+  grid_wait();
   const int lane = threadIdx.x & 31;
   const int t = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
   if (t >= total) return;
@@ -54,6 +56,8 @@ __global__ void __launch_bounds__(128)
                          int chunks) {
   __shared__ long long s_src[kPathChunk], s_dst[kPathChunk];
   __shared__ int s_bad;
+  grid_go();
+  grid_wait();
   const int per_seq = 2 * layers;
   const int b = blockIdx.x / per_seq, part = blockIdx.x % per_seq;
   const int layer = part >> 1;
@@ -106,6 +110,8 @@ __global__ void __launch_bounds__(1024)
                       const int *__restrict__ parents, int *__restrict__ lens_out, int B, int max_pages, int num_pages,
                       int page_size, int cols) {
   extern __shared__ int fresh[];  // [B, cols]
+  grid_go();
+  grid_wait();
   const int c0 = blockIdx.x * cols;
   for (int e = threadIdx.x; e < B * cols; e += blockDim.x) {
     const int b = e / cols, c = c0 + e % cols;
@@ -172,6 +178,8 @@ __global__ void __launch_bounds__(kBookThreads)
   const long long cap = (long long)max_pages * page_size;
   if (tid == 0) s_refused = s_copies = 0;
   __syncthreads();
+  grid_go();
+  grid_wait();
   auto held = [&](int len) { return (int)(((long long)len + page_size - 1) / page_size); };
   auto valid = [&](int a, int n) { return a >= 0 && n >= 0 && a <= cap && n <= cap; };
 
@@ -297,6 +305,8 @@ constexpr int kCopyChunk = 1024;
 __global__ void __launch_bounds__(256)
     cache_copy_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages, const int *__restrict__ copies,
                       int num_pages, int page_size, int layers, int chunks) {
+  grid_go();
+  grid_wait();
   const int page_chunks = page_size * chunks;
   const int pieces = (page_chunks + kCopyChunk - 1) / kCopyChunk;
   const long long work = (long long)copies[0] * layers * 2 * pieces;
@@ -312,8 +322,6 @@ __global__ void __launch_bounds__(256)
     for (int i = piece * kCopyChunk + threadIdx.x; i < end; i += blockDim.x) dst[i] = src[i];
   }
 }
-
-int launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 constexpr int kMaxBookRows = 4096;  // rows whose books fit the shared memory of one block
 
@@ -361,10 +369,9 @@ int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, 
   if (total == 0) return FA_OK;
   const PageGeom g{page_table, cache_lens, B, max_pages, num_pages, page_size};
   const unsigned grid = (unsigned)(((long long)total + 3) / 4);
-  cache_append_kernel<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), static_cast<uint4 *>(k_pages),
-      static_cast<uint4 *>(v_pages), g, cu_seqlens, total, Hkv * d / 8);
-  return launched();
+  return launch_after(cache_append_kernel, grid, 128, 0, static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k),
+                      static_cast<const uint4 *>(v), static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g,
+                      cu_seqlens, total, Hkv * d / 8);
 }
 
 int fa_cache_compact(void *k_pages, void *v_pages, const int *page_table, const int *cache_lens, const int *accepted,
@@ -383,10 +390,9 @@ int fa_cache_compact(void *k_pages, void *v_pages, const int *page_table, const 
     if (!ptr_aligned(x, 4)) return FA_ERR_ALIGNMENT;
   if ((rc = check_device()) != FA_OK) return rc;
   const PageGeom g{page_table, cache_lens, B, max_pages, num_pages, page_size};
-  cache_compact_kernel<<<(unsigned)(B * layers * 2), 128, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g, accepted, n_accepted, lens_out, max_accepted,
-      layers, Hkv * d / 8);
-  return launched();
+  return launch_after(cache_compact_kernel, (long long)B * layers * 2, 128, 0, static_cast<cudaStream_t>(stream),
+                      static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g, accepted, n_accepted, lens_out,
+                      max_accepted, layers, Hkv * d / 8);
 }
 
 int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const int *parents, int *lens_out, int B,
@@ -408,9 +414,8 @@ int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const 
     return FA_ERR_CUDA;
   const unsigned grid = (unsigned)((max_pages + cols - 1) / cols);
   const int threads = B * cols >= 1024 ? 1024 : (B * cols + 31) / 32 * 32;
-  cache_fork_kernel<<<grid, threads, smem, static_cast<cudaStream_t>(stream)>>>(
-      page_refs, page_table, cache_lens, parents, lens_out, B, max_pages, num_pages, page_size, cols);
-  return launched();
+  return launch_after(cache_fork_kernel, grid, threads, smem, static_cast<cudaStream_t>(stream), page_refs, page_table,
+                      cache_lens, parents, lens_out, B, max_pages, num_pages, page_size, cols);
 }
 
 size_t fa_cache_resize_workspace_bytes(int B) { return B > 0 && B <= kMaxBookRows ? resize_bytes(B) : 0; }
@@ -434,12 +439,11 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if ((rc = check_device()) != FA_OK) return rc;
   int *copies = static_cast<int *>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cache_resize_kernel<<<1, kBookThreads, (size_t)B * 8, s>>>(page_refs, page_table, cache_lens, new_lens, lens_out,
-                                                             status, copies, B, max_pages, num_pages, page_size);
-  if ((rc = launched()) != FA_OK) return rc;
-  cache_copy_kernel<<<152 * 4, 256, 0, s>>>(static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), copies,
-                                            num_pages, page_size, layers, Hkv * d / 8);
-  return launched();
+  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 8, s, page_refs, page_table, cache_lens,
+                         new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size)) != FA_OK)
+    return rc;
+  return launch_after(cache_copy_kernel, 152 * 4, 256, 0, s, static_cast<uint4 *>(k_pages),
+                      static_cast<uint4 *>(v_pages), (const int *)copies, num_pages, page_size, layers, Hkv * d / 8);
 }
 
 }  // extern "C"

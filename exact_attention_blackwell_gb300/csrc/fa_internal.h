@@ -140,6 +140,30 @@ struct Fp8Params {
   int sched_chunk;
 };
 
+#ifdef __CUDACC__
+// The kernels of a decoding step follow one another and are short, so each may be
+// launched while the one before it drains: it sets itself up, and before its first
+// access to global memory waits until everything launched before has completed
+// (launch_after; grid_wait).  grid_go lets the next such kernel begin early.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), long long blocks, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+#endif
+
 // A paged key/value cache (fa_cache.cu, fa_paged.cu): pages [num_pages,
 // page_size, Hkv, d] bf16, place p of sequence b in row p % page_size of page
 // page_table[b][p / page_size].
@@ -195,7 +219,10 @@ unsigned *device_status_ptr();
 
 // Encodes a 4-D tensor map over a bf16 [B, N, Hx, d] tensor, box = 64 columns x
 // `box_rows` rows of one head, 128-byte swizzle.  Returns 0 on success.
-int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int Hx, int d, int box_rows);
+// `narrow`: fetch 128 instead of 256 bytes into L2 around each box row (for boxes
+// whose 128-byte rows are all that is read of a tensor row).
+int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int Hx, int d, int box_rows,
+                         bool narrow = false);
 
 // Encodes a 4-D bf16 tensor map, box[0] = 64 columns, 128-byte swizzle; strides in bytes for dims 1..3.
 int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
