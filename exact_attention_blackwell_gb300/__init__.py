@@ -473,30 +473,53 @@ def _check_table(page_table, cache_lens):
             _check("cache_lens", cache_lens, torch.int32, (B,))], B, max_pages
 
 
-# A decoding step makes these calls for every layer, so their checks are written for the case that
-# passes: one expression over the operands, and only where it fails the checks that say what is wrong.
-_torch = None
+# A decoding step makes these calls for every layer.  Their ordinary case (operands as documented, on
+# the current device and stream, outputs allocated by the call) is checked and made by a CPython module,
+# csrc/paged_binding.cpp; where that returns None, the code below says what is wrong or does the rest.
+_fast = None
 
 
-def _load_torch():
-    global _torch
+def _paged_binding():
+    global _fast
+    if _fast is None:
+        import importlib.util
+
+        import torch
+
+        from . import build
+
+        path = build.binding_path(torch)
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with exact_attention_blackwell_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_paged_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.connect(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
+            "fa_cache_append", "fa_fwd_paged_workspace_bytes", "fa_fwd_paged", "fa_cache_compact", "fa_cache_fork",
+            "fa_cache_resize_workspace_bytes", "fa_cache_resize")))
+        _fast = module
+    return _fast
+
+
+def _done(result, what):
+    """The result of a call, or FaError where it is a status."""
+    if type(result) is int and result != FA_OK:
+        raise FaError(result, what)
+    return result
+
+
+def _workspace(given, nbytes, dev):
     import torch
 
-    lib()
-    _torch = torch
-    return torch
+    if given is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev), nbytes
+    return given, given.numel() * given.element_size()
 
 
-def _check_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens):
-    import torch
-
-    pages, _, _, _, Hkv, d = _check_pages(k_pages, v_pages, False)
-    table, B, _ = _check_table(page_table, cache_lens)
-    if k.dim() != 3:
-        raise ValueError("k and v must be [total, Hkv, d]")
-    total = k.shape[0]
-    _same_device(_check("k", k, torch.bfloat16, (total, Hkv, d)), _check("v", v, torch.bfloat16, (total, Hkv, d)),
-                 *pages, *table, _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
+def _check_workspace(workspace):
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return "workspace", workspace
 
 
 def cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, stream=None):
@@ -504,56 +527,23 @@ def cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, str
     sequence b (rows cu_seqlens[b]..cu_seqlens[b+1]) to place cache_lens[b] + i of the cache, i.e. row
     place % page_size of page page_table[b, place // page_size].  page_table int32 [B,max_pages],
     cache_lens int32 [B], cu_seqlens int32 [B+1]."""
-    torch = _torch or _load_torch()
-    bf16, i32 = torch.bfloat16, torch.int32
-    shape, rows, table = k_pages.shape, k.shape, page_table.shape
-    dev = k.get_device()
-    if not (len(shape) == 4 and len(rows) == 3 and len(table) == 2 and dev >= 0
-            and k.dtype is bf16 and v.dtype is bf16 and k_pages.dtype is bf16 and v_pages.dtype is bf16
-            and page_table.dtype is i32 and cache_lens.dtype is i32 and cu_seqlens.dtype is i32
-            and rows[1:] == shape[2:] and v.shape == rows and v_pages.shape == shape
-            and cache_lens.shape == table[:1] and cu_seqlens.shape == (table[0] + 1,)
-            and k.is_contiguous() and v.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and page_table.is_contiguous() and cache_lens.is_contiguous() and cu_seqlens.is_contiguous()
-            and dev == v.get_device() == k_pages.get_device() == v_pages.get_device() == page_table.get_device()
-            == cache_lens.get_device() == cu_seqlens.get_device()):
-        _check_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens)
-    if stream is not None or dev != torch._C._cuda_getDevice():
-        with _On(k.device, stream):
-            return cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens)
-    num_pages, page_size, Hkv, d = shape
-    total = rows[0]
-    if total == 0:
-        return
-    st = _lib.fa_cache_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                              page_table.data_ptr(), cache_lens.data_ptr(), cu_seqlens.data_ptr(), table[0], table[1],
-                              num_pages, page_size, total, Hkv, d, torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_append")
-
-
-def _check_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask, out, lse, workspace):
+    if stream is None:
+        st = (_fast or _paged_binding()).append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens)
+        if st is not None:
+            _done(st, "fa_cache_append")
+            return
     import torch
 
-    pages, *_ = _check_pages(k_pages, v_pages, False)
-    table, B, _ = _check_table(page_table, cache_lens)
-    if q.dim() != 3:
-        raise ValueError("q must be [total, H, d]")
-    total, H, _ = q.shape
-    d = k_pages.shape[3]
-    c = [_check("q", q, torch.bfloat16, (total, H, d)), *pages, *table,
-         _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))]
-    if tree_mask is not None:
-        c.append(_check("tree_mask", tree_mask, torch.int64, (total, (max_new + 63) // 64)))
-    if out is not None:
-        c.append(_check("out", out, torch.bfloat16, (total, H, d)))
-    if lse is not None:
-        c.append(_check("lse", lse, torch.float32, (H, total)))
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        c.append(("workspace", workspace))
-    _same_device(*c)
+    pages, _, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, False)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total = k.shape[0]
+    dev = _same_device(_check("k", k, torch.bfloat16, (total, Hkv, d)), _check("v", v, torch.bfloat16, (total, Hkv, d)),
+                       *pages, *table, _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
+    with _On(dev, stream):
+        _done(fa_cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, B, max_pages, num_pages,
+                              page_size, total, Hkv, d), "fa_cache_append")
 
 
 def attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask=None, scale=None,
@@ -564,62 +554,40 @@ def attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens,
     places before the new ones and, of the new ones, those up to itself, or with tree_mask (int64
     [total, ceil(max_new / 64)]) those whose bits are set in its words.  A token that sees nothing gets
     o = 0 and lse = -inf."""
-    torch = _torch or _load_torch()
-    bf16, i32 = torch.bfloat16, torch.int32
-    shape, rows, table = k_pages.shape, q.shape, page_table.shape
-    max_new = int(max_new)
-    words = (max_new + 63) // 64
-    dev = q.get_device()
-    if not (len(shape) == 4 and len(rows) == 3 and len(table) == 2 and dev >= 0
-            and q.dtype is bf16 and k_pages.dtype is bf16 and v_pages.dtype is bf16
-            and page_table.dtype is i32 and cache_lens.dtype is i32 and cu_seqlens.dtype is i32
-            and rows[2] == shape[3] and v_pages.shape == shape
-            and cache_lens.shape == table[:1] and cu_seqlens.shape == (table[0] + 1,)
-            and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and page_table.is_contiguous() and cache_lens.is_contiguous() and cu_seqlens.is_contiguous()
-            and dev == k_pages.get_device() == v_pages.get_device() == page_table.get_device()
-            == cache_lens.get_device() == cu_seqlens.get_device()
-            and (tree_mask is None or (tree_mask.dtype is torch.int64 and tree_mask.shape == (rows[0], words)
-                                       and tree_mask.is_contiguous() and tree_mask.get_device() == dev))
-            and out is None and lse is None and workspace is None):
-        _check_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask, out, lse, workspace)
-    if stream is not None or dev != torch._C._cuda_getDevice():
-        with _On(q.device, stream):
-            return attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask,
-                                       scale, out, lse, workspace)
-    num_pages, page_size, Hkv, d = shape
-    total, H, _ = rows
-    B = table[0]
-    o = torch.empty_like(q) if out is None else out
-    if lse is None:
-        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-    if total == 0:
-        return o, lse
-    if workspace is None:
-        nbytes = _lib.fa_fwd_paged_workspace_bytes(B, max_new, H, Hkv, d) or 1
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    st = _lib.fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                           cache_lens.data_ptr(), cu_seqlens.data_ptr(),
-                           None if tree_mask is None else tree_mask.data_ptr(), words, o.data_ptr(), lse.data_ptr(), B,
-                           table[1], num_pages, page_size, max_new, total, H, Hkv, d,
-                           1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(), nbytes,
-                           torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_paged")
-    return o, lse
-
-
-def _check_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted):
+    if stream is None and out is None and lse is None and workspace is None:
+        both = (_fast or _paged_binding()).attention(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new,
+                                                     tree_mask, scale)
+        if both is not None:
+            return _done(both, "fa_fwd_paged")
     import torch
 
-    pages, *_ = _check_pages(k_pages, v_pages, True)
-    table, B, _ = _check_table(page_table, cache_lens)
-    if accepted.dim() != 2:
-        raise ValueError("accepted must be [B, max_accepted]")
-    _same_device(*pages, *table, _check("accepted", accepted, torch.int32, (B, accepted.shape[1])),
-                 _check("n_accepted", n_accepted, torch.int32, (B,)))
+    pages, _, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, False)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, H, d]")
+    total, H, _ = q.shape
+    max_new = int(max_new)
+    words = (max_new + 63) // 64 if tree_mask is not None else 0
+    c = [_check("q", q, torch.bfloat16, (total, H, d)), *pages, *table,
+         _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))]
+    if tree_mask is not None:
+        c.append(_check("tree_mask", tree_mask, torch.int64, (total, words)))
+    if out is not None:
+        c.append(_check("out", out, torch.bfloat16, (total, H, d)))
+    if lse is not None:
+        c.append(_check("lse", lse, torch.float32, (H, total)))
+    if workspace is not None:
+        c.append(_check_workspace(workspace))
+    dev = _same_device(*c)
+    with _On(dev, stream):
+        o = torch.empty_like(q) if out is None else out
+        lse = torch.empty((H, total), dtype=torch.float32, device=dev) if lse is None else lse
+        if total > 0:
+            workspace, nbytes = _workspace(workspace, fa_fwd_paged_workspace_bytes(B, max_new, H, Hkv, d), dev)
+            _done(fa_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, tree_mask, words, o, lse, B,
+                               max_pages, num_pages, page_size, max_new, total, H, Hkv, d,
+                               1.0 / math.sqrt(d) if scale is None else scale, workspace, nbytes), "fa_fwd_paged")
+    return o, lse
 
 
 def cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, stream=None):
@@ -628,83 +596,47 @@ def cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted
     accepted[b, i] go to place cache_lens[b] + i for i < n_accepted[b] -> new lengths int32 [B].
     accepted int32 [B,max_accepted] ascends along each path; a path ends before the first entry that
     does not."""
-    torch = _torch or _load_torch()
-    bf16, i32 = torch.bfloat16, torch.int32
-    shape, paths, table = k_pages.shape, accepted.shape, page_table.shape
-    dev = k_pages.get_device()
-    if not (4 <= len(shape) <= 5 and len(paths) == 2 and len(table) == 2 and dev >= 0
-            and k_pages.dtype is bf16 and v_pages.dtype is bf16 and page_table.dtype is i32
-            and cache_lens.dtype is i32 and accepted.dtype is i32 and n_accepted.dtype is i32
-            and v_pages.shape == shape and paths[0] == table[0]
-            and cache_lens.shape == table[:1] and n_accepted.shape == table[:1]
-            and k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous()
-            and cache_lens.is_contiguous() and accepted.is_contiguous() and n_accepted.is_contiguous()
-            and dev == v_pages.get_device() == page_table.get_device() == cache_lens.get_device()
-            == accepted.get_device() == n_accepted.get_device()):
-        _check_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted)
-    if stream is not None or dev != torch._C._cuda_getDevice():
-        with _On(k_pages.device, stream):
-            return cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted)
-    num_pages, page_size, Hkv, d = shape[-4:]
-    lens = torch.empty_like(cache_lens)
-    st = _lib.fa_cache_compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), cache_lens.data_ptr(),
-                               accepted.data_ptr(), n_accepted.data_ptr(), lens.data_ptr(), table[0], paths[1],
-                               table[1], num_pages, page_size, shape[0] if len(shape) == 5 else 1, Hkv, d,
-                               torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_compact")
-    return lens
-
-
-def _check_fork(page_refs, page_table, cache_lens, parents):
+    if stream is None:
+        lens = (_fast or _paged_binding()).compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted)
+        if lens is not None:
+            return _done(lens, "fa_cache_compact")
     import torch
 
-    table, B, _ = _check_table(page_table, cache_lens)
-    if page_refs.dim() != 1:
-        raise ValueError("page_refs must be [num_pages]")
-    _same_device(_check("page_refs", page_refs, torch.int32, page_refs.shape), *table,
-                 _check("parents", parents, torch.int32, (B,)))
+    pages, layers, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, True)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be [B, max_accepted]")
+    most = accepted.shape[1]
+    dev = _same_device(*pages, *table, _check("accepted", accepted, torch.int32, (B, most)),
+                       _check("n_accepted", n_accepted, torch.int32, (B,)))
+    with _On(dev, stream):
+        lens = torch.empty_like(cache_lens)
+        _done(fa_cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, lens, B, most, max_pages,
+                               num_pages, page_size, layers, Hkv, d), "fa_cache_compact")
+    return lens
 
 
 def cache_fork(page_refs, page_table, cache_lens, parents, page_size, stream=None):
     """Row b of page_table becomes what row parents[b] was before the call, sharing its pages (-1 empties
     the row; b leaves it alone) -> new lengths int32 [B].  page_refs int32 [num_pages] counts the rows
     that hold each page and is kept in step; no key or value moves."""
-    torch = _torch or _load_torch()
-    i32 = torch.int32
-    refs, table = page_refs.shape, page_table.shape
-    dev = page_refs.get_device()
-    if not (len(refs) == 1 and len(table) == 2 and dev >= 0 and page_refs.dtype is i32 and page_table.dtype is i32
-            and cache_lens.dtype is i32 and parents.dtype is i32
-            and cache_lens.shape == table[:1] and parents.shape == table[:1]
-            and page_refs.is_contiguous() and page_table.is_contiguous() and cache_lens.is_contiguous()
-            and parents.is_contiguous()
-            and dev == page_table.get_device() == cache_lens.get_device() == parents.get_device()):
-        _check_fork(page_refs, page_table, cache_lens, parents)
-    if stream is not None or dev != torch._C._cuda_getDevice():
-        with _On(page_refs.device, stream):
-            return cache_fork(page_refs, page_table, cache_lens, parents, page_size)
-    lens = torch.empty_like(cache_lens)
-    st = _lib.fa_cache_fork(page_refs.data_ptr(), page_table.data_ptr(), cache_lens.data_ptr(), parents.data_ptr(),
-                            lens.data_ptr(), table[0], table[1], refs[0], int(page_size),
-                            torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_fork")
-    return lens
-
-
-def _check_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace):
+    if stream is None:
+        lens = (_fast or _paged_binding()).fork(page_refs, page_table, cache_lens, parents, page_size)
+        if lens is not None:
+            return _done(lens, "fa_cache_fork")
     import torch
 
-    pages, _, num_pages, *_ = _check_pages(k_pages, v_pages, True)
-    table, B, _ = _check_table(page_table, cache_lens)
-    c = [_check("page_refs", page_refs, torch.int32, (num_pages,)), *pages, *table,
-         _check("new_lens", new_lens, torch.int32, (B,))]
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        c.append(("workspace", workspace))
-    _same_device(*c)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if page_refs.dim() != 1:
+        raise ValueError("page_refs must be [num_pages]")
+    num_pages = page_refs.shape[0]
+    dev = _same_device(_check("page_refs", page_refs, torch.int32, (num_pages,)), *table,
+                       _check("parents", parents, torch.int32, (B,)))
+    with _On(dev, stream):
+        lens = torch.empty_like(cache_lens)
+        _done(fa_cache_fork(page_refs, page_table, cache_lens, parents, lens, B, max_pages, num_pages, int(page_size)),
+              "fa_cache_fork")
+    return lens
 
 
 def cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace=None, stream=None):
@@ -713,36 +645,23 @@ def cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, 
     page is first copied into one of its own, in every layer -> (lengths int32 [B], status int32 [2]).
     status[0] is the number of pages that were missing (then no row has grown), status[1] the number of
     rows left alone because a length was negative or past the table."""
-    torch = _torch or _load_torch()
-    bf16, i32 = torch.bfloat16, torch.int32
-    shape, table = k_pages.shape, page_table.shape
-    dev = k_pages.get_device()
-    if not (4 <= len(shape) <= 5 and len(table) == 2 and dev >= 0
-            and k_pages.dtype is bf16 and v_pages.dtype is bf16 and page_refs.dtype is i32
-            and page_table.dtype is i32 and cache_lens.dtype is i32 and new_lens.dtype is i32
-            and v_pages.shape == shape and page_refs.shape == shape[-4:-3]
-            and cache_lens.shape == table[:1] and new_lens.shape == table[:1]
-            and k_pages.is_contiguous() and v_pages.is_contiguous() and page_refs.is_contiguous()
-            and page_table.is_contiguous() and cache_lens.is_contiguous() and new_lens.is_contiguous()
-            and dev == v_pages.get_device() == page_refs.get_device() == page_table.get_device()
-            == cache_lens.get_device() == new_lens.get_device()
-            and workspace is None):
-        _check_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace)
-    if stream is not None or dev != torch._C._cuda_getDevice():
-        with _On(k_pages.device, stream):
-            return cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, workspace)
-    num_pages, page_size, Hkv, d = shape[-4:]
-    lens = torch.empty_like(cache_lens)
-    status = torch.empty(2, dtype=i32, device=k_pages.device)
-    if workspace is None:
-        nbytes = _lib.fa_cache_resize_workspace_bytes(table[0]) or 1
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_pages.device)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    st = _lib.fa_cache_resize(page_refs.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                              cache_lens.data_ptr(), new_lens.data_ptr(), lens.data_ptr(), status.data_ptr(), table[0],
-                              table[1], num_pages, page_size, shape[0] if len(shape) == 5 else 1, Hkv, d,
-                              workspace.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_resize")
+    if stream is None and workspace is None:
+        both = (_fast or _paged_binding()).resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens)
+        if both is not None:
+            return _done(both, "fa_cache_resize")
+    import torch
+
+    pages, layers, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, True)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    c = [_check("page_refs", page_refs, torch.int32, (num_pages,)), *pages, *table,
+         _check("new_lens", new_lens, torch.int32, (B,))]
+    if workspace is not None:
+        c.append(_check_workspace(workspace))
+    dev = _same_device(*c)
+    with _On(dev, stream):
+        lens = torch.empty_like(cache_lens)
+        status = torch.empty(2, dtype=torch.int32, device=dev)
+        workspace, nbytes = _workspace(workspace, fa_cache_resize_workspace_bytes(B), dev)
+        _done(fa_cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, lens, status, B, max_pages,
+                              num_pages, page_size, layers, Hkv, d, workspace, nbytes), "fa_cache_resize")
     return lens, status

@@ -2,7 +2,10 @@
 
 Every ``csrc/*.cu`` translation unit is compiled for sm_103a only, in parallel,
 then linked into one shared library with the CUDA runtime linked statically,
-so the C ABI of ``include/fa.h`` is the only interface.
+so the C ABI of ``include/fa.h`` is the only interface.  The torch helpers of the
+paged cache have their ordinary call in a small CPython module beside it
+(``csrc/paged_binding.cpp``), compiled with the host compiler against the
+installed torch and named after its version.
 """
 from __future__ import annotations
 
@@ -10,8 +13,10 @@ import concurrent.futures as cf
 import glob
 import hashlib
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -32,12 +37,43 @@ def _flags(extra=()):
                    f"-I{CSRC}", f"-I{os.path.join(os.path.dirname(HERE), 'include')}"] + list(extra)
 
 
+BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
+
+
+def binding_path(torch) -> str:
+    return os.path.join(HERE, "_paged_binding_" + re.sub(r"[^0-9A-Za-z]", "_", torch.__version__) + ".so")
+
+
+def build_binding(force: bool = False) -> str:
+    import torch
+
+    path = binding_path(torch)
+    header = os.path.join(os.path.dirname(HERE), "include", "fa.h")
+    if not force and os.path.exists(path) and os.path.getmtime(path) >= max(map(os.path.getmtime, (BINDING_SRC, header))):
+        return path
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
+    libs = os.path.join(root, "lib")
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{os.path.join(root, 'include')}",
+           f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{cuda}", BINDING_SRC, "-o", tmp, f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = LIB_PATH) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
         os.path.join(os.path.dirname(HERE), "include", "fa.h")]
     newest = max(os.path.getmtime(p) for p in deps)
     if not force and not extra_flags and os.path.exists(lib_path) and os.path.getmtime(lib_path) >= newest:
+        build_binding()
         return lib_path
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = nvcc_path()
@@ -57,8 +93,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(build_binding, force) if lib_path == LIB_PATH else None
         objs = list(ex.map(compile_one, srcs))
+        if binding is not None:
+            binding.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs,
                        capture_output=True, text=True)
