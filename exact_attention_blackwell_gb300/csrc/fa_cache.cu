@@ -46,8 +46,10 @@ __global__ void __launch_bounds__(128)
 // One block per (sequence, layer, k or v); each thread carries its 16-byte
 // columns of the rows along the path in ascending order.  A path ascends, so
 // row i is never the source of a later move (source of move j > i is >= j), and
-// a thread touches its own columns only: no barrier is needed between moves.
-constexpr int kPathChunk = 128;
+// a thread touches its own columns only: no barrier is needed between moves, and
+// eight of them can be in flight (32 sequences x 32 layers, paths of up to 17: 13 us
+// where one at a time took 17).
+constexpr int kPathChunk = 128, kMoves = 8;
 
 __global__ void __launch_bounds__(128)
     cache_compact_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages,
@@ -83,11 +85,16 @@ __global__ void __launch_bounds__(128)
     }
     __syncthreads();
     const int stop = min(min(n - i0, kPathChunk), s_bad == INT_MAX ? INT_MAX : s_bad - i0);
-    for (int m = 0; m < stop; ++m) {
-      if (s_src[m] < 0) continue;
-      const uint4 *src = pages + (size_t)s_src[m] * chunks;
-      uint4 *dst = pages + (size_t)s_dst[m] * chunks;
-      for (int c = threadIdx.x; c < chunks; c += blockDim.x) dst[c] = src[c];
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+      for (int m0 = 0; m0 < stop; m0 += kMoves) {
+        uint4 x[kMoves];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u)
+          if (m0 + u < stop && s_src[m0 + u] >= 0) x[u] = pages[(size_t)s_src[m0 + u] * chunks + c];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u)
+          if (m0 + u < stop && s_src[m0 + u] >= 0) pages[(size_t)s_dst[m0 + u] * chunks + c] = x[u];
+      }
     }
     moved += max(stop, 0);
     const bool ended = s_bad != INT_MAX;
@@ -139,30 +146,33 @@ __global__ void __launch_bounds__(1024)
 // ------------------------------------------------------------------ resize
 // One block keeps the books: shrinking rows give their pages back, then the
 // growing rows' needs are summed, then free pages are handed out lowest first.
+// The block's time is a chain of loads, each about 0.6 us; so lengths are kept in
+// shared memory, and the counts of the first pages are fetched with them and used
+// where no row shrinks.
 constexpr int kBookThreads = 1024;
 constexpr int kPagesPerThread = 16;
 
 // Exclusive sum over the block; *total gets the whole sum.
 __device__ int block_scan(int x, int *warp_sums, int *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = x;
+  unsigned s = x;  // sums may wrap (see s_need)
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    const unsigned y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
   __syncthreads();
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  int w = lane < kBookThreads / 32 ? warp_sums[lane] : 0;
+  unsigned w = lane < kBookThreads / 32 ? (unsigned)warp_sums[lane] : 0u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int base = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-  return s - x + (warp > 0 ? base : 0);
+  *total = (int)__shfl_sync(0xffffffffu, w, 31);
+  const unsigned base = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return (int)(s - (unsigned)x + (warp > 0 ? base : 0u));
 }
 
 // copies: [0] their number, then (from, to, rows) for each
@@ -171,91 +181,118 @@ __global__ void __launch_bounds__(kBookThreads)
                         const int *__restrict__ new_lens, int *__restrict__ lens_out, int *__restrict__ status,
                         int *__restrict__ copies, int B, int max_pages, int num_pages, int page_size) {
   extern __shared__ int sm[];
-  int *last = sm, *first = sm + B;  // a growing row's shared partial page (or -1); its first rank among the taken pages
+  int *had = sm, *want = sm + B;              // lengths; -1 in both where the row is refused
+  int *last = sm + 2 * B, *first = sm + 3 * B;  // a growing row's shared partial page (or -1); its first rank among the taken pages
   __shared__ int warp_sums[32];
   __shared__ int s_refused, s_copies;
+  __shared__ unsigned long long s_need;  // the ranks below are 32 bits: they are used only where this fits the pool
   const int tid = threadIdx.x;
   const long long cap = (long long)max_pages * page_size;
-  if (tid == 0) s_refused = s_copies = 0;
+  if (tid == 0) {
+    s_refused = s_copies = 0;
+    s_need = 0;
+  }
   __syncthreads();
   grid_go();
   grid_wait();
   auto held = [&](int len) { return (int)(((long long)len + page_size - 1) / page_size); };
-  auto valid = [&](int a, int n) { return a >= 0 && n >= 0 && a <= cap && n <= cap; };
-
-  // shrinking rows: one warp a row
-  for (int b = tid >> 5; b < B; b += kBookThreads / 32) {
-    const int a = lens[b], n = new_lens[b];
-    if (!valid(a, n)) {
-      if ((tid & 31) == 0) atomicAdd(&s_refused, 1);
-      continue;
+  constexpr int kStretch = kBookThreads * kPagesPerThread;
+  // free pages of this thread's 16 from start + 16 tid on, as bits
+  auto free_pages = [&](int start) {
+    const int p = start + tid * kPagesPerThread;
+    unsigned mask = 0;
+    if (p + kPagesPerThread <= num_pages && (reinterpret_cast<uintptr_t>(refs) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < kPagesPerThread / 4; ++i) {
+        const int4 x = __ldcg(reinterpret_cast<const int4 *>(refs + p) + i);
+        mask |= ((x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3) << (4 * i);
+      }
+    } else {
+      for (int i = 0; i < kPagesPerThread; ++i)
+        if (p + i < num_pages && __ldcg(refs + p + i) == 0) mask |= 1u << i;
     }
-    for (int c = held(n) + (tid & 31); c < held(a); c += 32) {
-      const int page = table[(size_t)b * max_pages + c];
-      if (page >= 0 && page < num_pages) atomicSub(refs + page, 1);
-      table[(size_t)b * max_pages + c] = -1;
+    return mask;
+  };
+  unsigned mask = free_pages(0);
+  bool shrinks = false;
+  for (int b = tid; b < B; b += kBookThreads) {
+    int a = lens[b], n = new_lens[b];
+    if (a < 0 || n < 0 || a > cap || n > cap) {
+      atomicAdd(&s_refused, 1);
+      lens_out[b] = a;
+      a = n = -1;
     }
+    had[b] = a;
+    want[b] = n;
+    shrinks |= n < a;
   }
-  __threadfence();
-  __syncthreads();
+  if (__syncthreads_or(shrinks)) {
+    for (int b = tid >> 5; b < B; b += kBookThreads / 32) {  // one warp a row
+      if (want[b] >= had[b]) continue;
+      for (int c = held(want[b]) + (tid & 31); c < held(had[b]); c += 32) {
+        const int page = table[(size_t)b * max_pages + c];
+        if (page >= 0 && page < num_pages) atomicSub(refs + page, 1);
+        table[(size_t)b * max_pages + c] = -1;
+      }
+    }
+    __threadfence();
+    __syncthreads();
+    mask = free_pages(0);
+  }
 
   // growing rows whose last page is shared and only partly filled
+  bool grows = false, any_shared = false;
   for (int b = tid; b < B; b += kBookThreads) {
-    const int a = lens[b], n = new_lens[b];
+    const int a = had[b];
     int page = -1;
-    if (valid(a, n) && n > a && a % page_size != 0) {
+    grows |= want[b] > a;
+    if (want[b] > a && a % page_size != 0) {
       page = table[(size_t)b * max_pages + a / page_size];
       if (page < 0 || page >= num_pages || __ldcg(refs + page) <= 1) page = -1;
     }
     last[b] = page;
+    any_shared |= page >= 0;
   }
-  __syncthreads();
+  const bool sharing = __syncthreads_or(any_shared);
   // in row order, each of them takes a copy while another row still holds the page
-  int need_before = 0;
-  for (int b0 = 0; b0 < B; b0 += kBookThreads) {
-    const int b = b0 + tid;
-    int need = 0, copy = 0;
-    if (b < B) {
-      const int a = lens[b], n = new_lens[b];
-      if (last[b] >= 0) {
-        int rank = 0;
-        for (int o = 0; o < b; ++o) rank += last[o] == last[b];
-        copy = __ldcg(refs + last[b]) - rank > 1;
+  int total = 0;
+  if (__syncthreads_or(grows)) {
+    for (int b0 = 0; b0 < B; b0 += kBookThreads) {
+      const int b = b0 + tid;
+      int need = 0, copy = 0;
+      if (b < B && want[b] > had[b]) {
+        if (sharing && last[b] >= 0) {
+          int rank = 0;
+          for (int o = 0; o < b; ++o) rank += last[o] == last[b];
+          copy = __ldcg(refs + last[b]) - rank > 1;
+        }
+        need = held(want[b]) - held(had[b]) + copy;
+        if (need) atomicAdd(&s_need, (unsigned long long)need);
       }
-      if (valid(a, n) && n > a) need = held(n) - held(a) + copy;
+      int sum;
+      const int at = block_scan(need, warp_sums, &sum);
+      if (b < B) first[b] = (int)(((unsigned)total + (unsigned)at) * 2u) + copy;
+      total = (int)((unsigned)total + (unsigned)sum);
     }
-    int sum;
-    const int at = block_scan(need, warp_sums, &sum);
-    if (b < B) first[b] = (need_before + at) * 2 + copy;
-    need_before += sum;
+    __syncthreads();
   }
-  const int total = need_before;
-  __syncthreads();
-  // enough free pages?  `masks` of the last stretch looked at stays in registers
-  int found = 0, p0 = 0;
-  unsigned mask = 0;
-  int at = 0;
-  constexpr int kStretch = kBookThreads * kPagesPerThread;
-  auto look = [&](int start) {
-    mask = 0;
-    const int p = start + tid * kPagesPerThread;
-#pragma unroll
-    for (int i = 0; i < kPagesPerThread; ++i)
-      if (p + i < num_pages && __ldcg(refs + p + i) == 0) mask |= 1u << i;
+  const bool fits = s_need <= (unsigned long long)num_pages;
+  if (!fits) total = INT_MAX;  // more than there can be: count the free pages, all of them
+  // enough free pages?  Those of the last stretch looked at stay in `mask`
+  int found = 0, p0 = 0, at = 0;
+  for (; p0 < num_pages && found < total; p0 += kStretch) {
+    if (p0 > 0) mask = free_pages(p0);
     int sum;
     at = block_scan(__popc(mask), warp_sums, &sum);
-    return sum;
-  };
-  for (; p0 < num_pages && found < total; p0 += kStretch) found += look(p0);
-  const bool can = found >= total;
+    found += sum;
+  }
+  const bool can = fits && found >= total;
   if (tid == 0) {
-    status[0] = can ? 0 : total - found;
+    status[0] = can ? 0 : (int)min(s_need - (unsigned long long)found, (unsigned long long)INT_MAX);
     status[1] = s_refused;
   }
-  for (int b = tid; b < B; b += kBookThreads) {
-    const int a = lens[b], n = new_lens[b];
-    lens_out[b] = !valid(a, n) || (n > a && !can) ? a : n;
-  }
+  for (int b = tid; b < B; b += kBookThreads)
+    if (had[b] >= 0) lens_out[b] = want[b] > had[b] && !can ? had[b] : want[b];
   if (!can || total == 0) {
     if (tid == 0) copies[0] = 0;
     return;
@@ -263,7 +300,11 @@ __global__ void __launch_bounds__(kBookThreads)
   int done = 0;
   const bool once = p0 <= kStretch;  // one stretch held them all: it is still in registers
   for (int s0 = 0; done < total; s0 += kStretch) {
-    const int sum = once ? found : look(s0);
+    int sum = found;
+    if (!once) {
+      mask = free_pages(s0);
+      at = block_scan(__popc(mask), warp_sums, &sum);
+    }
     int k = done + at;
     unsigned m = mask;
     while (m && k < total) {
@@ -275,7 +316,7 @@ __global__ void __launch_bounds__(kBookThreads)
         if ((first[mid] >> 1) <= k) lo = mid;
         else hi = mid;
       }
-      const int a = lens[lo];
+      const int a = had[lo];
       int *row = table + (size_t)lo * max_pages;
       const int copy = first[lo] & 1, nth = k - (first[lo] >> 1);
       if (copy && nth == 0) {
@@ -300,7 +341,7 @@ __global__ void __launch_bounds__(kBookThreads)
 
 // The filled rows of shared pages, in every layer, k and v: contiguous runs of
 // rows * chunks 16-byte pieces, cut into pieces of kCopyChunk.
-constexpr int kCopyChunk = 1024;
+constexpr int kCopyChunk = 2048;
 
 __global__ void __launch_bounds__(256)
     cache_copy_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages, const int *__restrict__ copies,
@@ -319,7 +360,13 @@ __global__ void __launch_bounds__(256)
     uint4 *pages = ((part & 1) ? v_pages : k_pages) + (size_t)(part >> 1) * num_pages * page_chunks;
     const uint4 *src = pages + (size_t)from * page_chunks;
     uint4 *dst = pages + (size_t)to * page_chunks;
-    for (int i = piece * kCopyChunk + threadIdx.x; i < end; i += blockDim.x) dst[i] = src[i];
+    uint4 x[kCopyChunk / 256];
+#pragma unroll
+    for (int u = 0; u < kCopyChunk / 256; ++u)
+      if (const int i = piece * kCopyChunk + u * 256 + (int)threadIdx.x; i < end) x[u] = src[i];
+#pragma unroll
+    for (int u = 0; u < kCopyChunk / 256; ++u)
+      if (const int i = piece * kCopyChunk + u * 256 + (int)threadIdx.x; i < end) dst[i] = x[u];
   }
 }
 
@@ -430,7 +477,7 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if (rc == FA_OK) rc = check_page_rows(layers, num_pages, page_size, Hkv, d);
   if (rc != FA_OK) return rc;
   if (lens_out == cache_lens || lens_out == new_lens) return FA_ERR_INVALID_ARG;
-  if (B > kMaxBookRows) return FA_ERR_UNSUPPORTED;
+  if (B > kMaxBookRows || num_pages > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (!ptr_aligned(k_pages, 16) || !ptr_aligned(v_pages, 16)) return FA_ERR_ALIGNMENT;
   for (const void *x : {(const void *)page_refs, (const void *)page_table, (const void *)cache_lens,
                         (const void *)new_lens, (const void *)lens_out, (const void *)status})
@@ -438,11 +485,14 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if (!workspace || workspace_bytes < resize_bytes(B) || !ptr_aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   int *copies = static_cast<int *>(workspace);
+  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBookRows * 16) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 8, s, page_refs, page_table, cache_lens,
+  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 16, s, page_refs, page_table, cache_lens,
                          new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size)) != FA_OK)
     return rc;
-  return launch_after(cache_copy_kernel, 152 * 4, 256, 0, s, static_cast<uint4 *>(k_pages),
+  return launch_after(cache_copy_kernel, 152 * 2, 256, 0, s, static_cast<uint4 *>(k_pages),
                       static_cast<uint4 *>(v_pages), (const int *)copies, num_pages, page_size, layers, Hkv * d / 8);
 }
 

@@ -208,6 +208,22 @@ def test_resize_takes_nothing_when_pages_are_missing():
     assert refs.tolist() == [1] * 6 and table.tolist() == [[0, 2, 1], [4, -1, -1], [3, 5, -1]]
 
 
+def test_resize_counts_needs_past_32_bits():
+    """4096 rows that want 2^20 pages each: 2^32 in all, which wraps to 0 in 32 bits."""
+    cols = 1 << 20
+    k = v = rows((5, 16, 1, 64), 1)
+    table = torch.full((4096, cols), -1, dtype=torch.int32, device="cuda")
+    refs = i32([0, 1, 0, 0, 1])
+    lens = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    out, status = fa.cache_resize(refs, k, v, table, lens, torch.full_like(lens, cols * 16))
+    assert status.tolist() == [2**31 - 1, 0] and int(out.sum()) == 0 and refs.tolist() == [0, 1, 0, 0, 1]
+    want = lens.clone()
+    want[4095] = 48
+    out, status = fa.cache_resize(refs, k, v, table, lens, want)
+    assert status.tolist() == [0, 0] and out.tolist() == want.tolist() and refs.tolist() == [1] * 5
+    assert table[4095, :4].tolist() == [0, 2, 3, -1]
+
+
 def test_resize_with_rubbish_in_the_table_stays_in_bounds():
     k, v = rows((4, 16, 1, 64), 1), rows((4, 16, 1, 64), 2)
     refs, table = i32([2, 2, 0, 0]), i32([[99, -1], [-7, 2**31 - 1], [0, 1]])
