@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(1024)
 // shared memory, and the counts of the first pages are fetched with them and used
 // where no row shrinks.
 constexpr int kBookThreads = 1024;
-constexpr int kPagesPerThread = 16;
+constexpr int kPagesPerThread = 16, kStretch = kBookThreads * kPagesPerThread;
 
 // Exclusive sum over the block; *total gets the whole sum.
 __device__ int block_scan(int x, int *warp_sums, int *total) {
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kBookThreads)
   extern __shared__ int sm[];
   int *had = sm, *want = sm + B;              // lengths; -1 in both where the row is refused
   int *last = sm + 2 * B, *first = sm + 3 * B;  // a growing row's shared partial page (or -1); its first rank among the taken pages
+  unsigned short *list = reinterpret_cast<unsigned short *>(sm + 4 * B);  // [kStretch]
   __shared__ int warp_sums[32];
   __shared__ int s_refused, s_copies;
   __shared__ unsigned long long s_need;  // the ranks below are 32 bits: they are used only where this fits the pool
@@ -196,7 +197,6 @@ __global__ void __launch_bounds__(kBookThreads)
   grid_go();
   grid_wait();
   auto held = [&](int len) { return (int)(((long long)len + page_size - 1) / page_size); };
-  constexpr int kStretch = kBookThreads * kPagesPerThread;
   // free pages of this thread's 16 from start + 16 tid on, as bits
   auto free_pages = [&](int start) {
     const int p = start + tid * kPagesPerThread;
@@ -248,7 +248,9 @@ __global__ void __launch_bounds__(kBookThreads)
     grows |= want[b] > a;
     if (want[b] > a && a % page_size != 0) {
       page = table[(size_t)b * max_pages + a / page_size];
-      if (page < 0 || page >= num_pages || __ldcg(refs + page) <= 1) page = -1;
+      const int count = page >= 0 && page < num_pages ? __ldcg(refs + page) : 0;
+      if (count <= 1) page = -1;
+      first[b] = count;  // until the row's rank takes its place
     }
     last[b] = page;
     any_shared |= page >= 0;
@@ -262,13 +264,16 @@ __global__ void __launch_bounds__(kBookThreads)
       int need = 0, copy = 0;
       if (b < B && want[b] > had[b]) {
         if (sharing && last[b] >= 0) {
-          int rank = 0;
+          int rank = 0;  // rows before this one that have to copy the same page
+#pragma unroll 8
           for (int o = 0; o < b; ++o) rank += last[o] == last[b];
-          copy = __ldcg(refs + last[b]) - rank > 1;
+          copy = first[b] - rank > 1;
         }
         need = held(want[b]) - held(had[b]) + copy;
-        if (need) atomicAdd(&s_need, (unsigned long long)need);
       }
+      // a row needs at most 2^26 pages + 1: 32 of them stay below 2^32
+      const unsigned warp_need = __reduce_add_sync(0xffffffffu, (unsigned)need);
+      if ((tid & 31) == 0 && warp_need) atomicAdd(&s_need, (unsigned long long)warp_need);
       int sum;
       const int at = block_scan(need, warp_sums, &sum);
       if (b < B) first[b] = (int)(((unsigned)total + (unsigned)at) * 2u) + copy;
@@ -305,11 +310,14 @@ __global__ void __launch_bounds__(kBookThreads)
       mask = free_pages(s0);
       at = block_scan(__popc(mask), warp_sums, &sum);
     }
-    int k = done + at;
-    unsigned m = mask;
-    while (m && k < total) {
-      const int page = s0 + tid * kPagesPerThread + __ffs(m) - 1;
-      m &= m - 1;
+    // the stretch's free pages in order, then one thread for each of them
+    const int take = min(sum, total - done);
+    int k = at;
+    for (unsigned m = mask; m && k < take; m &= m - 1) list[k++] = (unsigned short)(tid * kPagesPerThread + __ffs(m) - 1);
+    __syncthreads();
+    for (int i = tid; i < take; i += kBookThreads) {
+      const int page = s0 + list[i];
+      k = done + i;
       int lo = 0, hi = B;  // the last row whose first rank is <= k
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -330,7 +338,6 @@ __global__ void __launch_bounds__(kBookThreads)
         row[held(a) + nth - copy] = page;
       }
       refs[page] = 1;
-      ++k;
     }
     done += sum;
     __syncthreads();
@@ -485,11 +492,11 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if (!workspace || workspace_bytes < resize_bytes(B) || !ptr_aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   int *copies = static_cast<int *>(workspace);
-  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBookRows * 16) !=
+  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBookRows * 16 + kStretch * 2) !=
       cudaSuccess)
     return FA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 16, s, page_refs, page_table, cache_lens,
+  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table, cache_lens,
                          new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size)) != FA_OK)
     return rc;
   return launch_after(cache_copy_kernel, 152 * 2, 256, 0, s, static_cast<uint4 *>(k_pages),
