@@ -579,11 +579,12 @@ int fa_last_device_status(void *stream) { return fa_last_device_status_site(stre
 
 int fa_debug_stall(int mode) {
 #ifdef FA_TEST_STALL
-  if (mode < 0 || mode > 3) return FA_ERR_INVALID_ARG;
+  if (mode < 0 || mode > 5) return FA_ERR_INVALID_ARG;
   int rc = check_device();
   if (rc != FA_OK) return rc;
   if ((rc = set_test_stall_fwd(mode)) != FA_OK) return rc;
-  return set_test_stall_bwd(mode);
+  if ((rc = set_test_stall_bwd(mode)) != FA_OK) return rc;
+  return set_test_stall_paged(mode);
 #else
   (void)mode;
   return FA_ERR_UNSUPPORTED;

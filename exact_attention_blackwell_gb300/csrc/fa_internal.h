@@ -230,11 +230,13 @@ int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[
 
 // Test builds only (-DFA_TEST_STALL): block 0 of the chosen kernel skips one
 // barrier arrival (1: the forward's first P, 2: the dK/dV kernels' first P,
-// 3: the dQ kernels' first dS), so that a bounded wait runs out and the kernel
+// 3: the dQ kernels' first dS, 4: the paged kernel's first P, 5: the few-rows paged
+// kernel's first tile read), so that a bounded wait runs out and the kernel
 // unwinds through its abort path.  Each translation unit keeps its own flag.
 #ifdef FA_TEST_STALL
 int set_test_stall_fwd(int mode);
 int set_test_stall_bwd(int mode);
+int set_test_stall_paged(int mode);
 #define FA_STALL_FLAG_DECL static __device__ int g_test_stall;
 #define FA_STALL(k) (g_test_stall == (k) && blockIdx.x == 0)
 #else

@@ -18,8 +18,9 @@ namespace {
 // Work.  A unit is one key tile (bn places) of one item; an item is one (sequence,
 // HB adjacent kv heads, row group), a row group being QT tiles of TB * G rows (TB
 // tokens with the G query heads that share a kv head).  The units of all items stand in one
-// line, cut into equal stretches for the blocks, so that ragged batches keep all
-// SMs busy; the lengths are known on the device only, so every block sums them up
+// line, each item's after `lead` units without a tile that stand for its other costs
+// (fetching its Q, writing its result), cut into equal stretches for the blocks, so
+// that ragged batches keep all SMs busy; the lengths are known on the device only, so every block sums them up
 // itself.  A block that gets only a part of an item writes its unnormalised O with
 // the row maxima and sums; paged_combine_kernel joins the parts.
 struct PagedParams {
@@ -39,6 +40,7 @@ struct PagedParams {
   int bn_log2, QT, HB;  // places in a tile; row tiles and kv heads of an item
   int heads;            // Hkv / HB
   int min_units;        // a block's stretch is no shorter
+  int lead;             // units that stand for what an item costs beside its tiles
   int join;             // warps that share a task of the join
   float scale_log2;
 };
@@ -82,6 +84,8 @@ template <bool PAIR>
 __device__ __forceinline__ int v_fill(int j, int nt) {
   return PAIR ? 2 * j + 1 : j + 1 < nt ? 2 * j + 2 : 2 * nt - 1;
 }
+
+FA_STALL_FLAG_DECL
 
 enum PagedSite : int {
   kPSiteQ = 31, kPSiteKFull = 32, kPSiteVFull = 33, kPSitePFull = 34, kPSiteEmpty = 35,
@@ -138,7 +142,7 @@ __device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long
     if (s.n == 0) return 0;
     int tiles, groups;
     paged_units(p, s, tiles, groups);
-    return (long long)tiles * groups * p.heads;
+    return (long long)(tiles + p.lead) * groups * p.heads;
   };
   auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
     long long sum = x;
@@ -199,6 +203,7 @@ struct PagedWalk {
   long long u, end, base;
   int b, tiles, groups;
   PagedSeq s;
+  int items;  // so far
   // the current item
   int kh, rg, j0, j1;
   bool whole, first;
@@ -206,6 +211,7 @@ struct PagedWalk {
   __device__ void start(const PagedParams &p, const PagedStretch &r, const PagedStart &at) {
     u = r.begin;
     end = at.b < 0 ? r.begin : r.end;
+    items = 0;
     base = at.base;
     b = at.b;
     s = at.s;
@@ -218,24 +224,30 @@ struct PagedWalk {
     }
     if (b < p.g.B) paged_units(p, s, tiles, groups);
   }
-  __device__ bool next(const PagedParams &p, long long begin) {
-    if (u >= end) return false;
-    if ((unsigned)(u - base) >= (unsigned)tiles * groups * p.heads) {
-      base = u;
-      ++b;
-      load(p);
-      if (b >= p.g.B) return false;
+  __device__ bool next(const PagedParams &p) {
+    while (u < end) {
+      const unsigned span = (unsigned)(tiles + p.lead);
+      if ((unsigned)(u - base) >= span * groups * p.heads) {
+        base = u;
+        ++b;
+        load(p);
+        if (b >= p.g.B) return false;
+        continue;
+      }
+      const unsigned r = (unsigned)(u - base);  // a sequence's units fit 31 bits (checked by the host)
+      const int item = (int)(r / span), at = (int)(r - (unsigned)item * span);
+      const int stop = end - u < (int)span - at ? at + (int)(end - u) : (int)span;
+      u += stop - at;
+      j0 = max(at - p.lead, 0);
+      j1 = stop - p.lead;
+      if (j1 <= j0) continue;  // the units without a tile only
+      kh = groups == 1 ? item : item / groups;
+      rg = item - kh * groups;
+      whole = j0 == 0 && j1 == tiles;
+      first = items++ == 0;
+      return true;
     }
-    const unsigned r = (unsigned)(u - base);  // a sequence's units fit 31 bits (checked by the host)
-    const int item = (int)(r / (unsigned)tiles);
-    j0 = (int)(r - (unsigned)item * (unsigned)tiles);
-    j1 = end - u < tiles - j0 ? j0 + (int)(end - u) : tiles;
-    kh = groups == 1 ? item : item / groups;
-    rg = item - kh * groups;
-    whole = j0 == 0 && j1 == tiles;
-    first = u == begin;
-    u += j1 - j0;
-    return true;
+    return false;
   }
 };
 
@@ -363,7 +375,6 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   grid_go();
   grid_wait();
   const PagedStretch stretch = block_stretch<C::kThreads>(p, s_sums, at);
-  const long long begin = stretch.begin;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     int tile_no = 0, o_no = 0, pv_no = 0;  // tiles, items, and items of several tiles of this row tile so far
     int tiles = 0, item = 0;               // tiles and items of the block
     bool ok = true;
-    while (ok && walk.next(p, begin)) {
+    while (ok && walk.next(p)) {
       ++item;
       const int tokens = tile_tokens(t), nt = walk.j1 - walk.j0;
       const int i = (walk.rg * QT + t) * p.TB + tok;  // this row's token in its sequence
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             tmem_wait_st();
             tc_fence_before();
           }
-          mbar_arrive_warp(p_bar(t, buf));
+          if (!(FA_STALL(4) && tile_no == 0 && t == 0)) mbar_arrive_warp(p_bar(t, buf));
         }
         // ----------------------------------------------------- epilogue
         if (ok) ok = mbar_wait_warp(o_bar(t), o_no & 1, wctx, kPSiteOFull);
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     int fill = 0, seg = 0;      // ring slots, items
     int s_no[QT] = {}, p_no[QT] = {};  // tiles through S and through P V, by row tile
     bool ok = true;
-    while (ok && walk.next(p, begin)) {
+    while (ok && walk.next(p)) {
       const int nt = walk.j1 - walk.j0;
       bool act[QT];
 #pragma unroll
@@ -683,7 +694,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     const uint32_t ring = sbase + C::kOffRing;
     int fill = 0, seg = 0, tile = 0;
     bool ok = true;
-    while (ok && walk.next(p, begin)) {
+    while (ok && walk.next(p)) {
       const int nt = walk.j1 - walk.j0;
       const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
       auto page_at = [&](int j) {  // this lane's page of tile j: -2 where the sequence has ended, -1 where there is none
@@ -864,7 +875,7 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
     const int sharers = W / p.HB, hb = warp / sharers, sub = warp - hb * sharers;  // warps of a kv head
     const float c2 = p.scale_log2;
     int fill = 0, item = 0;
-    while (walk.next(p, stretch.begin)) {
+    while (walk.next(p)) {
       ++item;
       const int nt = walk.j1 - walk.j0, rows = walk.s.n * p.G, kh = walk.kh * p.HB + hb;
       // this thread's rows: 16 m + q4 and + 8
@@ -1012,7 +1023,7 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
             }
           }
         }
-        mbar_arrive_warp(empty_bar(slot));
+        if (!(FA_STALL(5) && fill == 0 && warp == 0)) mbar_arrive_warp(empty_bar(slot));
       }
       float row_l[MT][2];
 #pragma unroll
@@ -1136,7 +1147,7 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
     // lane = (kv * HB + head) * boxes + box: at most 2 * HB * (64 / HB) / 16 = 8 lanes
     const int box = lane % boxes, head = lane / boxes % p.HB, kv = lane / (boxes * p.HB);
     int fill = 0;
-    while (ok && walk.next(p, stretch.begin)) {
+    while (ok && walk.next(p)) {
       const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
       auto page_at = [&](int j) {  // -2 where the sequence has ended, -1 where there is no page
         const int pos = j * bn + box * box_rows;
@@ -1214,11 +1225,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
   int parts = 0, c0 = 0;
   long long first = 0;
   if (mine) {
-    const long long u0 = p.prefix[b] + (long long)item * tiles;
+    const long long u0 = p.prefix[b] + (long long)item * (tiles + p.lead);
     const long long per = stretch_units(p, p.prefix[p.g.B], blocks);
-    c0 = (int)quot(u0, per);
-    parts = (int)quot(u0 + tiles - 1, per) - c0 + 1;
-    // only the first block can have had another item before this one: then it is its second part
+    c0 = (int)quot(u0 + p.lead, per);
+    parts = (int)quot(u0 + p.lead + tiles - 1, per) - c0 + 1;
+    // only the first block can have had tiles of another item before this one's: it begins before this
+    // item's units (the ones before them are tiles), and this is its second part
     first = (long long)c0 * 2 + (u0 > c0 * per ? 1 : 0);
     mine = parts > 1;  // else one block had it all and has written the result
     if (!mine) parts = 0;
@@ -1368,6 +1380,13 @@ int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pa
 }
 
 }  // namespace
+
+#ifdef FA_TEST_STALL
+int set_test_stall_paged(int mode) {
+  return cudaMemcpyToSymbol(g_test_stall, &mode, sizeof(int)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+#endif
+
 }  // namespace fa
 
 using namespace fa;
@@ -1399,7 +1418,8 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   if (total == 0) return FA_OK;
   const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
   // the units of one sequence are counted in 31 bits
-  if ((double)max_pages * page_size / w.bn * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB) >= 2147483648.0) return FA_ERR_UNSUPPORTED;
+  if (((double)max_pages * page_size / w.bn + 8) * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB) >= 2147483648.0)
+    return FA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1424,6 +1444,9 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.bn_log2 = w.bn == 128 ? 7 : w.bn == 64 ? 6 : w.bn == 32 ? 5 : 4;
   p.heads = Hkv / w.HB;
   p.min_units = w.MT ? 2 : 1;
+  // Measured, in microseconds of tiles, against none: 48 ragged sequences of drafted trees 54 (63), at head
+  // dim 64 44 (74), at head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).
+  p.lead = w.MT ? 2 : w.QT == 2 ? 4 : 3;
   // parts an item is cut into on average, two a warp and four in flight
   const long long items = (long long)B * p.heads * (w.TB * w.QT >= max_new ? 1 : (max_new + w.TB * w.QT - 1) / (w.TB * w.QT));
   p.join = w.blocks / items >= 16 ? 8 : w.blocks / items >= 8 ? 4 : 1;

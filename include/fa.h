@@ -324,7 +324,10 @@ int fa_last_device_status(void *stream);
  * slot free, 14 S computed, 15 dP computed, 16 P stored, 17 dS stored,
  * 19 final MMA, 20 MMA drain, 21 shared-memory alignment, 22 the dQ kernel's
  * Q and dO tiles loaded; fused backward: 23 dQ partial computed, 24 S read
- * into registers, 25 dQ partial read out).  Outputs of a call in which a wait
+ * into registers, 25 dQ partial read out); paged attention 31-39 (31 Q tile
+ * loaded, 32/33 K/V tile loaded, 34 P stored, 35 ring slot free, 36 S computed,
+ * 37 O readable, 38 MMA drain, 39 Q tile free) and, with few rows, 41 K and V
+ * tile loaded, 42 ring slot free.  Outputs of a call in which a wait
  * ran out are unspecified. */
 int fa_last_device_status_site(void *stream, int *site);
 
@@ -332,7 +335,8 @@ int fa_last_device_status_site(void *stream, int *site);
  * build), makes block 0 of one kernel skip one barrier arrival on every later
  * launch until called again with mode 0, so that a bounded wait runs out and
  * the kernel unwinds through its abort path (1: the forward's first P, 2: the
- * dK/dV kernels' first P, 3: the dQ kernel's first dS); build such a library
+ * dK/dV kernels' first P, 3: the dQ kernel's first dS, 4: the paged attention
+ * kernel's first P, 5: its few-rows kernel's first tile read); build such a library
  * with a short -DFA_WAIT_LIMIT_NS.  Returns FA_ERR_INVALID_ARG for another
  * mode.  In every other build it does nothing and returns FA_ERR_UNSUPPORTED. */
 int fa_debug_stall(int mode);

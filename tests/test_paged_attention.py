@@ -39,6 +39,11 @@ CASES = [
     ([60, 3], [256, 200], 32, 2, 1, 64),
     ([60, 3], [256, 131], 16, 4, 2, 256),
     ([5] * 40, [1, 2] * 20, 16, 2, 2, 64),
+    ([600, 33], [90, 70], 256, 4, 2, 128),
+    ([200, 15], [140, 150], 16, 2, 2, 128),
+    ([700, 300], [33, 31], 128, 20, 4, 256),
+    ([40, 500, 90], [4, 2, 4], 16, 12, 3, 128),
+    ([40, 500, 90], [2, 2, 1], 32, 12, 2, 256),
 ]
 
 
@@ -135,6 +140,27 @@ def test_rows_of_no_sequence_and_past_max_new_are_left_alone():
     keep = [1, 2, 3, 4, 5, 6]
     s2 = s
     pm.check_attention(s2, o[keep], lse[:, keep], tuple(x[keep] if x.dim() == 3 else x[:, keep] for x in ref), "the rest")
+
+
+@pytest.mark.parametrize("B,new_of,H,Hkv,d", [(700, lambda b: 1, 2, 2, 64), (1500, lambda b: 3 if b % 97 == 5 else 0, 4, 4, 128),
+                                              (400, lambda b: b % 23, 4, 1, 128), (1000, lambda b: 40 if b == 999 else 0, 4, 1, 64),
+                                              (370, lambda b: 70 if b % 9 == 0 else 1, 2, 1, 128)])
+def test_many_sequences(B, new_of, H, Hkv, d):
+    """More sequences than a block has threads, most of them without new tokens."""
+    s = pm.Setup([(7 * b) % 90 for b in range(B)], [new_of(b) for b in range(B)], 16, Hkv, d, seed=B, H=H)
+    o, lse = run(s, max(s.new))
+    pm.check_attention(s, o, lse, pm.attention(s, s.q), f"B {B}")
+
+
+def test_max_new_may_be_larger_than_any_sequence_has():
+    s = pm.Setup([200, 31, 0, 77], [5, 0, 3, 1], 32, 2, 128, seed=4, H=4)
+    ref = pm.attention(s, s.q)
+    for most in (5, 8, 9, 17, 64, 65, 256):
+        o, lse = run(s, most)
+        pm.check_attention(s, o, lse, ref, f"max_new {most}")
+        mask, seen = pm.tree_masks(s.new, (most + 63) // 64, seed=most)
+        o, lse = run(s, most, mask)
+        pm.check_attention(s, o, lse, pm.attention(s, s.q, seen), f"max_new {most}, trees")
 
 
 def test_empty_batch():
