@@ -120,37 +120,65 @@ __device__ __forceinline__ long long stretch_units(const PagedParams &p, long lo
   return max(quot(total + blocks - 1, blocks), (long long)p.min_units);
 }
 
-// This block's stretch [begin, end) of all units; *at gets the sequence it begins
-// in (b stays -1 where there is none) and that one's first unit, after the caller's
-// next barrier.  By all threads of the block.  Block 0 also leaves every sequence's
-// first unit in p.prefix for the join.
-struct PagedStretch {
-  long long begin, end;
-};
+__device__ __forceinline__ long long units_of(const PagedParams &p, const PagedSeq &s) {
+  if (s.n == 0) return 0;
+  int tiles, groups;
+  paged_units(p, s, tiles, groups);
+  return (long long)(tiles + p.lead) * groups * p.heads;
+}
+__device__ __forceinline__ long long warp_scan(long long x) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+
+// A block's stretch [begin, end) of all units, the sequence it begins in (b < 0
+// where there is none) and that one's first unit.
 struct PagedStart {
-  long long base;
+  long long begin, end, base;
   PagedSeq s;
   int b;
 };
+
+// Up to 32 sequences: every warp sums them up by itself, a lane each.
+constexpr int kWarpSeqs = 32;
+__device__ __forceinline__ PagedStart warp_stretch(const PagedParams &p) {
+  const int lane = threadIdx.x & 31;
+  PagedSeq s = {0, 0, 0, 0};
+  if (lane < p.g.B) s = paged_seq(p, lane);
+  const long long x = units_of(p, s), sum = warp_scan(x), total = __shfl_sync(0xffffffffu, sum, 31);
+  const long long per = stretch_units(p, total, gridDim.x);
+  PagedStart r;
+  r.begin = min(per * blockIdx.x, total);
+  r.end = min(r.begin + per, total);
+  const unsigned here = __ballot_sync(0xffffffffu, r.begin >= sum - x && r.begin < sum);
+  const int b = __ffs(here) - 1, from = max(b, 0);
+  r.base = __shfl_sync(0xffffffffu, sum - x, from);
+  r.s.start = __shfl_sync(0xffffffffu, s.start, from);
+  r.s.n = __shfl_sync(0xffffffffu, s.n, from);
+  r.s.len = __shfl_sync(0xffffffffu, s.len, from);
+  r.s.keys = __shfl_sync(0xffffffffu, s.keys, from);
+  r.b = b;
+  return r;
+}
+
+// More: the block together, through *at (b = -1 on entry), which holds the result
+// after the caller's next barrier.  Block 0 also leaves every sequence's first unit
+// in p.prefix for the join.
 template <int THREADS>
-__device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long long *s_sums, PagedStart *at) {
+__device__ __forceinline__ void block_stretch(const PagedParams &p, long long *s_sums, PagedStart *at) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PagedSeq s;
-  auto units_of = [&](int b) -> long long {
+  auto units = [&](int b) -> long long {
     if (b >= p.g.B) return 0;
     s = paged_seq(p, b);
-    if (s.n == 0) return 0;
-    int tiles, groups;
-    paged_units(p, s, tiles, groups);
-    return (long long)(tiles + p.lead) * groups * p.heads;
+    return units_of(p, s);
   };
   auto block_scan = [&](long long x, long long &total) -> long long {  // exclusive
-    long long sum = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
+    const long long sum = warp_scan(x);
     __syncthreads();
     if (lane == 31) s_sums[warp] = sum;
     __syncthreads();
@@ -158,44 +186,37 @@ __device__ __forceinline__ PagedStretch block_stretch(const PagedParams &p, long
     total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-      const long long x = s_sums[w];
-      if (w < warp) before += x;
-      total += x;
+      const long long y = s_sums[w];
+      if (w < warp) before += y;
+      total += y;
     }
     return before + sum - x;
   };
-  long long first_sum;
-  const long long mine = units_of(threadIdx.x), first_before = block_scan(mine, first_sum);
-  long long total_units = first_sum;
-  for (int b0 = THREADS; b0 < p.g.B; b0 += THREADS) {
+  long long total_units = 0;
+  for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
     long long sum;
-    block_scan(units_of(b0 + (int)threadIdx.x), sum);
+    block_scan(units(b0 + (int)threadIdx.x), sum);
     total_units += sum;
   }
   const long long per = stretch_units(p, total_units, gridDim.x);
-  PagedStretch r;
-  r.begin = min(per * blockIdx.x, total_units);
-  r.end = min(r.begin + per, total_units);
+  const long long begin = min(per * blockIdx.x, total_units);
   long long done = 0;
   for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
     const int b = b0 + (int)threadIdx.x;
-    long long before = first_before, sum = first_sum, x = mine;
-    if (p.g.B > THREADS) {
-      x = units_of(b);
-      before = block_scan(x, sum);
-    }
-    before += done;
-    if (b < p.g.B && r.begin >= before && r.begin < before + x) {
+    long long sum;
+    const long long x = units(b), before = done + block_scan(x, sum);
+    if (b < p.g.B && begin >= before && begin < before + x) {
+      at->begin = begin;
+      at->end = min(begin + per, total_units);
       at->base = before;
       at->s = s;
       at->b = b;
     }
     if (blockIdx.x == 0 && b < p.g.B) p.prefix[b] = before;
     done += sum;
-    if (blockIdx.x != 0 && done > r.begin) break;
+    if (blockIdx.x != 0 && done > begin) break;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.prefix[p.g.B] = total_units;
-  return r;
 }
 
 // A stretch of units, item by item; every warp of a block walks its own copy.
@@ -208,9 +229,9 @@ struct PagedWalk {
   int kh, rg, j0, j1;
   bool whole, first;
 
-  __device__ void start(const PagedParams &p, const PagedStretch &r, const PagedStart &at) {
-    u = r.begin;
-    end = at.b < 0 ? r.begin : r.end;
+  __device__ void start(const PagedParams &p, const PagedStart &at) {
+    u = at.b < 0 ? 0 : at.begin;
+    end = at.b < 0 ? 0 : at.end;
     items = 0;
     base = at.base;
     b = at.b;
@@ -346,7 +367,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   uint8_t *misc = smem + C::kOffMisc;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
-  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 192);  // 32 bytes
+  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 192);  // 48 bytes
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
   volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
   long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32] <= 11
@@ -372,15 +393,15 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
   }
-  grid_go();
   grid_wait();
-  const PagedStretch stretch = block_stretch<C::kThreads>(p, s_sums, at);
+  grid_go();  // only now: the join reads the call's inputs without a wait of its own
+  if (p.g.B > kWarpSeqs) block_stretch<C::kThreads>(p, s_sums, at);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PagedWalk walk;
-  walk.start(p, stretch, *at);
+  walk.start(p, p.g.B > kWarpSeqs ? *at : warp_stretch(p));
 
   auto tile_tokens = [&](int t) { return max(0, min(p.TB, walk.s.n - (walk.rg * QT + t) * p.TB)); };
 
@@ -796,7 +817,7 @@ struct FewCfg {
   static_assert(kStages >= 2, "ring");
   static constexpr int kOffRing = 0, kOffJoin = 2 * kStages * kTileBytes, kOffBar = kOffJoin + kJoinBytes;
   static constexpr int kOffMisc = kOffBar + 16 * kStages;
-  static constexpr int kOffML = kOffMisc + 80;  // [kWarps][16 * MT] float2
+  static constexpr int kOffML = kOffMisc + 96;  // [kWarps][16 * MT] float2
   static constexpr int kOffSums = kOffML + kWarps * 16 * MT * 8;
   static constexpr int kSmemBytes = kOffSums + 8 * (kWarps + 1) + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
@@ -840,9 +861,9 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
   uint8_t *misc = smem + C::kOffMisc;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc);
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 4);             // the last item with cleared V values
-  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 8);                  // 32 bytes
-  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 40);  // [kStages] granules without a page
-  static_assert(sizeof(PagedStart) <= 32 && 40 + 4 * C::kStages <= 80, "");
+  PagedStart *at = reinterpret_cast<PagedStart *>(misc + 8);                  // 48 bytes
+  volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 56);  // [kStages] granules without a page
+  static_assert(sizeof(PagedStart) <= 48 && 56 + 4 * C::kStages <= 96, "");
   float2 *s_ml = reinterpret_cast<float2 *>(smem + C::kOffML);
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -861,13 +882,12 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
   }
-  grid_go();
   grid_wait();
-  const PagedStretch stretch =
-      block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), at);
+  grid_go();  // only now: the join reads the call's inputs without a wait of its own
+  if (p.g.B > kWarpSeqs) block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), at);
   __syncthreads();
   PagedWalk walk;
-  walk.start(p, stretch, *at);
+  walk.start(p, p.g.B > kWarpSeqs ? *at : warp_stretch(p));
   bool ok = true;
 
   if (warp < W) {
@@ -1221,12 +1241,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
   const int row = (rt - rg * p.QT) * rows + (i - rt * p.TB) * GG + hg;
   const int item = group * groups + rg, all = p.QT * rows;
   grid_go();
+  long long u0 = 0, total = 0;
+  if (p.g.B <= kWarpSeqs) {
+    PagedSeq x = {0, 0, 0, 0};
+    if (lane < p.g.B) x = paged_seq(p, lane);
+    const long long x_units = units_of(p, x), sum = warp_scan(x_units);
+    u0 = __shfl_sync(0xffffffffu, sum - x_units, b);
+    total = __shfl_sync(0xffffffffu, sum, 31);
+  }
   grid_wait();
   int parts = 0, c0 = 0;
   long long first = 0;
   if (mine) {
-    const long long u0 = p.prefix[b] + (long long)item * (tiles + p.lead);
-    const long long per = stretch_units(p, p.prefix[p.g.B], blocks);
+    if (p.g.B > kWarpSeqs) {
+      u0 = p.prefix[b];
+      total = p.prefix[p.g.B];
+    }
+    u0 += (long long)item * (tiles + p.lead);
+    const long long per = stretch_units(p, total, blocks);
     c0 = (int)quot(u0 + p.lead, per);
     parts = (int)quot(u0 + p.lead + tiles - 1, per) - c0 + 1;
     // only the first block can have had tiles of another item before this one's: it begins before this

@@ -375,6 +375,35 @@ def test_captured_step_replays_on_other_contents():
     assert lens.tolist() == [61, 28, 321]
 
 
+@pytest.mark.parametrize("new,H,Hkv,d", [(1, 8, 4, 128), (30, 8, 2, 128), (70, 4, 2, 64)])
+def test_lengths_of_one_call_feed_the_next_at_once(new, H, Hkv, d):
+    """cache_compact's lengths go straight into the attention while the moves of many layers still run:
+    each kernel may start early but must not read what the one before it has yet to write."""
+    page, B, layers = 16, 24, 48
+    s = pm.Setup([120] * B, [new] * B, page, Hkv, d, seed=new, H=H)
+    deep = s.k_pages[None].repeat(layers, 1, 1, 1, 1), s.v_pages[None].repeat(layers, 1, 1, 1, 1)
+    base = i32([10 + b for b in range(B)])
+    paths = i32([list(range(40))] * B)
+    counts = [i32([(7 * b + 13 * r) % 41 for b in range(B)]) for r in range(6)]
+
+    def step(kept, wait):
+        lens = fa.cache_compact(*deep, s.t_table, base, paths, kept)
+        if wait:
+            torch.cuda.synchronize()
+        o, lse = fa.attention_fwd_paged(s.q, s.k_pages, s.v_pages, s.t_table, lens, s.t_cu, new)
+        if wait:
+            torch.cuda.synchronize()
+        return lens, o, lse
+
+    want = [step(c, True) for c in counts]
+    for _ in range(20):
+        for c, w in zip(counts, want):
+            got = step(c, False)
+            assert all(torch.equal(x, y) for x, y in zip(got, w))
+        got = [step(c, False) for c in counts]
+        assert all(torch.equal(x, y) for g, w in zip(got, want) for x, y in zip(g, w))
+
+
 def test_calls_on_a_given_stream_and_two_at_once():
     s = [pm.Setup([700, 33], [9, 20], 32, 2, 128, seed=20 + i, H=8) for i in range(2)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
