@@ -790,10 +790,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   }
 }
 
-
 // ------------------------------------------------------------------ few rows
-// All rows of a kv head (new tokens x G heads) in one or two 16-row fragments:
-// a decoding step, a short chain.  The cache is read once and each byte of it
+// All rows of a kv head (new tokens x G heads) in one 16-row fragment: a decoding
+// step, a short chain.  The cache is read once and each byte of it
 // meets few multiplications, so HBM is the bound and the work around the tiles is
 // what has to be small.  mma.sync.m16n8k16 fits: a warp takes 16 places of a
 // tile through S, softmax and P V in its own registers (running maximum, sum and O
@@ -805,20 +804,20 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 // A head's row is only 128 to 512 bytes of the cache; fetching adjacent heads
 // together keeps DRAM pages and 256-byte L2 lines whole, and with HB = 4 each warp
 // has a head to itself and nothing to join.
-template <int D, int MT>
+template <int D>
 struct FewCfg {
   static constexpr int kWarps = 4, kBoxes = D / 64;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kTileBytes = 16 * kWarps * D * 2;  // K or V of a tile
-  static constexpr int kMinBlocks = D * MT <= 128 ? 2 : 1;
+  static constexpr int kMinBlocks = D <= 128 ? 2 : 1;
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
-  static constexpr int kJoinBytes = (kWarps / 2) * 16 * MT * D * 4;
+  static constexpr int kJoinBytes = (kWarps / 2) * 16 * D * 4;
   static constexpr int kStages = (kSmemMax - 1024 - 1024 - kJoinBytes) / (2 * kTileBytes);
   static_assert(kStages >= 2, "ring");
   static constexpr int kOffRing = 0, kOffJoin = 2 * kStages * kTileBytes, kOffBar = kOffJoin + kJoinBytes;
   static constexpr int kOffMisc = kOffBar + 16 * kStages;
-  static constexpr int kOffML = kOffMisc + 96;  // [kWarps][16 * MT] float2
-  static constexpr int kOffSums = kOffML + kWarps * 16 * MT * 8;
+  static constexpr int kOffML = kOffMisc + 96;  // [kWarps][16] float2
+  static constexpr int kOffSums = kOffML + kWarps * 16 * 8;
   static constexpr int kSmemBytes = kOffSums + 8 * (kWarps + 1) + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
 };
@@ -848,10 +847,10 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
 
 enum FewSite : int { kFSiteFull = 41, kFSiteEmpty = 42 };
 
-template <int D, int MT>
-__global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBlocks)
+template <int D>
+__global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
     paged_few_kernel(const __grid_constant__ PagedParams p) {
-  using C = FewCfg<D, MT>;
+  using C = FewCfg<D>;
   constexpr int W = C::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -898,34 +897,29 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
     while (walk.next(p)) {
       ++item;
       const int nt = walk.j1 - walk.j0, rows = walk.s.n * p.G, kh = walk.kh * p.HB + hb;
-      // this thread's rows: 16 m + q4 and + 8
-      uint32_t qf[MT][D / 16][4];
-      int tok[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
+      // this thread's rows: q4 and q4 + 8
+      uint32_t qf[D / 16][4];
+      int tok[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int r = 16 * m + 8 * hf + q4;
-          tok[m][hf] = r / p.G;
+          const int r = 8 * hf + q4;
+          tok[hf] = r / p.G;
           const uint32_t *qr = reinterpret_cast<const uint32_t *>(
-              p.q + ((size_t)(walk.s.start + tok[m][hf]) * p.H + kh * p.G + (r - tok[m][hf] * p.G)) * D);
+              p.q + ((size_t)(walk.s.start + tok[hf]) * p.H + kh * p.G + (r - tok[hf] * p.G)) * D);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            qf[m][k][hf] = r < rows ? qr[8 * k + (lane & 3)] : 0u;
-            qf[m][k][hf + 2] = r < rows ? qr[8 * k + 4 + (lane & 3)] : 0u;
+            qf[k][hf] = r < rows ? qr[8 * k + (lane & 3)] : 0u;
+            qf[k][hf + 2] = r < rows ? qr[8 * k + 4 + (lane & 3)] : 0u;
           }
         }
-      auto words = [&](int m, int hf) {
-        return p.mask && 16 * m + 8 * hf + q4 < rows ? p.mask + (size_t)(walk.s.start + tok[m][hf]) * p.words : nullptr;
+      auto words = [&](int hf) {
+        return p.mask && 8 * hf + q4 < rows ? p.mask + (size_t)(walk.s.start + tok[hf]) * p.words : nullptr;
       };
-      float o[MT][D / 8][4], m_ref[MT][2], l_sum[MT][2];
+      float o[D / 8][4], m_ref[2], l_sum[2];
+      m_ref[0] = m_ref[1] = -INFINITY;
+      l_sum[0] = l_sum[1] = 0.f;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        m_ref[m][0] = m_ref[m][1] = -INFINITY;
-        l_sum[m][0] = l_sum[m][1] = 0.f;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
-      }
+      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
       bool cleared = false;
       for (int j = 0; j < nt; ++j, ++fill) {
         const int slot = fill % C::kStages;
@@ -934,70 +928,62 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
         if (ok && kv0 < walk.s.keys && !((bad[slot] >> sub) & 1)) {
           const uint32_t kt = sbase + C::kOffRing + 2 * slot * C::kTileBytes + hb * head_bytes + 16 * sub * 128;
           const uint32_t vt = kt + C::kTileBytes;
-          float s[MT][2][4] = {};
+          float s[2][4] = {};
           {
             const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               uint32_t kf[4];
               ldsm4(kf, kt + (k >> 2) * box_bytes + key * 128 + (((2 * (k & 3) + half) ^ (key & 7)) << 4));
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816(s[m][0], qf[m][k], kf[0], kf[1]);
-                mma16816(s[m][1], qf[m][k], kf[2], kf[3]);
-              }
+              mma16816(s[0], qf[k], kf[0], kf[1]);
+              mma16816(s[1], qf[k], kf[2], kf[3]);
             }
           }
           const bool tail = kv0 + 16 > walk.s.len;
           if (tail) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int hf = 0; hf < 2; ++hf) {
+              const int pre = walk.s.len - kv0;
+              const unsigned see = (pre <= 0 ? 0u : (1u << pre) - 1u) |
+                                   seen_bits(words(hf), tok[hf], walk.s.keys - walk.s.len, kv0 - walk.s.len);
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int pre = walk.s.len - kv0;
-                const unsigned see = (pre <= 0 ? 0u : (1u << pre) - 1u) |
-                                     seen_bits(words(m, hf), tok[m][hf], walk.s.keys - walk.s.len, kv0 - walk.s.len);
+              for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (!((see >> (8 * n + c4 + e)) & 1)) s[m][n][2 * hf + e] = -INFINITY;
-              }
-          }
-          uint32_t pf[MT][4];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float top[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-              top[hf] = fmaxf(fmaxf(s[m][0][2 * hf], s[m][0][2 * hf + 1]), fmaxf(s[m][1][2 * hf], s[m][1][2 * hf + 1])) * c2;
-            // the maximum moves only where a score is more than kRescaleTau above it (at first: above -inf)
-            if (__any_sync(0xffffffffu, top[0] - m_ref[m][0] > kRescaleTau || top[1] - m_ref[m][1] > kRescaleTau)) {
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                float t = top[hf];
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                t = fmaxf(t, m_ref[m][hf]);
-                const float alpha = t == m_ref[m][hf] ? 1.f : ex2_mufu(m_ref[m][hf] - t);
-                m_ref[m][hf] = t;
-                l_sum[m][hf] *= alpha;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                  o[m][n][2 * hf] *= alpha;
-                  o[m][n][2 * hf + 1] *= alpha;
-                }
-              }
+                for (int e = 0; e < 2; ++e)
+                  if (!((see >> (8 * n + c4 + e)) & 1)) s[n][2 * hf + e] = -INFINITY;
             }
+          }
+          uint32_t pf[4];
+          float top[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            top[hf] = fmaxf(fmaxf(s[0][2 * hf], s[0][2 * hf + 1]), fmaxf(s[1][2 * hf], s[1][2 * hf + 1])) * c2;
+          // the maximum moves only where a score is more than kRescaleTau above it (at first: above -inf)
+          if (__any_sync(0xffffffffu, top[0] - m_ref[0] > kRescaleTau || top[1] - m_ref[1] > kRescaleTau)) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const float neg = m_ref[m][hf] == -INFINITY ? 0.f : -m_ref[m][hf];
+              float t = top[hf];
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+              t = fmaxf(t, m_ref[hf]);
+              const float alpha = t == m_ref[hf] ? 1.f : ex2_mufu(m_ref[hf] - t);
+              m_ref[hf] = t;
+              l_sum[hf] *= alpha;
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                const float e0 = ex2_mufu(fmaf(s[m][n][2 * hf], c2, neg)), e1 = ex2_mufu(fmaf(s[m][n][2 * hf + 1], c2, neg));
-                l_sum[m][hf] += e0 + e1;
-                pf[m][2 * n + hf] = pack_bf16x2(e0, e1);
+              for (int n = 0; n < D / 8; ++n) {
+                o[n][2 * hf] *= alpha;
+                o[n][2 * hf + 1] *= alpha;
               }
+            }
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float neg = m_ref[hf] == -INFINITY ? 0.f : -m_ref[hf];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float e0 = ex2_mufu(fmaf(s[n][2 * hf], c2, neg)), e1 = ex2_mufu(fmaf(s[n][2 * hf + 1], c2, neg));
+              l_sum[hf] += e0 + e1;
+              pf[2 * n + hf] = pack_bf16x2(e0, e1);
             }
           }
           const int key = lane & 15, part = lane >> 4;
@@ -1006,11 +992,8 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
             for (int n = 0; n < D / 16; ++n) {
               uint32_t vf[4];
               ldsm4_t(vf, vt + (n >> 2) * box_bytes + key * 128 + (((2 * (n & 3) + part) ^ (key & 7)) << 4));
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816(o[m][2 * n], pf[m], vf[0], vf[1]);
-                mma16816(o[m][2 * n + 1], pf[m], vf[2], vf[3]);
-              }
+              mma16816(o[2 * n], pf, vf[0], vf[1]);
+              mma16816(o[2 * n + 1], pf, vf[2], vf[3]);
             }
           } else {
             // Values that not every row sees: past the end they hold anything, and 0 * NaN is NaN; among
@@ -1035,81 +1018,68 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
               vf[1] = cut(vf[1], 8);
               vf[2] = cut(vf[2], 0);
               vf[3] = cut(vf[3], 8);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816(o[m][2 * n], pf[m], vf[0], vf[1]);
-                mma16816(o[m][2 * n + 1], pf[m], vf[2], vf[3]);
-              }
+              mma16816(o[2 * n], pf, vf[0], vf[1]);
+              mma16816(o[2 * n + 1], pf, vf[2], vf[3]);
             }
           }
         }
         if (!(FA_STALL(5) && fill == 0 && warp == 0)) mbar_arrive_warp(empty_bar(slot));
       }
-      float row_l[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
+      float row_l[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float l = l_sum[m][hf];
+          float l = l_sum[hf];
           l += __shfl_xor_sync(0xffffffffu, l, 1);
           l += __shfl_xor_sync(0xffffffffu, l, 2);
-          row_l[m][hf] = l;  // m_ref is the row's already: its lanes moved it together
+          row_l[hf] = l;  // m_ref is the row's already: its lanes moved it together
         }
       bool is_odd = __any_sync(0xffffffffu, cleared);
       if (sharers > 1) {
         // ----------------------------------------------------- join the warps of a kv head
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
           for (int hf = 0; hf < 2; ++hf)
             if ((lane & 3) == 0)
-              s_ml[warp * 16 * MT + 16 * m + 8 * hf + q4] = make_float2(m_ref[m][hf], row_l[m][hf]);
+              s_ml[warp * 16 + 8 * hf + q4] = make_float2(m_ref[hf], row_l[hf]);
         if (is_odd && lane == 0) *odd = item;
         named_bar_sync(1, 32 * W);
         is_odd = *odd == item;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float2 *ml = s_ml + hb * sharers * 16 * MT + 16 * m + 8 * hf + q4;
+            const float2 *ml = s_ml + hb * sharers * 16 + 8 * hf + q4;
             float top = -INFINITY, l = 0.f;
-            for (int w = 0; w < sharers; ++w) top = fmaxf(top, ml[w * 16 * MT].x);
+            for (int w = 0; w < sharers; ++w) top = fmaxf(top, ml[w * 16].x);
             const float base = top == -INFINITY ? 0.f : top;
             for (int w = 0; w < sharers; ++w) {
-              const float2 x = ml[w * 16 * MT];
+              const float2 x = ml[w * 16];
               l += x.y * ex2_mufu(x.x - base);
             }
-            const float a = ex2_mufu(m_ref[m][hf] - base);
-            m_ref[m][hf] = top;
-            row_l[m][hf] = l;
+            const float a = ex2_mufu(m_ref[hf] - base);
+            m_ref[hf] = top;
+            row_l[hf] = l;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-              o[m][n][2 * hf] *= a;
-              o[m][n][2 * hf + 1] *= a;
+              o[n][2 * hf] *= a;
+              o[n][2 * hf + 1] *= a;
             }
           }
-        float4 *join = reinterpret_cast<float4 *>(smem + C::kOffJoin);  // [W / 2][MT * D / 8][32 lanes]
+        float4 *join = reinterpret_cast<float4 *>(smem + C::kOffJoin);  // [W / 2][D / 8][32 lanes]
         for (int step = sharers / 2; step >= 1; step >>= 1) {
           if (sub >= step && sub < 2 * step) {
-            float4 *to = join + (hb * step + sub - step) * MT * (D / 8) * 32 + lane;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
+            float4 *to = join + (hb * step + sub - step) * (D / 8) * 32 + lane;
 #pragma unroll
               for (int n = 0; n < D / 8; ++n)
-                to[(m * (D / 8) + n) * 32] = make_float4(o[m][n][0], o[m][n][1], o[m][n][2], o[m][n][3]);
+                to[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
           }
           named_bar_sync(1, 32 * W);
           if (sub < step) {
-            const float4 *from = join + (hb * step + sub) * MT * (D / 8) * 32 + lane;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
+            const float4 *from = join + (hb * step + sub) * (D / 8) * 32 + lane;
 #pragma unroll
               for (int n = 0; n < D / 8; ++n) {
-                const float4 x = from[(m * (D / 8) + n) * 32];
-                o[m][n][0] += x.x;
-                o[m][n][1] += x.y;
-                o[m][n][2] += x.z;
-                o[m][n][3] += x.w;
+                const float4 x = from[n * 32];
+                o[n][0] += x.x;
+                o[n][1] += x.y;
+                o[n][2] += x.z;
+                o[n][3] += x.w;
               }
           }
           named_bar_sync(1, 32 * W);
@@ -1118,43 +1088,39 @@ __global__ void __launch_bounds__(FewCfg<D, MT>::kThreads, FewCfg<D, MT>::kMinBl
       if (sub == 0 && ok) {
         if (is_odd) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int n = 0; n < D / 8; ++n) {
-                if (16 * m + 8 * hf + q4 >= rows) continue;
+                if (8 * hf + q4 >= rows) continue;
                 float add[2];
-                add_unfinite(p, walk.s, walk.b, kh, words(m, hf), tok[m][hf], walk.j0 * bn, walk.j1 * bn, D, 8 * n + c4, 2, add);
-                o[m][n][2 * hf] += add[0];
-                o[m][n][2 * hf + 1] += add[1];
+                add_unfinite(p, walk.s, walk.b, kh, words(hf), tok[hf], walk.j0 * bn, walk.j1 * bn, D, 8 * n + c4, 2, add);
+                o[n][2 * hf] += add[0];
+                o[n][2 * hf + 1] += add[1];
               }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const int r = 16 * m + 8 * hf + q4;
+            const int r = 8 * hf + q4;
             if (r >= rows) continue;
-            const float l = row_l[m][hf];
+            const float l = row_l[hf];
             if (walk.whole) {
-              const int h = kh * p.G + (r - tok[m][hf] * p.G);
-              const size_t q_row = (size_t)walk.s.start + tok[m][hf];
+              const int h = kh * p.G + (r - tok[hf] * p.G);
+              const size_t q_row = (size_t)walk.s.start + tok[hf];
               const float inv = l == 0.f ? 0.f : 1.0f / l;
               uint32_t *to = reinterpret_cast<uint32_t *>(p.o + (q_row * p.H + h) * D + c4);
 #pragma unroll
-              for (int n = 0; n < D / 8; ++n) to[4 * n] = pack_bf16x2(o[m][n][2 * hf] * inv, o[m][n][2 * hf + 1] * inv);
-              if ((lane & 3) == 0 && p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[m][hf] + __log2f(l)) * 0.69314718055994531f;
+              for (int n = 0; n < D / 8; ++n) to[4 * n] = pack_bf16x2(o[n][2 * hf] * inv, o[n][2 * hf + 1] * inv);
+              if ((lane & 3) == 0 && p.lse) p.lse[(size_t)h * p.total + q_row] = (m_ref[hf] + __log2f(l)) * 0.69314718055994531f;
             } else {
-              const int GG = p.HB * p.G, all = p.TB * GG, row = tok[m][hf] * GG + hb * p.G + (r - tok[m][hf] * p.G);
+              const int GG = p.HB * p.G, all = p.TB * GG, row = tok[hf] * GG + hb * p.G + (r - tok[hf] * p.G);
               const size_t slot = ((size_t)blockIdx.x * 2 + (walk.first ? 0 : 1)) * all;
               float *to = p.part_o + slot * D + c4 * all + row;
 #pragma unroll
               for (int n = 0; n < D / 8; ++n, to += 8 * all) {
-                to[0] = o[m][n][2 * hf];
-                to[all] = o[m][n][2 * hf + 1];
+                to[0] = o[n][2 * hf];
+                to[all] = o[n][2 * hf + 1];
               }
-              if ((lane & 3) == 0) p.part_ml[slot + row] = make_float2(m_ref[m][hf], l);
+              if ((lane & 3) == 0) p.part_ml[slot + row] = make_float2(m_ref[hf], l);
             }
           }
       }
@@ -1345,7 +1311,7 @@ constexpr int kSMs = 152;
 constexpr int tile_keys(int QT) { return QT == 2 ? 128 : 64; }
 
 struct PagedPlan {
-  int MT;  // 16-row fragments of the few-rows kernel, 0: the tcgen05 kernel
+  bool few;  // the few-rows kernel, else the tcgen05 kernel
   int QT, HB, bn, TB, blocks;
   size_t part_o, part_ml, prefix, bytes;
 };
@@ -1353,12 +1319,14 @@ struct PagedPlan {
 PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
   PagedPlan w;
   const int rows = max_new * G;
-  w.MT = rows <= 16 ? 1 : 0;
+  // One 16-row fragment.  (Two of them, at dims 64 and 128, were 40 % slower on 16 x 8000 places at 32 rows than
+  // the tcgen05 kernel at dim 128, and 30 % at dim 64.)
+  w.few = rows <= 16;
   w.TB = 128 / G < max_new ? 128 / G : max_new;
   w.QT = max_new > w.TB && d <= 128 ? 2 : 1;
-  w.HB = !w.MT ? 1 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-  w.bn = w.MT ? 64 / w.HB : tile_keys(w.QT);
-  w.blocks = kSMs * (w.MT ? (d * w.MT <= 128 ? 2 : 1) : (w.QT == 1 && d <= 128 ? 2 : 1));
+  w.HB = !w.few ? 1 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+  w.bn = w.few ? 64 / w.HB : tile_keys(w.QT);
+  w.blocks = kSMs * (w.few ? (d <= 128 ? 2 : 1) : (w.QT == 1 && d <= 128 ? 2 : 1));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)2 * w.blocks * w.HB * w.QT * w.TB * G;
   w.part_o = 0;
@@ -1403,11 +1371,11 @@ int launch_paged(PagedParams &p, int blocks, const void *q, const void *k_pages,
                     stream);
 }
 
-template <int D, int MT>
+template <int D>
 int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pages, cudaStream_t stream) {
-  using C = FewCfg<D, MT>;
+  using C = FewCfg<D>;
   if (page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D, MT>, paged_combine_kernel<D>,
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D>, paged_combine_kernel<D>,
                     stream);
 }
 
@@ -1475,10 +1443,10 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.TB = w.TB;
   p.bn_log2 = w.bn == 128 ? 7 : w.bn == 64 ? 6 : w.bn == 32 ? 5 : 4;
   p.heads = Hkv / w.HB;
-  p.min_units = w.MT ? 2 : 1;
+  p.min_units = w.few ? 2 : 1;
   // Measured, in microseconds of tiles, against none: 48 ragged sequences of drafted trees 54 (63), at head
   // dim 64 44 (74), at head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).
-  p.lead = w.MT ? 2 : w.QT == 2 ? 4 : 3;
+  p.lead = w.few ? 2 : w.QT == 2 ? 4 : 3;
   // parts an item is cut into on average, two a warp and four in flight
   const long long items = (long long)B * p.heads * (w.TB * w.QT >= max_new ? 1 : (max_new + w.TB * w.QT - 1) / (w.TB * w.QT));
   p.join = w.blocks / items >= 16 ? 8 : w.blocks / items >= 8 ? 4 : 1;
@@ -1486,10 +1454,10 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.HB = w.HB;
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (w.MT == 1) {
-    if (d == 64) return launch_few<64, 1>(p, w.blocks, k_pages, v_pages, s);
-    if (d == 128) return launch_few<128, 1>(p, w.blocks, k_pages, v_pages, s);
-    return launch_few<256, 1>(p, w.blocks, k_pages, v_pages, s);
+  if (w.few) {
+    if (d == 64) return launch_few<64>(p, w.blocks, k_pages, v_pages, s);
+    if (d == 128) return launch_few<128>(p, w.blocks, k_pages, v_pages, s);
+    return launch_few<256>(p, w.blocks, k_pages, v_pages, s);
   }
   if (d == 64)
     return w.QT == 2 ? launch_paged<64, tile_keys(2), 2>(p, w.blocks, q, k_pages, v_pages, s)

@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -84,6 +85,16 @@ struct Cache {
   }
 };
 
+// A call's workspace, from torch's allocator on the current stream: given back when
+// the call has been enqueued, reused only by later work on that stream.
+struct Workspace {
+  const size_t bytes;
+  void *const p;
+  explicit Workspace(size_t n) : bytes(n), p(c10::cuda::CUDACachingAllocator::raw_alloc(n ? n : 1)) {}
+  ~Workspace() { c10::cuda::CUDACachingAllocator::raw_delete(p); }
+  Workspace(const Workspace &) = delete;
+};
+
 PyObject *status_or(int status, PyObject *result) {
   if (status == FA_OK) return result;
   Py_XDECREF(result);
@@ -127,12 +138,11 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   at::Tensor out = at::empty(q->sizes(), device), lse = at::empty({H, total}, device.dtype(at::kFloat));
   int status = FA_OK;
   if (total > 0) {
-    const size_t bytes = g_paged_bytes(c.B, (int)max_new, H, c.Hkv, c.d);
-    at::Tensor workspace = at::empty({(int64_t)(bytes ? bytes : 1)}, device.dtype(at::kByte));
+    const Workspace workspace(g_paged_bytes(c.B, (int)max_new, H, c.Hkv, c.d));
     status = g_paged(q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens), ints(cu),
                      mask ? static_cast<const long long *>(mask->data_ptr()) : nullptr, mask ? words : 0, out.data_ptr(),
                      static_cast<float *>(lse.data_ptr()), c.B, c.max_pages, c.num_pages, c.page_size, (int)max_new, total, H,
-                     c.Hkv, c.d, scale, workspace.data_ptr(), bytes, o.stream());
+                     c.Hkv, c.d, scale, workspace.p, workspace.bytes, o.stream());
   }
   if (status != FA_OK) return PyLong_FromLong(status);
   PyObject *x = THPVariable_Wrap(std::move(out)), *y = THPVariable_Wrap(std::move(lse));
@@ -185,13 +195,11 @@ PyObject *resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const Cache c(o, a[1], a[2], a[3], a[4], true);
   const at::Tensor *refs = o.take(a[0], at::kInt, 1, 1), *want = o.take(a[5], at::kInt, 1, 1);
   if (!o.current() || refs->size(0) != c.num_pages || want->size(0) != c.B) Py_RETURN_NONE;
-  const auto opts = c.lens->options();
-  at::Tensor lens = at::empty({c.B}, opts), said = at::empty({2}, opts);
-  const size_t bytes = g_resize_bytes(c.B);
-  at::Tensor workspace = at::empty({(int64_t)(bytes ? bytes : 1)}, opts.dtype(at::kByte));
+  at::Tensor lens = at::empty({c.B}, c.lens->options()), said = at::empty({2}, c.lens->options());
+  const Workspace workspace(g_resize_bytes(c.B));
   const int status = g_resize(ints(refs), c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens), ints(want),
                               ints(&lens), ints(&said), c.B, c.max_pages, c.num_pages, c.page_size, c.layers, c.Hkv, c.d,
-                              workspace.data_ptr(), bytes, o.stream());
+                              workspace.p, workspace.bytes, o.stream());
   if (status != FA_OK) return PyLong_FromLong(status);
   PyObject *x = THPVariable_Wrap(std::move(lens)), *y = THPVariable_Wrap(std::move(said));
   PyObject *both = x && y ? PyTuple_Pack(2, x, y) : nullptr;
