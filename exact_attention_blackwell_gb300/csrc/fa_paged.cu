@@ -41,6 +41,7 @@ struct PagedParams {
   int heads;            // Hkv / HB
   int min_units;        // a block's stretch is no shorter
   int lead;             // units that stand for what an item costs beside its tiles
+  bool by_warp;         // up to 32 sequences, whose units fit 31 bits
   int join;             // warps that share a task of the join
   float scale_log2;
 };
@@ -89,7 +90,7 @@ FA_STALL_FLAG_DECL
 
 enum PagedSite : int {
   kPSiteQ = 31, kPSiteKFull = 32, kPSiteVFull = 33, kPSitePFull = 34, kPSiteEmpty = 35,
-  kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39
+  kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39, kPSiteVTail = 40
 };
 
 // Sequence b: its first new token, their number, places cached, places in all.
@@ -143,25 +144,43 @@ struct PagedStart {
   int b;
 };
 
-// Up to 32 sequences: every warp sums them up by itself, a lane each.
-constexpr int kWarpSeqs = 32;
-__device__ __forceinline__ PagedStart warp_stretch(const PagedParams &p) {
+// Up to 32 sequences whose units surely fit 31 bits (p.by_warp): every warp sums
+// them up by itself, a lane each.
+struct WarpUnits {
+  PagedSeq s;
+  unsigned before, after, total;
+};
+__device__ __forceinline__ WarpUnits warp_units(const PagedParams &p) {
   const int lane = threadIdx.x & 31;
-  PagedSeq s = {0, 0, 0, 0};
-  if (lane < p.g.B) s = paged_seq(p, lane);
-  const long long x = units_of(p, s), sum = warp_scan(x), total = __shfl_sync(0xffffffffu, sum, 31);
-  const long long per = stretch_units(p, total, gridDim.x);
+  WarpUnits w;
+  w.s = {0, 0, 0, 0};
+  if (lane < p.g.B) w.s = paged_seq(p, lane);
+  const unsigned x = (unsigned)units_of(p, w.s);
+  w.after = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, w.after, o);
+    if (lane >= o) w.after += y;
+  }
+  w.before = w.after - x;
+  w.total = __shfl_sync(0xffffffffu, w.after, 31);
+  return w;
+}
+__device__ __forceinline__ PagedStart warp_stretch(const PagedParams &p) {
+  const WarpUnits w = warp_units(p);
+  const unsigned per = max((w.total + gridDim.x - 1) / gridDim.x, (unsigned)p.min_units);
+  const unsigned begin = min(per * blockIdx.x, w.total);  // per * blocks < total + 2 * blocks
+  const unsigned here = __ballot_sync(0xffffffffu, begin >= w.before && begin < w.after);
   PagedStart r;
-  r.begin = min(per * blockIdx.x, total);
-  r.end = min(r.begin + per, total);
-  const unsigned here = __ballot_sync(0xffffffffu, r.begin >= sum - x && r.begin < sum);
-  const int b = __ffs(here) - 1, from = max(b, 0);
-  r.base = __shfl_sync(0xffffffffu, sum - x, from);
-  r.s.start = __shfl_sync(0xffffffffu, s.start, from);
-  r.s.n = __shfl_sync(0xffffffffu, s.n, from);
-  r.s.len = __shfl_sync(0xffffffffu, s.len, from);
-  r.s.keys = __shfl_sync(0xffffffffu, s.keys, from);
-  r.b = b;
+  r.b = __ffs(here) - 1;
+  const int from = max(r.b, 0);
+  r.begin = begin;
+  r.end = min(begin + per, w.total);
+  r.base = __shfl_sync(0xffffffffu, w.before, from);
+  r.s.start = __shfl_sync(0xffffffffu, w.s.start, from);
+  r.s.n = __shfl_sync(0xffffffffu, w.s.n, from);
+  r.s.len = __shfl_sync(0xffffffffu, w.s.len, from);
+  r.s.keys = __shfl_sync(0xffffffffu, w.s.keys, from);
   return r;
 }
 
@@ -291,33 +310,36 @@ __device__ __forceinline__ unsigned seen_bits(const unsigned long long *words, i
   return bits;
 }
 
+// bf16 pairs: infinities and NaNs made zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
 // The V rows of a tile that not every row of S sees.  Past the sequence's end
 // they hold anything, and 0 * NaN is NaN: cleared.  Among the new tokens
 // non-finite values are cleared too, and the epilogue adds them to the rows that
-// see them.  By the whole MMA warp, before the tile's P V; returns whether a new
-// token's value was cleared.  Rows from the last page's end on are zeros already.
+// see them.  By the 128 threads of row tile 0's softmax, before they hand over the
+// tile's first P (which the MMA warp takes before any other row tile's); returns
+// whether this warp cleared a new token's value.  Rows from the last page's end on
+// are zeros already.
 template <int D, int BN>
 __device__ __forceinline__ bool clear_unseen(uint8_t *tile, const PagedSeq &s, int kv0, int page_size) {
   const int r0 = max(s.len - kv0, 0), r1 = min((s.keys + page_size - 1) / page_size * page_size - kv0, BN);
-  const int lane = threadIdx.x & 31, chunk = lane & 7;
+  const int chunk = threadIdx.x & 7;
   bool any = false;
 #pragma unroll 1
   for (int bx = 0; bx < D / 64; ++bx) {
-#pragma unroll 4
-    for (int r = r0 + (lane >> 3); r < r1; r += 4) {
+#pragma unroll 2
+    for (int r = r0 + ((threadIdx.x & 127) >> 3); r < r1; r += 16) {
       uint4 *at = reinterpret_cast<uint4 *>(tile + bx * (BN * 128) + r * 128 + ((chunk ^ (r & 7)) * 16));
       if (kv0 + r >= s.keys) {
         *at = make_uint4(0, 0, 0, 0);
         continue;
       }
-      uint4 x = *at;
-      const uint4 was = x;
-      auto keep = [](uint32_t w) {
-        if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-        if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-        return w;
-      };
-      x = make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
+      const uint4 was = *at;
+      const uint4 x = make_uint4(finite_pair(was.x), finite_pair(was.y), finite_pair(was.z), finite_pair(was.w));
       if (x.x != was.x || x.y != was.y || x.z != was.z || x.w != was.w) {
         *at = x;
         any = true;
@@ -369,6 +391,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
   PagedStart *at = reinterpret_cast<PagedStart *>(misc + 192);  // 48 bytes
   volatile int *odd = reinterpret_cast<volatile int *>(misc + 248);  // [QT] the last item with cleared V values
+  volatile int *tail_hit = reinterpret_cast<volatile int *>(misc + 244);  // the same, as row tile 0's softmax finds them
   volatile unsigned *bad = reinterpret_cast<volatile unsigned *>(misc + 32);  // [16] granules without a page, by tile
   long long *s_sums = reinterpret_cast<long long *>(misc + 96);               // [kThreads / 32] <= 11
   const WaitCtx wctx{abort_flag, p.status};
@@ -380,7 +403,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
       mbar_init(bar, bar >= p_bar(0, 0) && bar < pv_bar(0) ? 4u : 1u);
     }
     *abort_flag = 0;
-    odd[0] = odd[1] = 0;
+    odd[0] = odd[1] = *tail_hit = 0;
     at->b = -1;
     fence_mbar_init();
   }
@@ -395,13 +418,13 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   }
   grid_wait();
   grid_go();  // only now: the join reads the call's inputs without a wait of its own
-  if (p.g.B > kWarpSeqs) block_stretch<C::kThreads>(p, s_sums, at);
+  if (!p.by_warp) block_stretch<C::kThreads>(p, s_sums, at);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   PagedWalk walk;
-  walk.start(p, p.g.B > kWarpSeqs ? *at : warp_stretch(p));
+  walk.start(p, p.by_warp ? warp_stretch(p) : *at);
 
   auto tile_tokens = [&](int t) { return max(0, min(p.TB, walk.s.n - (walk.rg * QT + t) * p.TB)); };
 
@@ -528,6 +551,16 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             tmem_wait_st();
             tc_fence_before();
           }
+          if (t == 0 && (!C::kPair || buf == 0)) {
+            const int tile = C::kPair ? j >> 1 : j, first = (walk.j0 + tile) * BN;
+            if (first + BN > walk.s.len) {
+              const int fv = 2 * tiles + v_fill<C::kPair>(tile, nt), sv = fv % C::kStages;
+              ok = mbar_wait_warp(full_bar(sv), (fv / C::kStages) & 1, wctx, kPSiteVTail);
+              if (!ok) break;
+              if (clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, first, p.g.page_size) && lane == 0)
+                *tail_hit = item;
+            }
+          }
           if (!(FA_STALL(4) && tile_no == 0 && t == 0)) mbar_arrive_warp(p_bar(t, buf));
         }
         // ----------------------------------------------------- epilogue
@@ -652,10 +685,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         const int fv = fill + v_fill<C::kPair>(j, nt), sv = slot_of(fv);
         ok = mbar_wait_warp(full_bar(sv), par_of(fv), wctx, kPSiteVFull);
         if (!ok) break;
-        const int kv0 = (walk.j0 + j) * BN;
         bool cleared = false;
-        if (kv0 + BN > walk.s.len)
-          cleared = clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, kv0, p.g.page_size);
         int sk = -1;
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
@@ -664,7 +694,9 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
           ok = mbar_wait_warp(p_bar(t, buf), par, wctx, kPSitePFull);
           if (!ok) break;
           tc_fence_after();
-          // this row tile's warps have left the epilogue of every earlier item
+          // Row tile 0's warps have cleared what they had to; this one's have left the epilogue of every
+          // earlier item.
+          if (t == 0) cleared = *tail_hit == seg;
           if (cleared && lane == 0) odd[t] = seg;
           __syncwarp();
           if (elect_one()) {
@@ -838,13 +870,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// bf16 pairs: infinities and NaNs made zero.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
-}
-
 enum FewSite : int { kFSiteFull = 41, kFSiteEmpty = 42 };
 
 template <int D>
@@ -883,10 +908,10 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
   }
   grid_wait();
   grid_go();  // only now: the join reads the call's inputs without a wait of its own
-  if (p.g.B > kWarpSeqs) block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), at);
+  if (!p.by_warp) block_stretch<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffSums), at);
   __syncthreads();
   PagedWalk walk;
-  walk.start(p, p.g.B > kWarpSeqs ? *at : warp_stretch(p));
+  walk.start(p, p.by_warp ? warp_stretch(p) : *at);
   bool ok = true;
 
   if (warp < W) {
@@ -1208,18 +1233,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
   const int item = group * groups + rg, all = p.QT * rows;
   grid_go();
   long long u0 = 0, total = 0;
-  if (p.g.B <= kWarpSeqs) {
-    PagedSeq x = {0, 0, 0, 0};
-    if (lane < p.g.B) x = paged_seq(p, lane);
-    const long long x_units = units_of(p, x), sum = warp_scan(x_units);
-    u0 = __shfl_sync(0xffffffffu, sum - x_units, b);
-    total = __shfl_sync(0xffffffffu, sum, 31);
+  if (p.by_warp) {
+    const WarpUnits w = warp_units(p);
+    u0 = __shfl_sync(0xffffffffu, w.before, b);
+    total = w.total;
   }
   grid_wait();
   int parts = 0, c0 = 0;
   long long first = 0;
   if (mine) {
-    if (p.g.B > kWarpSeqs) {
+    if (!p.by_warp) {
       u0 = p.prefix[b];
       total = p.prefix[p.g.B];
     }
@@ -1418,8 +1441,8 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   if (total == 0) return FA_OK;
   const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
   // the units of one sequence are counted in 31 bits
-  if (((double)max_pages * page_size / w.bn + 8) * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB) >= 2147483648.0)
-    return FA_ERR_UNSUPPORTED;
+  const double seq_units = ((double)max_pages * page_size / w.bn + 8) * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB);
+  if (seq_units >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1443,6 +1466,7 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.TB = w.TB;
   p.bn_log2 = w.bn == 128 ? 7 : w.bn == 64 ? 6 : w.bn == 32 ? 5 : 4;
   p.heads = Hkv / w.HB;
+  p.by_warp = B <= 32 && B * seq_units < 2147483648.0 - 4 * kSMs;
   p.min_units = w.few ? 2 : 1;
   // Measured, in microseconds of tiles, against none: 48 ragged sequences of drafted trees 54 (63), at head
   // dim 64 44 (74), at head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).

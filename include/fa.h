@@ -326,7 +326,7 @@ int fa_last_device_status(void *stream);
  * Q and dO tiles loaded; fused backward: 23 dQ partial computed, 24 S read
  * into registers, 25 dQ partial read out); paged attention 31-39 (31 Q tile
  * loaded, 32/33 K/V tile loaded, 34 P stored, 35 ring slot free, 36 S computed,
- * 37 O readable, 38 MMA drain, 39 Q tile free) and, with few rows, 41 K and V
+ * 37 O readable, 38 MMA drain, 39 Q tile free, 40 the last V tile loaded) and, with few rows, 41 K and V
  * tile loaded, 42 ring slot free.  Outputs of a call in which a wait
  * ran out are unspecified. */
 int fa_last_device_status_site(void *stream, int *site);
