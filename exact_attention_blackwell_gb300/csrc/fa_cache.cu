@@ -423,7 +423,7 @@ int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, 
   if (total == 0) return FA_OK;
   const PageGeom g{page_table, cache_lens, B, max_pages, num_pages, page_size};
   const unsigned grid = (unsigned)(((long long)total + 3) / 4);
-  return launch_after(cache_append_kernel, grid, 128, 0, static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k),
+  return launch_after(cache_append_kernel, grid, 1, 128, 0, static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k),
                       static_cast<const uint4 *>(v), static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g,
                       cu_seqlens, total, Hkv * d / 8);
 }
@@ -444,7 +444,7 @@ int fa_cache_compact(void *k_pages, void *v_pages, const int *page_table, const 
     if (!ptr_aligned(x, 4)) return FA_ERR_ALIGNMENT;
   if ((rc = check_device()) != FA_OK) return rc;
   const PageGeom g{page_table, cache_lens, B, max_pages, num_pages, page_size};
-  return launch_after(cache_compact_kernel, (long long)B * layers * 2, 128, 0, static_cast<cudaStream_t>(stream),
+  return launch_after(cache_compact_kernel, (long long)B * layers * 2, 1, 128, 0, static_cast<cudaStream_t>(stream),
                       static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g, accepted, n_accepted, lens_out,
                       max_accepted, layers, Hkv * d / 8);
 }
@@ -468,7 +468,7 @@ int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const 
     return FA_ERR_CUDA;
   const unsigned grid = (unsigned)((max_pages + cols - 1) / cols);
   const int threads = B * cols >= 1024 ? 1024 : (B * cols + 31) / 32 * 32;
-  return launch_after(cache_fork_kernel, grid, threads, smem, static_cast<cudaStream_t>(stream), page_refs, page_table,
+  return launch_after(cache_fork_kernel, grid, 1, threads, smem, static_cast<cudaStream_t>(stream), page_refs, page_table,
                       cache_lens, parents, lens_out, B, max_pages, num_pages, page_size, cols);
 }
 
@@ -496,10 +496,10 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
       cudaSuccess)
     return FA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_after(cache_resize_kernel, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table, cache_lens,
+  if ((rc = launch_after(cache_resize_kernel, 1, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table, cache_lens,
                          new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size)) != FA_OK)
     return rc;
-  return launch_after(cache_copy_kernel, 152 * 2, 256, 0, s, static_cast<uint4 *>(k_pages),
+  return launch_after(cache_copy_kernel, 152 * 2, 1, 256, 0, s, static_cast<uint4 *>(k_pages),
                       static_cast<uint4 *>(v_pages), (const int *)copies, num_pages, page_size, layers, Hkv * d / 8);
 }
 

@@ -149,9 +149,10 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
-int launch_after(void (*kernel)(P...), long long blocks, int threads, size_t smem, cudaStream_t stream, A... args) {
+int launch_after(void (*kernel)(P...), long long blocks, int blocks_y, int threads, size_t smem, cudaStream_t stream,
+                 A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)blocks_y);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -38,7 +38,7 @@ struct PagedParams {
   PageGeom g;
   int words, max_new, total, H, Hkv, G, TB;
   int bn_log2, QT, HB;  // places in a tile; row tiles and kv heads of an item
-  int heads;            // Hkv / HB
+  int heads, groups;    // Hkv / HB; row groups of max_new tokens
   int min_units;        // a block's stretch is no shorter
   int lead;             // units that stand for what an item costs beside its tiles
   bool by_warp;         // up to 32 sequences, whose units fit 31 bits
@@ -1196,122 +1196,128 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
   }
 }
 
-// Joins the parts of the items that were cut.  A task is eight columns of one row;
-// the p.join warps (1 to 8) that share 32 tasks take every join-th part each, four
-// of them in flight.  Parts are stored column by column, so that the rows of a row
-// tile (neighbouring tasks) are contiguous for the kernels' stores and the loads
-// here.  Everything that depends on the call's inputs alone is done before the wait
-// for the main kernel.
-constexpr int kJoinWarps = 8;
+// Joins the parts of the items that were cut.  Blocks go by (item, chunk); one
+// warp finds out where the item's parts are (before the wait for the main kernel as
+// far as the call's inputs tell), the others take it from there: the search for
+// every row by every thread was half of this kernel's time.  A task is COLS columns
+// of one row; with many parts (SHARED) p.join warps share 32 tasks and take every
+// join-th part each, U of them in flight.  Parts are stored column by column, so that neighbouring tasks are
+// contiguous for the kernels' stores and the loads here.
+constexpr int kJoinWarps = 8;  // at most; four unless all eight share their tasks
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
-  __shared__ float s_part[kJoinWarps][10][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % p.join;
-  const long long id = ((long long)blockIdx.x * (blockDim.x / 32 / p.join) + warp / p.join) * 32 + lane;
-  // neighbours: the rows of an item (token by token, its heads together)
-  const int GG = p.HB * p.G;
-  const long long r = quot(id, (long long)p.total * GG), tg = id - r * p.total * GG;
-  int tok = (int)quot(tg, GG);
-  const int cg = (int)(r % (D / 8)), group = (int)(r / (D / 8)), hg = (int)(tg - (long long)tok * GG);
-  bool mine = group < p.heads;
-  const int h = mine ? group * GG + hg : 0;
-  if (!mine) tok = 0;
-  int b = 0;
-  for (int hi = p.g.B; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (p.cu[mid] <= tok) b = mid;
-    else hi = mid;
-  }
+  constexpr int COLS = 8, U = 4;
+  __shared__ float s_part[SHARED ? kJoinWarps : 1][COLS + 2][32];
+  __shared__ unsigned s_u0, s_total;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int GG = p.HB * p.G, all = p.QT * p.TB * GG;
+  const int rg = (int)(blockIdx.x % p.groups), seq_kh = (int)(blockIdx.x / p.groups);
+  const int b = seq_kh / p.heads, kh = seq_kh - b * p.heads;
   const PagedSeq s = paged_seq(p, b);
-  const int i = tok - s.start;
-  mine = mine && i >= 0 && i < s.n;
+  const int tok0 = rg * p.QT * p.TB, rows = min(s.n - tok0, p.QT * p.TB) * GG;
   int tiles, groups;
   paged_units(p, s, tiles, groups);
-  const int rt = i / p.TB, rg = rt / p.QT, rows = p.TB * GG;
-  const int row = (rt - rg * p.QT) * rows + (i - rt * p.TB) * GG + hg;
-  const int item = group * groups + rg, all = p.QT * rows;
-  grid_go();
   long long u0 = 0, total = 0;
   if (p.by_warp) {
-    const WarpUnits w = warp_units(p);
-    u0 = __shfl_sync(0xffffffffu, w.before, b);
-    total = w.total;
-  }
-  grid_wait();
-  int parts = 0, c0 = 0;
-  long long first = 0;
-  if (mine) {
-    if (!p.by_warp) {
-      u0 = p.prefix[b];
-      total = p.prefix[p.g.B];
+    if (warp == 0) {
+      const WarpUnits w = warp_units(p);
+      if (lane == b) s_u0 = w.before;
+      if (lane == 0) s_total = w.total;
     }
-    u0 += (long long)item * (tiles + p.lead);
-    const long long per = stretch_units(p, total, blocks);
-    c0 = (int)quot(u0 + p.lead, per);
-    parts = (int)quot(u0 + p.lead + tiles - 1, per) - c0 + 1;
+    __syncthreads();
+    u0 = s_u0;
+    total = s_total;
+  }
+  // the item's parts: from the block with its first tile on
+  int c0 = 0, parts = 0;
+  long long first = 0;
+  auto find_parts = [&] {
+    const long long per = stretch_units(p, total, blocks), at = u0 + (long long)(kh * groups + rg) * (tiles + p.lead);
+    c0 = (int)quot(at + p.lead, per);
+    parts = (int)quot(at + p.lead + tiles - 1, per) - c0 + 1;
     // only the first block can have had tiles of another item before this one's: it begins before this
     // item's units (the ones before them are tiles), and this is its second part
-    first = (long long)c0 * 2 + (u0 > c0 * per ? 1 : 0);
-    mine = parts > 1;  // else one block had it all and has written the result
-    if (!mine) parts = 0;
+    first = (long long)c0 * 2 + (at > c0 * per ? 1 : 0);
+  };
+  if (p.by_warp && rows > 0) find_parts();
+  grid_go();
+  grid_wait();
+  if (rows <= 0) return;  // no such row group
+  if (!p.by_warp) {
+    u0 = p.prefix[b];
+    total = p.prefix[p.g.B];
+    find_parts();
   }
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  for (int k0 = share; k0 < parts; k0 += 4 * p.join) {
-    float2 ml[4];
-    float x[4][8];
+  if (parts == 1) return;  // one block had it all and has written the result
+  const int share = warp % p.join, tasks = rows * (D / COLS), step = (int)blockDim.x / p.join;
+  for (int base = blockIdx.y * step; base < tasks; base += gridDim.y * step) {
+    const int task = base + warp / p.join * 32 + lane;
+    const int cg = task / rows, row = task - cg * rows;
+    const bool mine = task < tasks;
+    float m = -INFINITY, l = 0.f, acc[COLS] = {};
+    for (int k0 = share; k0 < parts && mine; k0 += U * p.join) {
+      float2 ml[U];
+      float x[U][COLS];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u * p.join;
-      ml[u] = make_float2(-INFINITY, 0.f);
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * p.join;
+        ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-      if (k < parts) {
-        const size_t at = (size_t)(k == 0 ? first : (long long)(c0 + k) * 2) * all;
-        ml[u] = p.part_ml[at + row];
-        const float *from = p.part_o + at * D + (size_t)(8 * cg) * all + row;
+        for (int e = 0; e < COLS; ++e) x[u][e] = 0.f;
+        if (k < parts) {
+          const size_t at = (size_t)(k == 0 ? first : (long long)(c0 + k) * 2) * all;
+          ml[u] = p.part_ml[at + row];
+          const float *from = p.part_o + at * D + (size_t)(COLS * cg) * all + row;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = from[(size_t)e * all];
+          for (int e = 0; e < COLS; ++e) x[u][e] = from[(size_t)e * all];
+        }
+      }
+      float m_new = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) m_new = fmaxf(m_new, ml[u].x);
+      const float top = m_new == -INFINITY ? 0.f : m_new, a = ex2_mufu(m - top);
+      m = m_new;
+      l *= a;
+#pragma unroll
+      for (int e = 0; e < COLS; ++e) acc[e] *= a;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2_mufu(ml[u].x - top);
+        l += ml[u].y * w;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) acc[e] += x[u][e] * w;
       }
     }
-    const float m_new = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-    const float top = m_new == -INFINITY ? 0.f : m_new, a = ex2_mufu(m - top);
-    m = m_new;
-    l *= a;
+    if constexpr (SHARED) {
+      __syncthreads();
+      s_part[warp][COLS][lane] = m;
+      s_part[warp][COLS + 1][lane] = l;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= a;
+      for (int e = 0; e < COLS; ++e) s_part[warp][e][lane] = acc[e];
+      __syncthreads();
+      if (share != 0) continue;
+      for (int w = warp + 1; w < warp + p.join; ++w) {
+        const float mw = s_part[w][COLS][lane], m_new = fmaxf(m, mw), top = m_new == -INFINITY ? 0.f : m_new;
+        const float a = ex2_mufu(m - top), aw = ex2_mufu(mw - top);
+        m = m_new;
+        l = l * a + s_part[w][COLS + 1][lane] * aw;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float w = ex2_mufu(ml[u].x - top);
-      l += ml[u].y * w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += x[u][e] * w;
+        for (int e = 0; e < COLS; ++e) acc[e] = acc[e] * a + s_part[w][e][lane] * aw;
+      }
     }
+    if (!mine) continue;
+    const int tok = row / GG, h = kh * GG + row - tok * GG;
+    const size_t q_row = (size_t)s.start + tok0 + tok;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    uint4 *to = reinterpret_cast<uint4 *>(p.o + (q_row * p.H + h) * D + COLS * cg);
+#pragma unroll
+    for (int e = 0; e < COLS; e += 8)
+      to[e / 8] = make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
+                             pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+    if (cg == 0 && p.lse)
+      p.lse[(size_t)h * p.total + q_row] = ((m == -INFINITY ? 0.f : m) + __log2f(l)) * 0.69314718055994531f;
   }
-  if (p.join > 1) {
-    s_part[warp][8][lane] = m;
-    s_part[warp][9][lane] = l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s_part[warp][e][lane] = acc[e];
-    __syncthreads();
-    if (share != 0) return;
-    for (int w = warp + 1; w < warp + p.join; ++w) {
-      const float mw = s_part[w][8][lane], m_new = fmaxf(m, mw), top = m_new == -INFINITY ? 0.f : m_new;
-      const float a = ex2_mufu(m - top), aw = ex2_mufu(mw - top);
-      m = m_new;
-      l = l * a + s_part[w][9][lane] * aw;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + s_part[w][e][lane] * aw;
-    }
-  }
-  if (!mine) return;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  uint32_t y[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  *reinterpret_cast<uint4 *>(p.o + ((size_t)tok * p.H + h) * D + 8 * cg) = make_uint4(y[0], y[1], y[2], y[3]);
-  if (cg == 0 && p.lse)
-    p.lse[(size_t)h * p.total + tok] = ((m == -INFINITY ? 0.f : m) + __log2f(l)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxNew = 256;
@@ -1364,11 +1370,14 @@ int launch_two(const PagedParams &p, int d, int blocks, int threads, int smem, v
                void (*join)(PagedParams, int), cudaStream_t stream) {
   // on every launch: the attribute belongs to the function on the current device
   if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
-  const int rc = launch_after(main, blocks, threads, smem, stream, p);
+  const int rc = launch_after(main, blocks, 1, threads, smem, stream, p);
   if (rc != FA_OK) return rc;
-  const int warps = p.join > 4 ? p.join : 4;
-  const long long tasks = 32 * (warps / p.join);
-  return launch_after(join, ((long long)p.total * p.H * (d / 8) + tasks - 1) / tasks, 32 * warps, 0, stream, p, blocks);
+  // a block for each item and, where these are few, for chunks of it: one wave of blocks
+  const long long items = (long long)p.g.B * p.heads * p.groups;
+  const int threads_join = 32 * (p.join > 4 ? p.join : 4), step = threads_join / p.join;
+  const int chunks = (p.QT * p.TB * p.HB * p.G * (d / 8) + step - 1) / step;
+  const long long many = (14 * kSMs + items - 1) / items;
+  return launch_after(join, items, (int)(many < chunks ? many : chunks), threads_join, 0, stream, p, blocks);
 }
 
 int page_maps(PagedParams &p, const void *k_pages, const void *v_pages, int d) {
@@ -1390,16 +1399,14 @@ int launch_paged(PagedParams &p, int blocks, const void *q, const void *k_pages,
   const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
   const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
   if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) || page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, paged_combine_kernel<D>,
-                    stream);
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
 }
 
 template <int D>
 int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pages, cudaStream_t stream) {
   using C = FewCfg<D>;
   if (page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D>, paged_combine_kernel<D>,
-                    stream);
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D>, p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
 }
 
 }  // namespace
@@ -1471,9 +1478,13 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   // Measured, in microseconds of tiles, against none: 48 ragged sequences of drafted trees 54 (63), at head
   // dim 64 44 (74), at head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).
   p.lead = w.few ? 2 : w.QT == 2 ? 4 : 3;
-  // parts an item is cut into on average, two a warp and four in flight
-  const long long items = (long long)B * p.heads * (w.TB * w.QT >= max_new ? 1 : (max_new + w.TB * w.QT - 1) / (w.TB * w.QT));
-  p.join = w.blocks / items >= 16 ? 8 : w.blocks / items >= 8 ? 4 : 1;
+  p.groups = (max_new + w.TB * w.QT - 1) / (w.TB * w.QT);
+  const long long items = (long long)B * p.heads * p.groups;
+  if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  // Warps to a task of the join: by the parts of an item, as long as they make one wave.
+  const long long tasks = items * w.QT * w.TB * w.HB * (H / Hkv) * (d / 8);
+  p.join = 1;
+  while (p.join < 8 && 4 * p.join <= w.blocks / items + 1 && tasks * 2 * p.join <= 28ll * 32 * kSMs) p.join *= 2;
   p.QT = w.QT;
   p.HB = w.HB;
   p.scale_log2 = scale * 1.4426950408889634f;
