@@ -8,6 +8,7 @@
 
 #include "exp2_poly.cuh"
 #include "fa_internal.h"
+#include "fa_paged.h"
 
 namespace fa {
 
@@ -99,7 +100,7 @@ int get_encoder() {
 }
 }  // namespace
 
-int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int Hx, int d, int box_rows, bool narrow) {
+int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int Hx, int d, int box_rows) {
   if (get_encoder() != FA_OK) return FA_ERR_CUDA;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hx, (cuuint64_t)N, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)Hx * d * 2, (cuuint64_t)N * Hx * d * 2};
@@ -107,22 +108,36 @@ int encode_bf16_tile_map(CUtensorMap *map, const void *base, int B, int N, int H
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
                         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
-                        const uint32_t box_dims[4]) {
+static int encode_bf16_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                           const uint32_t box_dims[4], CUtensorMapL2promotion promotion) {
   if (get_encoder() != FA_OK) return FA_ERR_CUDA;
   const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
   const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
   const cuuint32_t box[4] = {box_dims[0], box_dims[1], box_dims[2], box_dims[3]};
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), d, st, box, estride,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+int encode_bf16_box_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                        const uint32_t box[4]) {
+  return encode_bf16_map(map, base, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+int encode_page_map(CUtensorMap *map, const void *pages, int num_pages, int page_size, int Hkv, int d, int box_rows,
+                    bool narrow) {
+  const uint64_t row = (uint64_t)Hkv * d * 2;
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)Hkv, (uint64_t)page_size, (uint64_t)num_pages};
+  const uint64_t strides[3] = {(uint64_t)d * 2, row, row * page_size};
+  const uint32_t box[4] = {64, 1, (uint32_t)box_rows, 1};
+  return encode_bf16_map(map, pages, dims, strides, box,
+                         narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 int encode_u8_tile_map(CUtensorMap *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],

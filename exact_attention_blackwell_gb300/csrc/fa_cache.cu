@@ -11,13 +11,15 @@
 
 #include <climits>
 
-#include "fa_internal.h"
+#include "fa_paged.h"
 
 namespace fa {
 namespace {
 
 // ------------------------------------------------------------------ append
 // One warp per token: rows of Hkv * d bf16 of k and v, 16 bytes a lane and step.
+// Bound by HBM: 131 thousand tokens of 16 heads of dim 128 take 311 us, 6.9 TB/s; a decoding
+// step of 64 tokens 2.6 us, which is launching and a chain of three loads.
 __global__ void __launch_bounds__(128)
     cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, uint4 *__restrict__ k_pages,
                         uint4 *__restrict__ v_pages, const __grid_constant__ PageGeom g, const int *__restrict__ cu,
@@ -47,8 +49,9 @@ __global__ void __launch_bounds__(128)
 // columns of the rows along the path in ascending order.  A path ascends, so
 // row i is never the source of a later move (source of move j > i is >= j), and
 // a thread touches its own columns only: no barrier is needed between moves, and
-// eight of them can be in flight (32 sequences x 32 layers, paths of up to 17: 13 us
-// where one at a time took 17).
+// eight of them can be in flight (32 sequences x 32 layers, 8 heads of dim 128, paths of
+// up to 17: 17 us where one at a time took 21).  Bound by the lookups along the path and
+// then by HBM.
 constexpr int kPathChunk = 128, kMoves = 8;
 
 __global__ void __launch_bounds__(128)
@@ -111,7 +114,8 @@ __device__ __forceinline__ int pages_held(int len, int page_size, int max_pages)
 }
 
 // A block owns `cols` columns of every row, so it can read all parents' entries
-// (kept in shared memory) before it writes any.
+// (kept in shared memory) before it writes any.  Bound by latency: 128 rows of 2048
+// entries take 4.4 us.
 __global__ void __launch_bounds__(1024)
     cache_fork_kernel(int *__restrict__ refs, int *__restrict__ table, const int *__restrict__ lens,
                       const int *__restrict__ parents, int *__restrict__ lens_out, int B, int max_pages, int num_pages,
@@ -126,7 +130,8 @@ __global__ void __launch_bounds__(1024)
     if (par < -1 || par >= B) par = b;
     if (c0 == 0 && e % cols == 0) lens_out[b] = par < 0 ? 0 : lens[par];
     if (par == b || c >= max_pages) continue;
-    const int now = par >= 0 && c < pages_held(lens[par], page_size, max_pages) ? table[(size_t)par * max_pages + c] : -1;
+    const int now =
+        par >= 0 && c < pages_held(lens[par], page_size, max_pages) ? table[(size_t)par * max_pages + c] : -1;
     const int old = c < pages_held(lens[b], page_size, max_pages) ? table[(size_t)b * max_pages + c] : -1;
     if (now != old) {  // counts of a page kept in place do not change
       if (now >= 0 && now < num_pages) atomicAdd(refs + now, 1);
@@ -148,7 +153,8 @@ __global__ void __launch_bounds__(1024)
 // growing rows' needs are summed, then free pages are handed out lowest first.
 // The block's time is a chain of loads, each about 0.6 us; so lengths are kept in
 // shared memory, and the counts of the first pages are fetched with them and used
-// where no row shrinks.
+// where no row shrinks.  48 rows growing by up to 40 places and shrinking again take 16 us
+// in two calls.
 constexpr int kBookThreads = 1024;
 constexpr int kPagesPerThread = 16, kStretch = kBookThreads * kPagesPerThread;
 
@@ -182,7 +188,8 @@ __global__ void __launch_bounds__(kBookThreads)
                         int *__restrict__ copies, int B, int max_pages, int num_pages, int page_size) {
   extern __shared__ int sm[];
   int *had = sm, *want = sm + B;              // lengths; -1 in both where the row is refused
-  int *last = sm + 2 * B, *first = sm + 3 * B;  // a growing row's shared partial page (or -1); its first rank among the taken pages
+  int *last = sm + 2 * B;   // a growing row's shared partial page (or -1)
+  int *first = sm + 3 * B;  // its first rank among the taken pages, doubled; + 1 where it copies
   unsigned short *list = reinterpret_cast<unsigned short *>(sm + 4 * B);  // [kStretch]
   __shared__ int warp_sums[32];
   __shared__ int s_refused, s_copies;
@@ -313,7 +320,8 @@ __global__ void __launch_bounds__(kBookThreads)
     // the stretch's free pages in order, then one thread for each of them
     const int take = min(sum, total - done);
     int k = at;
-    for (unsigned m = mask; m && k < take; m &= m - 1) list[k++] = (unsigned short)(tid * kPagesPerThread + __ffs(m) - 1);
+    for (unsigned m = mask; m && k < take; m &= m - 1)
+      list[k++] = (unsigned short)(tid * kPagesPerThread + __ffs(m) - 1);
     __syncthreads();
     for (int i = tid; i < take; i += kBookThreads) {
       const int page = s0 + list[i];
@@ -347,7 +355,8 @@ __global__ void __launch_bounds__(kBookThreads)
 }
 
 // The filled rows of shared pages, in every layer, k and v: contiguous runs of
-// rows * chunks 16-byte pieces, cut into pieces of kCopyChunk.
+// rows * chunks 16-byte pieces, cut into pieces of kCopyChunk.  Bound by HBM: about
+// 24 us for 64 rows' part-filled pages in 24 layers of 8 heads of dim 128.
 constexpr int kCopyChunk = 2048;
 
 __global__ void __launch_bounds__(256)
@@ -423,9 +432,9 @@ int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, 
   if (total == 0) return FA_OK;
   const PageGeom g{page_table, cache_lens, B, max_pages, num_pages, page_size};
   const unsigned grid = (unsigned)(((long long)total + 3) / 4);
-  return launch_after(cache_append_kernel, grid, 1, 128, 0, static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k),
-                      static_cast<const uint4 *>(v), static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), g,
-                      cu_seqlens, total, Hkv * d / 8);
+  return launch_after(cache_append_kernel, grid, 1, 128, 0, static_cast<cudaStream_t>(stream),
+                      static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), static_cast<uint4 *>(k_pages),
+                      static_cast<uint4 *>(v_pages), g, cu_seqlens, total, Hkv * d / 8);
 }
 
 int fa_cache_compact(void *k_pages, void *v_pages, const int *page_table, const int *cache_lens, const int *accepted,
@@ -468,8 +477,8 @@ int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const 
     return FA_ERR_CUDA;
   const unsigned grid = (unsigned)((max_pages + cols - 1) / cols);
   const int threads = B * cols >= 1024 ? 1024 : (B * cols + 31) / 32 * 32;
-  return launch_after(cache_fork_kernel, grid, 1, threads, smem, static_cast<cudaStream_t>(stream), page_refs, page_table,
-                      cache_lens, parents, lens_out, B, max_pages, num_pages, page_size, cols);
+  return launch_after(cache_fork_kernel, grid, 1, threads, smem, static_cast<cudaStream_t>(stream), page_refs,
+                      page_table, cache_lens, parents, lens_out, B, max_pages, num_pages, page_size, cols);
 }
 
 size_t fa_cache_resize_workspace_bytes(int B) { return B > 0 && B <= kMaxBookRows ? resize_bytes(B) : 0; }
@@ -492,13 +501,13 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if (!workspace || workspace_bytes < resize_bytes(B) || !ptr_aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   int *copies = static_cast<int *>(workspace);
-  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBookRows * 16 + kStretch * 2) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kMaxBookRows * 16 + kStretch * 2) != cudaSuccess)
     return FA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = launch_after(cache_resize_kernel, 1, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table, cache_lens,
-                         new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size)) != FA_OK)
-    return rc;
+  rc = launch_after(cache_resize_kernel, 1, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table,
+                    cache_lens, new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size);
+  if (rc != FA_OK) return rc;
   return launch_after(cache_copy_kernel, 152 * 2, 1, 256, 0, s, static_cast<uint4 *>(k_pages),
                       static_cast<uint4 *>(v_pages), (const int *)copies, num_pages, page_size, layers, Hkv * d / 8);
 }

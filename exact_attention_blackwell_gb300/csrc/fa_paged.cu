@@ -9,7 +9,7 @@
 
 #include <cmath>
 
-#include "fa_internal.h"
+#include "fa_paged.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -17,12 +17,13 @@ namespace {
 
 // Work.  A unit is one key tile (bn places) of one item; an item is one (sequence,
 // HB adjacent kv heads, row group), a row group being QT tiles of TB * G rows (TB
-// tokens with the G query heads that share a kv head).  The units of all items stand in one
-// line, each item's after `lead` units without a tile that stand for its other costs
-// (fetching its Q, writing its result), cut into equal stretches for the blocks, so
-// that ragged batches keep all SMs busy; the lengths are known on the device only, so every block sums them up
-// itself.  A block that gets only a part of an item writes its unnormalised O with
-// the row maxima and sums; paged_combine_kernel joins the parts.
+// tokens with the G query heads that share a kv head).  The units of all items stand
+// in one line, each item's after `lead` units without a tile that stand for its other
+// costs (fetching its Q, writing its result), cut into equal stretches for the blocks,
+// so that ragged batches keep all SMs busy; the lengths are known on the device only,
+// so every block sums them up itself.  A block that gets only a part of an item writes
+// its unnormalised O with the row maxima and sums; paged_combine_kernel joins the
+// parts.
 struct PagedParams {
   CUtensorMap tm_q;  // [total, Hkv, G, d]: box 64 columns x G heads x TB tokens
   CUtensorMap tm_k, tm_v;  // [num_pages, page_size, Hkv, d]: box 64 columns x min(page_size, BN) rows of one head
@@ -370,6 +371,20 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
   }
 }
 
+// Softmax with one pass over the keys: per row the running maximum m and sum l of
+// exp2(c2 S - m), O rescaled only where m grows by more than kRescaleTau.  Warps: 4 QT
+// of softmax (a thread to a row), one that issues tcgen05 MMAs, one that fetches tiles
+// page by page.  A byte of the cache meets 2 * rows FLOPs, so up to some 280 rows HBM is
+// the bound, and from 128 rows on the softmax: each place of a row costs an ex2.
+// One row tile: two blocks on an SM (head dims 64 and 128), tiles of 64 places, S one
+// tile ahead of the softmax.  Two: one block, 128 places (at 64 columns an MMA step costs
+// what it costs at 128), the softmax 64 columns at a time (128 columns a thread spilled
+// 600 bytes), one issuing warp that alternates between the row tiles (with one for each,
+// both softmaxes ran in phase: 4100 instead of 3500 cycles for 128 places).
+// Measured with the join: 16 ragged sequences of up to 7000 places, trees of up to 33
+// tokens, 4 kv heads of dim 256: 49 us, 4.7 TB/s; one of 32768 places, 64 tokens, 32 on 8
+// heads of dim 128: 41 us, 830 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
+// parts' way out and the join.
 template <int D, int BN, int QT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
     paged_fwd_kernel(const __grid_constant__ PagedParams p) {
@@ -836,6 +851,10 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 // A head's row is only 128 to 512 bytes of the cache; fetching adjacent heads
 // together keeps DRAM pages and 256-byte L2 lines whole, and with HB = 4 each warp
 // has a head to itself and nothing to join.
+// Measured with the join: 64 sequences of up to 8192 places, one token each, 32 on 8
+// heads of dim 128: 153.5 us, 6.7 TB/s (the tcgen05 kernel: 164); 32 of up to 2500,
+// chains of up to 7, 16 heads of dim 64: 34.5 us, 4.8 TB/s, of which some 9 are set-up,
+// the first tiles and the join.
 template <int D>
 struct FewCfg {
   static constexpr int kWarps = 4, kBoxes = D / 64;
@@ -891,7 +910,8 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
   float2 *s_ml = reinterpret_cast<float2 *>(smem + C::kOffML);
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bn = 1 << p.bn_log2, box_bytes = bn * 128, head_bytes = bn * D * 2;  // a 64-column box, a head's part of a tile
+  const int bn = 1 << p.bn_log2;
+  const int box_bytes = bn * 128, head_bytes = bn * D * 2;  // a 64-column box, a head's part of a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -1201,13 +1221,15 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
 // far as the call's inputs tell), the others take it from there: the search for
 // every row by every thread was half of this kernel's time.  A task is COLS columns
 // of one row; with many parts (SHARED) p.join warps share 32 tasks and take every
-// join-th part each, U of them in flight.  Parts are stored column by column, so that neighbouring tasks are
-// contiguous for the kernels' stores and the loads here.
+// join-th part each, U of them in flight.  Parts are stored column by column, so that
+// neighbouring tasks are contiguous for the kernels' stores and the loads here.  Bound
+// by latency: a few dependent loads, 4 us for 8 items of 256 rows in 19 parts each.
 constexpr int kJoinWarps = 8;  // at most; four unless all eight share their tasks
 
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
-  constexpr int COLS = 8, U = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
+  constexpr int COLS = 8, U = 4;  // one 16-byte store a task
   __shared__ float s_part[SHARED ? kJoinWarps : 1][COLS + 2][32];
   __shared__ unsigned s_u0, s_total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1236,8 +1258,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
     const long long per = stretch_units(p, total, blocks), at = u0 + (long long)(kh * groups + rg) * (tiles + p.lead);
     c0 = (int)quot(at + p.lead, per);
     parts = (int)quot(at + p.lead + tiles - 1, per) - c0 + 1;
-    // only the first block can have had tiles of another item before this one's: it begins before this
-    // item's units (the ones before them are tiles), and this is its second part
+    // only the first block can have had tiles of another item before this one's: it began before this
+    // item's units (the one before them is a tile), and this is its second part
     first = (long long)c0 * 2 + (at > c0 * per ? 1 : 0);
   };
   if (p.by_warp && rows > 0) find_parts();
@@ -1310,11 +1332,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_combine_kernel(const __
     const int tok = row / GG, h = kh * GG + row - tok * GG;
     const size_t q_row = (size_t)s.start + tok0 + tok;
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    uint4 *to = reinterpret_cast<uint4 *>(p.o + (q_row * p.H + h) * D + COLS * cg);
+    uint32_t w[COLS / 2];
 #pragma unroll
-    for (int e = 0; e < COLS; e += 8)
-      to[e / 8] = make_uint4(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
-                             pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+    for (int e = 0; e < COLS / 2; ++e) w[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint4 *>(p.o + (q_row * p.H + h) * D + COLS * cg) = make_uint4(w[0], w[1], w[2], w[3]);
     if (cg == 0 && p.lse)
       p.lse[(size_t)h * p.total + q_row] = ((m == -INFINITY ? 0.f : m) + __log2f(l)) * 0.69314718055994531f;
   }
@@ -1385,8 +1406,8 @@ int page_maps(PagedParams &p, const void *k_pages, const void *v_pages, int d) {
   // of the copy rate at 8000 places, 16 heads)
   const bool narrow = d == 64 && p.HB == 1;
   const int bn = 1 << p.bn_log2, box_rows = p.g.page_size < bn ? p.g.page_size : bn;
-  return encode_bf16_tile_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows, narrow) ||
-                 encode_bf16_tile_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows, narrow)
+  return encode_page_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows, narrow) ||
+                 encode_page_map(&p.tm_v, v_pages, p.g.num_pages, p.g.page_size, p.Hkv, d, box_rows, narrow)
              ? FA_ERR_CUDA
              : FA_OK;
 }
@@ -1399,14 +1420,16 @@ int launch_paged(PagedParams &p, int blocks, const void *q, const void *k_pages,
   const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.H * D * 2};
   const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
   if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) || page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>, p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_fwd_kernel<D, BN, QT>,
+                    p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
 }
 
 template <int D>
 int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pages, cudaStream_t stream) {
   using C = FewCfg<D>;
   if (page_maps(p, k_pages, v_pages, D)) return FA_ERR_CUDA;
-  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D>, p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
+  return launch_two(p, D, blocks, C::kThreads, C::kSmemBytes, paged_few_kernel<D>,
+                    p.join > 1 ? paged_combine_kernel<D, true> : paged_combine_kernel<D, false>, stream);
 }
 
 }  // namespace
@@ -1437,6 +1460,12 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   if (rc != FA_OK) return rc;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (tree_mask && (long long)mask_words * 64 < max_new) return FA_ERR_INVALID_ARG;
+  const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
+  // the units of one sequence are counted in 31 bits, and so are the items
+  const double seq_units = ((double)max_pages * page_size / w.bn + 8) * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB);
+  const int groups = (max_new + w.TB * w.QT - 1) / (w.TB * w.QT);
+  const long long items = (long long)B * (Hkv / w.HB) * groups;
+  if (seq_units >= 2147483648.0 || items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   for (const void *x : {q, k_pages, v_pages, (const void *)o})
     if (!ptr_aligned(x, 16)) return FA_ERR_ALIGNMENT;
   for (const void *x : {(const void *)page_table, (const void *)cache_lens, (const void *)cu_seqlens, (const void *)lse})
@@ -1446,10 +1475,6 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
     return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   if (total == 0) return FA_OK;
-  const PagedPlan w = paged_plan(B, max_new, Hkv, H / Hkv, d);
-  // the units of one sequence are counted in 31 bits
-  const double seq_units = ((double)max_pages * page_size / w.bn + 8) * (Hkv / w.HB) * ((max_new + w.TB - 1) / w.TB);
-  if (seq_units >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   PagedParams p;
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1475,12 +1500,10 @@ int fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages, const 
   p.heads = Hkv / w.HB;
   p.by_warp = B <= 32 && B * seq_units < 2147483648.0 - 4 * kSMs;
   p.min_units = w.few ? 2 : 1;
-  // Measured, in microseconds of tiles, against none: 48 ragged sequences of drafted trees 54 (63), at head
-  // dim 64 44 (74), at head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).
+  // In microseconds, against none: 48 ragged sequences of drafted trees 54 (63), at head dim 64 44 (74), at
+  // head dim 256 48 (56); 96 short sequences, one token each 25.7 (28.3).
   p.lead = w.few ? 2 : w.QT == 2 ? 4 : 3;
-  p.groups = (max_new + w.TB * w.QT - 1) / (w.TB * w.QT);
-  const long long items = (long long)B * p.heads * p.groups;
-  if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  p.groups = groups;
   // Warps to a task of the join: by the parts of an item, as long as they make one wave.
   const long long tasks = items * w.QT * w.TB * w.HB * (H / Hkv) * (d / 8);
   p.join = 1;

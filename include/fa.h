@@ -254,7 +254,8 @@ int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, 
  *     64 >= max_new, or NULL;
  *   max_new : no sequence has more new tokens (rows past it are not written),
  *     at most 256.
- *   H / Hkv at most 128.  workspace : caller-owned, 256-byte aligned, of at least
+ *   H / Hkv at most 128; more than 2^31 tiles of one sequence, or items of
+ *     (sequence, kv head), are FA_ERR_UNSUPPORTED.  workspace : caller-owned, 256-byte aligned, of at least
  *     fa_fwd_paged_workspace_bytes() bytes (0 for sizes that would be rejected).
  * No atomics: the result is bitwise reproducible. */
 size_t fa_fwd_paged_workspace_bytes(int B, int max_new, int H, int Hkv, int d);
@@ -324,10 +325,10 @@ int fa_last_device_status(void *stream);
  * slot free, 14 S computed, 15 dP computed, 16 P stored, 17 dS stored,
  * 19 final MMA, 20 MMA drain, 21 shared-memory alignment, 22 the dQ kernel's
  * Q and dO tiles loaded; fused backward: 23 dQ partial computed, 24 S read
- * into registers, 25 dQ partial read out); paged attention 31-39 (31 Q tile
+ * into registers, 25 dQ partial read out); paged attention 31-40 (31 Q tile
  * loaded, 32/33 K/V tile loaded, 34 P stored, 35 ring slot free, 36 S computed,
- * 37 O readable, 38 MMA drain, 39 Q tile free, 40 the last V tile loaded) and, with few rows, 41 K and V
- * tile loaded, 42 ring slot free.  Outputs of a call in which a wait
+ * 37 O readable, 38 MMA drain, 39 Q tile free, 40 last V tile loaded) and, with
+ * few rows, 41 K and V tile loaded, 42 ring slot free.  Outputs of a call in which a wait
  * ran out are unspecified. */
 int fa_last_device_status_site(void *stream, int *site);
 

@@ -56,6 +56,16 @@ def test_attention(args, code):
     assert fa.fa_fwd_paged(**a) == code
 
 
+@pytest.mark.parametrize("args", [dict(max_pages=1 << 26, num_pages=1, H=65535, Hkv=65535, d=64),  # tiles of a sequence
+                                  dict(B=65535, num_pages=1, H=65535, Hkv=65535, d=64)], ids=ids)  # items
+def test_attention_counts_work_in_31_bits(args):
+    test_attention(args, UNS)
+
+
+def test_resize_refuses_pools_past_2_to_30_pages():
+    test_resize(dict(num_pages=(1 << 30) + 1, layers=1, Hkv=1, d=64), UNS)
+
+
 def test_attention_workspace():
     assert fa.fa_fwd_paged_workspace_bytes(2, 1, 4, 2, 128) > 0
     for bad in ((0, 1, 4, 2, 128), (2, 0, 4, 2, 128), (2, 257, 4, 2, 128), (2, 1, 3, 2, 128), (2, 1, 4, 2, 96)):
