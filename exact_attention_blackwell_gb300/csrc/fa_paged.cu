@@ -378,12 +378,14 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
 // the bound, and from 128 rows on the softmax: each place of a row costs an ex2.
 // One row tile: two blocks on an SM (head dims 64 and 128), tiles of 64 places, S one
 // tile ahead of the softmax.  Two: one block, 128 places (at 64 columns an MMA step costs
-// what it costs at 128), the softmax 64 columns at a time (128 columns a thread spilled
-// 600 bytes), one issuing warp that alternates between the row tiles (with one for each,
-// both softmaxes ran in phase: 4100 instead of 3500 cycles for 128 places).
+// what it costs at 128), the softmax 64 columns at a time with one maximum for all 128
+// (the first half is read twice; 128 columns in a thread's registers spilled 600 bytes,
+// a maximum for each half took 42 instead of 38.7 us below), one issuing warp that
+// alternates between the row tiles (with one for each, both softmaxes ran in phase: 4100
+// instead of 3500 cycles for 128 places).
 // Measured with the join: 16 ragged sequences of up to 7000 places, trees of up to 33
 // tokens, 4 kv heads of dim 256: 49 us, 4.7 TB/s; one of 32768 places, 64 tokens, 32 on 8
-// heads of dim 128: 41 us, 830 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
+// heads of dim 128: 38.7 us, 890 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
 // parts' way out and the join.
 template <int D, int BN, int QT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
@@ -464,13 +466,12 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         const unsigned long long *words =
             p.mask && row ? p.mask + (size_t)(walk.s.start + i) * p.words : nullptr;
         float m_ref = -INFINITY, l_sum = 0.f;
-        // 64 columns at a time: a tile, or half of one
-        for (int j = 0; j < nt * (BN / 64) && ok; ++j, ++tile_no) {
-          const int kv0 = walk.j0 * BN + 64 * j;
-          const bool tail = kv0 + 64 > walk.s.len;
-          unsigned see[2];  // the places this row sees, while the tile is being multiplied
+        for (int j = 0; j < nt && ok; ++j, ++tile_no) {
+          const int kv0 = (walk.j0 + j) * BN;
+          const bool tail = kv0 + BN > walk.s.len;
+          unsigned see[BN / 32];  // the places this row sees, while the tile is being multiplied
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+          for (int w = 0; w < BN / 32; ++w) {
             see[w] = 0xffffffffu;
             if (tail) {
               const int at = kv0 + 32 * w, pre = walk.s.len - at;
@@ -478,34 +479,36 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
               if (pre < 32) see[w] |= seen_bits(words, i, walk.s.keys - walk.s.len, at - walk.s.len);
             }
           }
-          const int buf = tile_no & 1, par = (tile_no >> 1) & 1;
+          const int buf = C::kPair ? 0 : tile_no & 1;
           const uint32_t s_tm = tmem + lane_off + (uint32_t)(64 * (2 * t + buf));
-          if (!C::kPair) ok = mbar_wait_warp(s_bar(t, buf), par, wctx, kPSiteSFull);
-          else if (buf == 0) ok = mbar_wait_warp(s_bar(t, 0), par, wctx, kPSiteSFull);
+          ok = mbar_wait_warp(s_bar(t, buf), (C::kPair ? tile_no : tile_no >> 1) & 1, wctx, kPSiteSFull);
           if (!ok) break;
           tc_fence_after();
-          if (live) {
-            float s[64];
-            {
-              uint32_t sr[2][32];
-              tmem_ld_32x32b_x32(s_tm, sr[0]);
-              tmem_ld_32x32b_x32(s_tm + 32, sr[1]);
-              tmem_wait_ld(sr[0]);
-              reg_tie(sr[1]);
+          float s[64];  // of one half
+          const unsigned gone = bad[(tiles + j) & 15];
+          const bool masked = tail || gone;
+          if (gone) {
 #pragma unroll
-              for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
+            for (int w = 0; w < BN / 32; ++w) {
+              if ((gone >> (2 * w)) & 1) see[w] &= 0xffff0000u;
+              if ((gone >> (2 * w)) & 2) see[w] &= 0x0000ffffu;
             }
-            const unsigned gone = C::kPair ? bad[(tiles + (j >> 1)) & 15] >> (4 * buf) : bad[(tiles + j) & 15];
-            if (tail || gone) {
+          }
+          auto read_s = [&](int half) {
+            uint32_t sr[2][32];
+            tmem_ld_32x32b_x32(s_tm + 64 * half, sr[0]);
+            tmem_ld_32x32b_x32(s_tm + 64 * half + 32, sr[1]);
+            tmem_wait_ld(sr[0]);
+            reg_tie(sr[1]);
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                if ((gone >> (2 * w)) & 1) see[w] &= 0xffff0000u;
-                if ((gone >> (2 * w)) & 2) see[w] &= 0x0000ffffu;
+            for (int c = 0; c < 64; ++c) s[c] = __uint_as_float(sr[c >> 5][c & 31]);
+            if (masked) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!((see[w] >> c) & 1)) s[32 * w + c] = -INFINITY;
-              }
+              for (int c = 0; c < 64; ++c)
+                if (!((see[2 * half + (c >> 5)] >> (c & 31)) & 1)) s[c] = -INFINITY;
             }
+          };
+          auto max_s = [&] {
             float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
             for (int c = 4; c < 60; c += 8) {
@@ -516,20 +519,45 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
             }
             mx0 = fmax3(mx0, s[60], s[61]);
             mx1 = fmax3(mx1, s[62], s[63]);
-            const float m_blk = fmax3(mx0, mx1, fmaxf(mx2, mx3)) * c2;
+            return fmax3(mx0, mx1, fmaxf(mx2, mx3)) * c2;
+          };
+          float neg_m = 0.f;
+          auto weigh = [&](int half) {  // P over the half's S
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              float x[4], e[4];
+              ffma2(x[0], x[1], s[c], s[c + 1], c2, c2, neg_m, neg_m);
+              ffma2(x[2], x[3], s[c + 2], s[c + 3], c2, c2, neg_m, neg_m);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) e[u] = ex2_mufu(x[u]);
+              fadd2(l0, l1, l0, l1, e[0], e[1]);
+              fadd2(l2, l3, l2, l3, e[2], e[3]);
+              pk[c >> 1] = pack_bf16x2(e[0], e[1]);
+              pk[(c >> 1) + 1] = pack_bf16x2(e[2], e[3]);
+            }
+            tmem_st_32x32b_x32(s_tm + 64 * half, pk);
+            l_sum += (l0 + l1) + (l2 + l3);
+            tmem_wait_st();
+            tc_fence_before();
+          };
+          if (live) {
+            read_s(0);
+            float m_blk = max_s();
+            if (C::kPair) {  // the second half stays in registers and is weighed first
+              read_s(1);
+              m_blk = fmaxf(m_blk, max_s());
+            }
             if (j == 0) {
               m_ref = m_blk;
             } else if (__any_sync(0xffffffffu, row && (m_blk - m_ref) > kRescaleTau)) {
-              // O is read once the P V before is done.  A pair's S follows P V of the pair before it, and
-              // P V of its first half has a barrier; else S of the next tile follows P V of the last one,
-              // and where there is no next tile it has a barrier.
-              if (C::kPair) {
-                if (buf == 1) ok = mbar_wait_warp(pv_bar(t), par, wctx, kPSiteOFull);
-              } else if (j + 1 < nt) {
+              // O is read once the P V before is done.  A pair's S follows it; else S of the next tile follows
+              // it, and where there is no next tile it has a barrier.
+              if (!C::kPair && j + 1 < nt)
                 ok = mbar_wait_warp(s_bar(t, buf ^ 1), ((tile_no + 1) >> 1) & 1, wctx, kPSiteOFull);
-              } else {
+              else if (!C::kPair)
                 ok = mbar_wait_warp(pv_bar(t), pv_no & 1, wctx, kPSiteOFull);
-              }
               if (!ok) break;
               tc_fence_after();
               const float m_new = fmaxf(m_ref, m_blk);
@@ -546,34 +574,21 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
                 tmem_st_32x32b_x32(o_tm + 32 * c, o);
               }
             }
-            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: all weights 0
-            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              float x[4], e[4];
-              ffma2(x[0], x[1], s[c], s[c + 1], c2, c2, neg_m, neg_m);
-              ffma2(x[2], x[3], s[c + 2], s[c + 3], c2, c2, neg_m, neg_m);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) e[u] = ex2_mufu(x[u]);
-              fadd2(l0, l1, l0, l1, e[0], e[1]);
-              fadd2(l2, l3, l2, l3, e[2], e[3]);
-              pk[c >> 1] = pack_bf16x2(e[0], e[1]);
-              pk[(c >> 1) + 1] = pack_bf16x2(e[2], e[3]);
-            }
-            tmem_st_32x32b_x32(s_tm, pk);
-            l_sum += (l0 + l1) + (l2 + l3);
-            tmem_wait_st();
-            tc_fence_before();
+            neg_m = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: all weights 0
+            weigh(C::kPair ? 1 : 0);
           }
-          if (t == 0 && (!C::kPair || buf == 0)) {
-            const int tile = C::kPair ? j >> 1 : j, first = (walk.j0 + tile) * BN;
-            if (first + BN > walk.s.len) {
-              const int fv = 2 * tiles + v_fill<C::kPair>(tile, nt), sv = fv % C::kStages;
-              ok = mbar_wait_warp(full_bar(sv), (fv / C::kStages) & 1, wctx, kPSiteVTail);
-              if (!ok) break;
-              if (clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, first, p.g.page_size) && lane == 0)
-                *tail_hit = item;
+          if (t == 0 && tail) {
+            const int fv = 2 * tiles + v_fill<C::kPair>(j, nt), sv = fv % C::kStages;
+            ok = mbar_wait_warp(full_bar(sv), (fv / C::kStages) & 1, wctx, kPSiteVTail);
+            if (!ok) break;
+            if (clear_unseen<D, BN>(smem + C::kOffRing + sv * C::kTileBytes, walk.s, kv0, p.g.page_size) && lane == 0)
+              *tail_hit = item;
+          }
+          if (C::kPair) {
+            mbar_arrive_warp(p_bar(t, 1));
+            if (live) {
+              read_s(0);
+              weigh(0);
             }
           }
           if (!(FA_STALL(4) && tile_no == 0 && t == 0)) mbar_arrive_warp(p_bar(t, buf));
@@ -630,8 +645,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
   } else if (warp == C::kMmaWarp) {
     // ===================================================== MMA issue (whole warp; the elected lane issues)
     // One warp for both row tiles: their S and P V alternate in the pipe, so that one tile's softmax runs
-    // under the other's products.  (A warp each: both wait for S at once and compute at once, 4100 instead
-    // of 3500 cycles for 128 places of 256 rows.)
+    // under the other's products.
     constexpr uint32_t idesc_s = make_idesc_bf16(128, BN, false, false);
     constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, false, true);
     auto slot_of = [&](int f) { return f % C::kStages; };
@@ -646,7 +660,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         mma_ss(tmem + 128u * t + 64u * buf, q_desc + (uint32_t)((t * C::kQBytes + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
     };
-    // P V of the 64 places whose P is in buffer `buf`, rows 64 * half on of the tile
+    // P V of the 64 places whose P is in buffer `buf`, rows 64 * half on of the tile (of a pair the second
+    // half is ready first)
     auto issue_pv = [&](int t, int buf, int half, int slot, bool acc) {
       const uint64_t vd = ring_desc_v + (uint64_t)((slot * C::kTileBytes + half * 64 * 128) >> 4);
 #pragma unroll
@@ -706,7 +721,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
         for (int t = 0; t < QT; ++t) {
           if (!act[t] || !ok) continue;
           const int buf = C::kPair ? 0 : p_no[t] & 1, par = C::kPair ? p_no[t] & 1 : (p_no[t] >> 1) & 1;
-          ok = mbar_wait_warp(p_bar(t, buf), par, wctx, kPSitePFull);
+          ok = mbar_wait_warp(p_bar(t, C::kPair ? 1 : buf), par, wctx, kPSitePFull);
           if (!ok) break;
           tc_fence_after();
           // Row tile 0's warps have cleared what they had to; this one's have left the epilogue of every
@@ -715,15 +730,15 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
           if (cleared && lane == 0) odd[t] = seg;
           __syncwarp();
           if (elect_one()) {
-            issue_pv(t, buf, 0, sv, j > 0);
-            if (C::kPair || j == nt - 2) tc_commit(pv_bar(t));
+            issue_pv(t, C::kPair ? 1 : buf, C::kPair ? 1 : 0, sv, j > 0);
+            if (!C::kPair && j == nt - 2) tc_commit(pv_bar(t));
           }
           __syncwarp();
           if (C::kPair) {
-            ok = mbar_wait_warp(p_bar(t, 1), par, wctx, kPSitePFull);
+            ok = mbar_wait_warp(p_bar(t, 0), par, wctx, kPSitePFull);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) issue_pv(t, 1, 1, sv, true);
+            if (elect_one()) issue_pv(t, 0, 0, sv, true);
             __syncwarp();
           }
           ++p_no[t];
