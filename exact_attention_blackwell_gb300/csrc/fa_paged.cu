@@ -43,7 +43,7 @@ struct PagedParams {
   int min_units;        // a block's stretch is no shorter
   int lead;             // units that stand for what an item costs beside its tiles
   bool by_warp;         // up to 32 sequences, whose units fit 31 bits
-  int join;             // warps that share a task of the join
+  int join, join_y;     // the join: warps that share a task, blocks of a row group that is not the last
   float scale_log2;
 };
 
@@ -380,12 +380,12 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
 // tile ahead of the softmax.  Two: one block, 128 places (at 64 columns an MMA step costs
 // what it costs at 128), the softmax 64 columns at a time with one maximum for all 128
 // (the first half is read twice; 128 columns in a thread's registers spilled 600 bytes,
-// a maximum for each half took 42 instead of 38.7 us below), one issuing warp that
+// a maximum for each half took 3.3 us more below), one issuing warp that
 // alternates between the row tiles (with one for each, both softmaxes ran in phase: 4100
 // instead of 3500 cycles for 128 places).
 // Measured with the join: 16 ragged sequences of up to 7000 places, trees of up to 33
-// tokens, 4 kv heads of dim 256: 49 us, 4.7 TB/s; one of 32768 places, 64 tokens, 32 on 8
-// heads of dim 128: 38.7 us, 890 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
+// tokens, 4 kv heads of dim 256: 48 us, 4.8 TB/s; one of 32768 places, 64 tokens, 32 on 8
+// heads of dim 128: 37.5 us, 920 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
 // parts' way out and the join.
 template <int D, int BN, int QT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
@@ -1231,26 +1231,33 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
   }
 }
 
-// Joins the parts of the items that were cut.  Blocks go by (item, chunk); one
+// Joins the parts of the items that were cut.  Blocks go by (item, chunks of it); one
 // warp finds out where the item's parts are (before the wait for the main kernel as
 // far as the call's inputs tell), the others take it from there: the search for
 // every row by every thread was half of this kernel's time.  A task is COLS columns
 // of one row; with many parts (SHARED) p.join warps share 32 tasks and take every
 // join-th part each, U of them in flight.  Parts are stored column by column, so that
 // neighbouring tasks are contiguous for the kernels' stores and the loads here.  Bound
-// by latency: a few dependent loads, 4 us for 8 items of 256 rows in 19 parts each.
+// by latency: launch, the item's place, two rounds of loads from L2; 5 us after the main
+// kernel for 8 items of 256 rows in 19 parts each (21 MB, 13 us from DRAM).  At 72
+// registers those 1024 blocks run at once (80: 38.0 instead of 37.4 us for the call).
 constexpr int kJoinWarps = 8;  // at most; four unless all eight share their tasks
+// Blocks of four warps: some 6 to 7 run at once on an SM, and many items are whole or
+// short, whose blocks end at once.  (7 to an SM, each with more chunks: 48 ragged trees of
+// 64 rows 59.6 instead of 54.5 us; 20: 55.4.)
+constexpr int kJoinWave = 14 * 152;
 
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-    paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
+__global__ void __maxnreg__(SHARED ? 72 : 80) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
   constexpr int COLS = 8, U = 4;  // one 16-byte store a task
   __shared__ float s_part[SHARED ? kJoinWarps : 1][COLS + 2][32];
   __shared__ unsigned s_u0, s_total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int GG = p.HB * p.G, all = p.QT * p.TB * GG;
-  const int rg = (int)(blockIdx.x % p.groups), seq_kh = (int)(blockIdx.x / p.groups);
-  const int b = seq_kh / p.heads, kh = seq_kh - b * p.heads;
+  const int b = (int)blockIdx.x / p.heads, kh = (int)blockIdx.x - b * p.heads;
+  const int rg = min((int)blockIdx.y / p.join_y, p.groups - 1);
+  const int chunk0 = (int)blockIdx.y - rg * p.join_y;
+  const int chunk_step = rg < p.groups - 1 ? p.join_y : (int)gridDim.y - (p.groups - 1) * p.join_y;
   const PagedSeq s = paged_seq(p, b);
   const int tok0 = rg * p.QT * p.TB, rows = min(s.n - tok0, p.QT * p.TB) * GG;
   int tiles, groups;
@@ -1267,28 +1274,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     total = s_total;
   }
   // the item's parts: from the block with its first tile on
-  int c0 = 0, parts = 0;
-  long long first = 0;
+  int c0 = 0, parts = 0, first = 0;
   auto find_parts = [&] {
     const long long per = stretch_units(p, total, blocks), at = u0 + (long long)(kh * groups + rg) * (tiles + p.lead);
     c0 = (int)quot(at + p.lead, per);
     parts = (int)quot(at + p.lead + tiles - 1, per) - c0 + 1;
     // only the first block can have had tiles of another item before this one's: it began before this
     // item's units (the one before them is a tile), and this is its second part
-    first = (long long)c0 * 2 + (at > c0 * per ? 1 : 0);
+    first = 2 * c0 + (at > c0 * per ? 1 : 0);
   };
   if (p.by_warp && rows > 0) find_parts();
   grid_go();
+  // Nothing to join: no such row group, or one block had it all and has written the result.  The first
+  // block waits in any case, so that the grid does not end before the main kernel has.
+  if ((rows <= 0 || parts == 1) && (blockIdx.x | blockIdx.y) != 0) return;
   grid_wait();
-  if (rows <= 0) return;  // no such row group
+  if (rows <= 0) return;
   if (!p.by_warp) {
     u0 = p.prefix[b];
     total = p.prefix[p.g.B];
     find_parts();
   }
-  if (parts == 1) return;  // one block had it all and has written the result
+  if (parts == 1) return;
   const int share = warp % p.join, tasks = rows * (D / COLS), step = (int)blockDim.x / p.join;
-  for (int base = blockIdx.y * step; base < tasks; base += gridDim.y * step) {
+  for (int base = chunk0 * step; base < tasks; base += chunk_step * step) {
     const int task = base + warp / p.join * 32 + lane;
     const int cg = task / rows, row = task - cg * rows;
     const bool mine = task < tasks;
@@ -1303,11 +1312,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 #pragma unroll
         for (int e = 0; e < COLS; ++e) x[u][e] = 0.f;
         if (k < parts) {
-          const size_t at = (size_t)(k == 0 ? first : (long long)(c0 + k) * 2) * all;
+          const unsigned at = (unsigned)(k == 0 ? first : (c0 + k) * 2) * all;  // < 2^20 rows in all
           ml[u] = p.part_ml[at + row];
-          const float *from = p.part_o + at * D + (size_t)(COLS * cg) * all + row;
+          const float *from = p.part_o + (at * D + COLS * cg * all + row);
 #pragma unroll
-          for (int e = 0; e < COLS; ++e) x[u][e] = from[(size_t)e * all];
+          for (int e = 0; e < COLS; ++e, from += all) x[u][e] = *from;
         }
       }
       float m_new = m;
@@ -1402,18 +1411,25 @@ PagedPlan paged_plan(int B, int max_new, int Hkv, int G, int d) {
 }
 
 // The main kernel, then the join.
-int launch_two(const PagedParams &p, int d, int blocks, int threads, int smem, void (*main)(PagedParams),
+int launch_two(PagedParams &p, int d, int blocks, int threads, int smem, void (*main)(PagedParams),
                void (*join)(PagedParams, int), cudaStream_t stream) {
   // on every launch: the attribute belongs to the function on the current device
   if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
   const int rc = launch_after(main, blocks, 1, threads, smem, stream, p);
   if (rc != FA_OK) return rc;
-  // a block for each item and, where these are few, for chunks of it: one wave of blocks
-  const long long items = (long long)p.g.B * p.heads * p.groups;
+  // for each (sequence, kv heads) blocks for chunks of its row groups, the last of which may be short: at most
+  // kJoinWave in all, and one to a row group at least
+  const long long line = (long long)p.g.B * p.heads;
   const int threads_join = 32 * (p.join > 4 ? p.join : 4), step = threads_join / p.join;
-  const int chunks = (p.QT * p.TB * p.HB * p.G * (d / 8) + step - 1) / step;
-  const long long many = (14 * kSMs + items - 1) / items;
-  return launch_after(join, items, (int)(many < chunks ? many : chunks), threads_join, 0, stream, p, blocks);
+  const int full = p.QT * p.TB, last = p.max_new - (p.groups - 1) * full;
+  auto chunks = [&](int tokens) { return (tokens * p.HB * p.G * (d / 8) + step - 1) / step; };
+  const long long wave = kJoinWave * 128 / threads_join / line;
+  long long many = wave / p.groups, end = many < chunks(last) ? many : chunks(last);
+  if (end < 1) end = 1;
+  if (p.groups > 1) many = (wave - end) / (p.groups - 1);
+  if (many > chunks(full)) many = chunks(full);
+  p.join_y = many < 1 ? 1 : (int)many;
+  return launch_after(join, line, (int)((p.groups - 1) * p.join_y + end), threads_join, 0, stream, p, blocks);
 }
 
 int page_maps(PagedParams &p, const void *k_pages, const void *v_pages, int d) {
