@@ -47,6 +47,12 @@ struct PagedParams {
   float scale_log2;
 };
 
+// Head dim 64: the rings of an SM's blocks hold 128 KB.  With all that fits (176 to 192 KB)
+// the many short rows in flight cost bandwidth: 16 x 8000 places, one token, 16 heads 86.5
+// against 83.7 us, 8 x 16000, 40 tokens 98 against 90.  (Dim 256, few rows, wants all: 192 KB
+// 154 us, 128 KB 165, for 32 x 8000 places, 4 heads.)
+constexpr int kNarrowRing = 128 * 1024;
+
 template <int D, int BN_, int QT_>
 struct PagedCfg {
   static constexpr int kBoxes = D / 64;
@@ -55,8 +61,9 @@ struct PagedCfg {
   static constexpr int kBoxBytes = BN_ * 128;     // its 64-column box
   static constexpr int kMinBlocks = (QT_ == 1 && D <= 128) ? 2 : 1;
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
-  static constexpr int kStages = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
-  static_assert(kStages >= 4, "ring");
+  static constexpr int kStagesFit = (kSmemMax - 1024 - 512 - QT_ * kQBytes) / kTileBytes;
+  static constexpr int kStages = D == 64 ? kNarrowRing / kMinBlocks / kTileBytes : kStagesFit;
+  static_assert(kStages >= 4 && kStages <= kStagesFit, "ring");
   static constexpr int kThreads = 128 * QT_ + 64;  // softmax warps, MMA warp, TMA warp
   static constexpr int kMmaWarp = 4 * QT_, kLoadWarp = 4 * QT_ + 1;
   // S of row tile t: 128 columns from 128 t (two tiles of 64 places, or one of 128), then O
@@ -878,8 +885,9 @@ struct FewCfg {
   static constexpr int kMinBlocks = D <= 128 ? 2 : 1;
   static constexpr int kSmemMax = kMinBlocks == 2 ? 113 * 1024 : 227 * 1024;
   static constexpr int kJoinBytes = (kWarps / 2) * 16 * D * 4;
-  static constexpr int kStages = (kSmemMax - 1024 - 1024 - kJoinBytes) / (2 * kTileBytes);
-  static_assert(kStages >= 2, "ring");
+  static constexpr int kStagesFit = (kSmemMax - 1024 - 1024 - kJoinBytes) / (2 * kTileBytes);
+  static constexpr int kStages = D == 64 ? kNarrowRing / kMinBlocks / (2 * kTileBytes) : kStagesFit;
+  static_assert(kStages >= 2 && kStages <= kStagesFit, "ring");
   static constexpr int kOffRing = 0, kOffJoin = 2 * kStages * kTileBytes, kOffBar = kOffJoin + kJoinBytes;
   static constexpr int kOffMisc = kOffBar + 16 * kStages;
   static constexpr int kOffML = kOffMisc + 96;  // [kWarps][16] float2
