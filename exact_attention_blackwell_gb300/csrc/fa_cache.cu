@@ -49,12 +49,12 @@ __global__ void __launch_bounds__(128)
 // columns of the rows along the path in ascending order.  A path ascends, so
 // row i is never the source of a later move (source of move j > i is >= j), and
 // a thread touches its own columns only: no barrier is needed between moves, and
-// eight of them can be in flight (32 sequences x 32 layers, 8 heads of dim 128, paths of
-// up to 17: 17 us where one at a time took 21).  Bound by the lookups along the path and
-// then by HBM.
-constexpr int kPathChunk = 128, kMoves = 8;
+// six of them are in flight (32 sequences x 32 layers, 8 heads of dim 128, paths of up to
+// 17: 17.2 us; one at a time 21, eight with fewer blocks on an SM 17.7, k and v by one
+// block 17.4).  Bound by the lookups along the path and then by HBM.
+constexpr int kPathChunk = 128, kMoves = 6;
 
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 11)
     cache_compact_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages,
                          const __grid_constant__ PageGeom g, const int *__restrict__ accepted,
                          const int *__restrict__ n_accepted, int *__restrict__ lens_out, int max_accepted, int layers,
@@ -115,7 +115,7 @@ __device__ __forceinline__ int pages_held(int len, int page_size, int max_pages)
 
 // A block owns `cols` columns of every row, so it can read all parents' entries
 // (kept in shared memory) before it writes any.  Bound by latency: 128 rows of 2048
-// entries take 4.4 us.
+// entries take 5 us.
 __global__ void __launch_bounds__(1024)
     cache_fork_kernel(int *__restrict__ refs, int *__restrict__ table, const int *__restrict__ lens,
                       const int *__restrict__ parents, int *__restrict__ lens_out, int B, int max_pages, int num_pages,
@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(256)
 }
 
 constexpr int kMaxBookRows = 4096;  // rows whose books fit the shared memory of one block
+constexpr int kPlainSmem = 47 * 1024;  // with what is static, a launch has this much without asking
 
 size_t resize_bytes(int B) { return ((size_t)(1 + 3 * (size_t)B) * 4 + 255) & ~size_t(255); }
 
@@ -472,8 +473,8 @@ int fa_cache_fork(int *page_refs, int *page_table, const int *cache_lens, const 
   int cols = 8;  // one 32-byte sector of each row at least
   while (cols < 1024 && cols < max_pages && B * cols * 2 <= 1024) cols *= 2;
   const int smem = B * cols * 4;
-  if (cudaFuncSetAttribute(cache_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBookRows * 8 * 4) !=
-      cudaSuccess)
+  if (smem > kPlainSmem && cudaFuncSetAttribute(cache_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                kMaxBookRows * 8 * 4) != cudaSuccess)
     return FA_ERR_CUDA;
   const unsigned grid = (unsigned)((max_pages + cols - 1) / cols);
   const int threads = B * cols >= 1024 ? 1024 : (B * cols + 31) / 32 * 32;
@@ -501,12 +502,13 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
   if (!workspace || workspace_bytes < resize_bytes(B) || !ptr_aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((rc = check_device()) != FA_OK) return rc;
   int *copies = static_cast<int *>(workspace);
-  if (cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMaxBookRows * 16 + kStretch * 2) != cudaSuccess)
+  const int smem = B * 16 + kStretch * 2;
+  if (smem > kPlainSmem && cudaFuncSetAttribute(cache_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                kMaxBookRows * 16 + kStretch * 2) != cudaSuccess)
     return FA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = launch_after(cache_resize_kernel, 1, 1, kBookThreads, (size_t)B * 16 + kStretch * 2, s, page_refs, page_table,
-                    cache_lens, new_lens, lens_out, status, copies, B, max_pages, num_pages, page_size);
+  rc = launch_after(cache_resize_kernel, 1, 1, kBookThreads, smem, s, page_refs, page_table, cache_lens, new_lens,
+                    lens_out, status, copies, B, max_pages, num_pages, page_size);
   if (rc != FA_OK) return rc;
   return launch_after(cache_copy_kernel, 152 * 2, 1, 256, 0, s, static_cast<uint4 *>(k_pages),
                       static_cast<uint4 *>(v_pages), (const int *)copies, num_pages, page_size, layers, Hkv * d / 8);
