@@ -389,10 +389,10 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
 // (the first half is read twice; 128 columns in a thread's registers spilled 600 bytes,
 // a maximum for each half took 3.3 us more below), one issuing warp that
 // alternates between the row tiles (with one for each, both softmaxes ran in phase: 4100
-// instead of 3500 cycles for 128 places).
+// instead of 3500 cycles for 128 places at that time; 3100 now, of which MMAs 2048).
 // Measured with the join: 16 ragged sequences of up to 7000 places, trees of up to 33
 // tokens, 4 kv heads of dim 256: 48 us, 4.8 TB/s; one of 32768 places, 64 tokens, 32 on 8
-// heads of dim 128: 37.5 us, 920 TFLOP/s; of both 9 to 15 us are set-up, the first tiles, the
+// heads of dim 128: 36.5 us, 940 TFLOP/s; of both 13 to 14 us are set-up, the first tiles, the
 // parts' way out and the join.
 template <int D, int BN, int QT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 // has a head to itself and nothing to join.
 // Measured with the join: 64 sequences of up to 8192 places, one token each, 32 on 8
 // heads of dim 128: 153.5 us, 6.7 TB/s (the tcgen05 kernel: 164); 32 of up to 2500,
-// chains of up to 7, 16 heads of dim 64: 34.5 us, 4.8 TB/s, of which some 9 are set-up,
+// chains of up to 7, 16 heads of dim 64: 32.4 us, 5.1 TB/s, of which some 8 are set-up,
 // the first tiles and the join.
 template <int D>
 struct FewCfg {
