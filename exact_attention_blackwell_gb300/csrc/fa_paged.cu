@@ -1247,7 +1247,7 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
 // join-th part each, U of them in flight.  Parts are stored column by column, so that
 // neighbouring tasks are contiguous for the kernels' stores and the loads here.  Bound
 // by latency: launch, the item's place, two rounds of loads from L2; 5 us after the main
-// kernel for 8 items of 256 rows in 19 parts each (21 MB, 13 us from DRAM).  At 72
+// kernel for 8 items of 256 rows in 19 parts each (21 MB, 10 us from DRAM).  At 72
 // registers those 1024 blocks run at once (80: 38.0 instead of 37.4 us for the call).
 constexpr int kJoinWarps = 8;  // at most; four unless all eight share their tasks
 // Blocks of four warps: some 6 to 7 run at once on an SM, and many items are whole or
