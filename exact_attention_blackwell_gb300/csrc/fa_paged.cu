@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "fa_paged.h"
+#include "paged_seq.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -101,19 +102,8 @@ enum PagedSite : int {
   kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39, kPSiteVTail = 40
 };
 
-// Sequence b: its first new token, their number, places cached, places in all.
-struct PagedSeq {
-  int start, n, len, keys;
-};
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
-  PagedSeq s;
-  const long long cap = (long long)p.g.max_pages * p.g.page_size;
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  s.start = max(0, min(c0, p.total));
-  s.n = max(0, min(min(c1, p.total) - s.start, p.max_new));
-  s.len = (int)max(0ll, min((long long)p.g.cache_lens[b], cap));
-  s.keys = (int)min((long long)s.len + s.n, cap);
-  return s;
+  return paged_seq_of(p.cu[b], p.cu[b + 1], p.g.cache_lens[b], p.total, p.max_new, p.g.max_pages * p.g.page_size);
 }
 __device__ __forceinline__ void paged_units(const PagedParams &p, const PagedSeq &s, int &tiles, int &groups) {
   tiles = (s.keys + (1 << p.bn_log2) - 1) >> p.bn_log2;
