@@ -16,14 +16,20 @@
 namespace fa {
 namespace {
 
+// These kernels begin while the kernel before them may still be writing what they read
+// (launch_after): so no pointer here is __restrict__.  That would promise that its contents
+// hold for the whole kernel, and a load through it could come before grid_wait or from a
+// cache that is not kept in step.
+
 // ------------------------------------------------------------------ append
 // One warp per token: rows of Hkv * d bf16 of k and v, 16 bytes a lane and step.
 // Bound by HBM: 131 thousand tokens of 16 heads of dim 128 take 311 us, 6.9 TB/s; a decoding
 // step of 64 tokens 2.6 us, which is launching and a chain of three loads.
+constexpr int kAppendSteps = 4;  // 16-byte pieces of k and of v that a lane has in flight
+
 __global__ void __launch_bounds__(128)
-    cache_append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, uint4 *__restrict__ k_pages,
-                        uint4 *__restrict__ v_pages, const __grid_constant__ PageGeom g, const int *__restrict__ cu,
-                        int total, int chunks) {
+    cache_append_kernel(const uint4 *k, const uint4 *v, uint4 *k_pages, uint4 *v_pages,
+                        const __grid_constant__ PageGeom g, const int *cu, int total, int chunks) {
   grid_go();
   grid_wait();
   const int lane = threadIdx.x & 31;
@@ -38,9 +44,20 @@ __global__ void __launch_bounds__(128)
   const size_t row = (size_t)page * g.page_size + (size_t)((len + i) % g.page_size);
   const uint4 *ks = k + (size_t)t * chunks, *vs = v + (size_t)t * chunks;
   uint4 *kd = k_pages + row * chunks, *vd = v_pages + row * chunks;
-  for (int c = lane; c < chunks; c += 32) {
-    kd[c] = ks[c];
-    vd[c] = vs[c];
+  for (int c0 = lane; c0 < chunks; c0 += 32 * kAppendSteps) {
+    uint4 x[kAppendSteps], y[kAppendSteps];
+#pragma unroll
+    for (int u = 0; u < kAppendSteps; ++u)
+      if (const int c = c0 + 32 * u; c < chunks) {
+        x[u] = ks[c];
+        y[u] = vs[c];
+      }
+#pragma unroll
+    for (int u = 0; u < kAppendSteps; ++u)
+      if (const int c = c0 + 32 * u; c < chunks) {
+        kd[c] = x[u];
+        vd[c] = y[u];
+      }
   }
 }
 
@@ -55,10 +72,8 @@ __global__ void __launch_bounds__(128)
 constexpr int kPathChunk = 128, kMoves = 6;
 
 __global__ void __launch_bounds__(128, 11)
-    cache_compact_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages,
-                         const __grid_constant__ PageGeom g, const int *__restrict__ accepted,
-                         const int *__restrict__ n_accepted, int *__restrict__ lens_out, int max_accepted, int layers,
-                         int chunks) {
+    cache_compact_kernel(uint4 *k_pages, uint4 *v_pages, const __grid_constant__ PageGeom g, const int *accepted,
+                         const int *n_accepted, int *lens_out, int max_accepted, int layers, int chunks) {
   __shared__ long long s_src[kPathChunk], s_dst[kPathChunk];
   __shared__ int s_bad;
   grid_go();
@@ -117,9 +132,8 @@ __device__ __forceinline__ int pages_held(int len, int page_size, int max_pages)
 // (kept in shared memory) before it writes any.  Bound by latency: 128 rows of 2048
 // entries take 5 us.
 __global__ void __launch_bounds__(1024)
-    cache_fork_kernel(int *__restrict__ refs, int *__restrict__ table, const int *__restrict__ lens,
-                      const int *__restrict__ parents, int *__restrict__ lens_out, int B, int max_pages, int num_pages,
-                      int page_size, int cols) {
+    cache_fork_kernel(int *refs, int *table, const int *lens, const int *parents, int *lens_out, int B, int max_pages,
+                      int num_pages, int page_size, int cols) {
   extern __shared__ int fresh[];  // [B, cols]
   grid_go();
   grid_wait();
@@ -183,9 +197,8 @@ __device__ int block_scan(int x, int *warp_sums, int *total) {
 
 // copies: [0] their number, then (from, to, rows) for each
 __global__ void __launch_bounds__(kBookThreads)
-    cache_resize_kernel(int *__restrict__ refs, int *__restrict__ table, const int *__restrict__ lens,
-                        const int *__restrict__ new_lens, int *__restrict__ lens_out, int *__restrict__ status,
-                        int *__restrict__ copies, int B, int max_pages, int num_pages, int page_size) {
+    cache_resize_kernel(int *refs, int *table, const int *lens, const int *new_lens, int *lens_out, int *status,
+                        int *copies, int B, int max_pages, int num_pages, int page_size) {
   extern __shared__ int sm[];
   int *had = sm, *want = sm + B;              // lengths; -1 in both where the row is refused
   int *last = sm + 2 * B;   // a growing row's shared partial page (or -1)
@@ -360,8 +373,8 @@ __global__ void __launch_bounds__(kBookThreads)
 constexpr int kCopyChunk = 2048;
 
 __global__ void __launch_bounds__(256)
-    cache_copy_kernel(uint4 *__restrict__ k_pages, uint4 *__restrict__ v_pages, const int *__restrict__ copies,
-                      int num_pages, int page_size, int layers, int chunks) {
+    cache_copy_kernel(uint4 *k_pages, uint4 *v_pages, const int *copies, int num_pages, int page_size, int layers,
+                      int chunks) {
   grid_go();
   grid_wait();
   const int page_chunks = page_size * chunks;
