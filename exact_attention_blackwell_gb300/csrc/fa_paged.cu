@@ -102,8 +102,13 @@ enum PagedSite : int {
   kPSiteSFull = 36, kPSiteOFull = 37, kPSiteDrain = 38, kPSiteQFree = 39, kPSiteVTail = 40
 };
 
+// EARLY: before the kernel's grid_wait (the join's), from L2, so that no line is used which an
+// SM's L1 still holds from before these arrays were written.
+template <bool EARLY = false>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
-  return paged_seq_of(p.cu[b], p.cu[b + 1], p.g.cache_lens[b], p.total, p.max_new, p.g.max_pages * p.g.page_size);
+  auto at = [](const int *x) { return EARLY ? __ldcg(x) : *x; };
+  return paged_seq_of(at(p.cu + b), at(p.cu + b + 1), at(p.g.cache_lens + b), p.total, p.max_new,
+                      p.g.max_pages * p.g.page_size);
 }
 __device__ __forceinline__ void paged_units(const PagedParams &p, const PagedSeq &s, int &tiles, int &groups) {
   tiles = (s.keys + (1 << p.bn_log2) - 1) >> p.bn_log2;
@@ -148,11 +153,12 @@ struct WarpUnits {
   PagedSeq s;
   unsigned before, after, total;
 };
+template <bool EARLY = false>
 __device__ __forceinline__ WarpUnits warp_units(const PagedParams &p) {
   const int lane = threadIdx.x & 31;
   WarpUnits w;
   w.s = {0, 0, 0, 0};
-  if (lane < p.g.B) w.s = paged_seq(p, lane);
+  if (lane < p.g.B) w.s = paged_seq<EARLY>(p, lane);
   const unsigned x = (unsigned)units_of(p, w.s);
   w.after = x;
 #pragma unroll
@@ -1230,9 +1236,10 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
 }
 
 // Joins the parts of the items that were cut.  Blocks go by (item, chunks of it); one
-// warp finds out where the item's parts are (before the wait for the main kernel as
-// far as the call's inputs tell), the others take it from there: the search for
-// every row by every thread was half of this kernel's time.  A task is COLS columns
+// warp finds out where the item's parts are, the others take it from there: the search
+// for every row by every thread was half of this kernel's time.  With up to 32 sequences
+// that is before the wait for the main kernel, on lengths read from L2; with more, all is
+// read after it.  A task is COLS columns
 // of one row; with many parts (SHARED) p.join warps share 32 tasks and take every
 // join-th part each, U of them in flight.  Parts are stored column by column, so that
 // neighbouring tasks are contiguous for the kernels' stores and the loads here.  Bound
@@ -1249,6 +1256,7 @@ template <int D, bool SHARED>
 __global__ void __maxnreg__(SHARED ? 72 : 80) paged_combine_kernel(const __grid_constant__ PagedParams p, int blocks) {
   constexpr int COLS = 8, U = 4;  // one 16-byte store a task
   __shared__ float s_part[SHARED ? kJoinWarps : 1][COLS + 2][32];
+  __shared__ PagedSeq s_seq;
   __shared__ unsigned s_u0, s_total;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int GG = p.HB * p.G, all = p.QT * p.TB * GG;
@@ -1256,21 +1264,33 @@ __global__ void __maxnreg__(SHARED ? 72 : 80) paged_combine_kernel(const __grid_
   const int rg = min((int)blockIdx.y / p.join_y, p.groups - 1);
   const int chunk0 = (int)blockIdx.y - rg * p.join_y;
   const int chunk_step = rg < p.groups - 1 ? p.join_y : (int)gridDim.y - (p.groups - 1) * p.join_y;
-  const PagedSeq s = paged_seq(p, b);
-  const int tok0 = rg * p.QT * p.TB, rows = min(s.n - tok0, p.QT * p.TB) * GG;
-  int tiles, groups;
-  paged_units(p, s, tiles, groups);
+  // Up to 32 sequences: one warp fetches what the call's tables say of the sequence and of the units before it,
+  // before the wait, so that blocks with nothing to join can end.  More: after it, together with p.prefix.
+  PagedSeq s;
   long long u0 = 0, total = 0;
   if (p.by_warp) {
     if (warp == 0) {
-      const WarpUnits w = warp_units(p);
-      if (lane == b) s_u0 = w.before;
+      const WarpUnits w = warp_units<true>(p);
+      if (lane == b) {
+        s_seq = w.s;
+        s_u0 = w.before;
+      }
       if (lane == 0) s_total = w.total;
     }
     __syncthreads();
+    s = s_seq;
     u0 = s_u0;
     total = s_total;
+  } else {
+    grid_go();
+    grid_wait();
+    u0 = p.prefix[b];
+    total = p.prefix[p.g.B];
+    s = paged_seq(p, b);
   }
+  const int tok0 = rg * p.QT * p.TB, rows = min(s.n - tok0, p.QT * p.TB) * GG;
+  int tiles, groups;
+  paged_units(p, s, tiles, groups);
   // the item's parts: from the block with its first tile on
   int c0 = 0, parts = 0, first = 0;
   auto find_parts = [&] {
@@ -1281,19 +1301,16 @@ __global__ void __maxnreg__(SHARED ? 72 : 80) paged_combine_kernel(const __grid_
     // item's units (the one before them is a tile), and this is its second part
     first = 2 * c0 + (at > c0 * per ? 1 : 0);
   };
-  if (p.by_warp && rows > 0) find_parts();
-  grid_go();
+  if (rows > 0) find_parts();
   // Nothing to join: no such row group, or one block had it all and has written the result.  The first
   // block waits in any case, so that the grid does not end before the main kernel has.
-  if ((rows <= 0 || parts == 1) && (blockIdx.x | blockIdx.y) != 0) return;
-  grid_wait();
-  if (rows <= 0) return;
-  if (!p.by_warp) {
-    u0 = p.prefix[b];
-    total = p.prefix[p.g.B];
-    find_parts();
+  const bool idle = rows <= 0 || parts == 1;
+  if (p.by_warp) {
+    grid_go();
+    if (idle && (blockIdx.x | blockIdx.y) != 0) return;
+    grid_wait();
   }
-  if (parts == 1) return;
+  if (idle) return;
   const int share = warp % p.join, tasks = rows * (D / COLS), step = (int)blockDim.x / p.join;
   for (int base = chunk0 * step; base < tasks; base += chunk_step * step) {
     const int task = base + warp / p.join * 32 + lane;

@@ -120,3 +120,15 @@ def test_append_reads_the_keys_of_the_kernel_before():
         fa.cache_compact(*deep, s.t_table, s.t_lens, path, kept)
         fa.cache_append(deep[0][-1, p], deep[1][-1, p], to_k, to_v, i32([[0]]), i32([0]), cu)
         assert torch.equal(bits(to_k[0]), bits(want[p]))
+
+
+def test_the_join_reads_the_lengths_from_l2_before_its_wait():
+    """The join looks at cu_seqlens and cache_lens before it waits for the main kernel: past L1, which may still
+    hold lines from before these arrays were written."""
+    text = open(os.path.join(CSRC, "fa_paged.cu")).read()
+    join = text[text.index("paged_combine_kernel(const __grid_constant__"):]
+    early = join[: join.index("grid_wait();")]
+    assert "warp_units<true>(p)" in early
+    assert not re.search(r"paged_seq\(|warp_units\(|p\.cu\b|cache_lens|page_table|p\.mask|prefix\[", early)
+    seq = text[text.index("PagedSeq paged_seq(const PagedParams"):]
+    assert "EARLY ? __ldcg(x) : *x" in seq[: seq.index("\n}\n")]
