@@ -542,8 +542,9 @@ def cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, str
     dev = _same_device(_check("k", k, torch.bfloat16, (total, Hkv, d)), _check("v", v, torch.bfloat16, (total, Hkv, d)),
                        *pages, *table, _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
     with _On(dev, stream):
-        _done(fa_cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, B, max_pages, num_pages,
-                              page_size, total, Hkv, d), "fa_cache_append")
+        if total > 0:
+            _done(fa_cache_append(k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, B, max_pages, num_pages,
+                                  page_size, total, Hkv, d), "fa_cache_append")
 
 
 def attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens, max_new, tree_mask=None, scale=None,

@@ -432,7 +432,8 @@ extern "C" {
 int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, const int *page_table,
                     const int *cache_lens, const int *cu_seqlens, int B, int max_pages, int num_pages, int page_size,
                     int total, int Hkv, int d, void *stream) {
-  if (!k || !v || !k_pages || !v_pages || !page_table || !cache_lens || !cu_seqlens) return FA_ERR_INVALID_ARG;
+  if (!k_pages || !v_pages || !page_table || !cache_lens || !cu_seqlens) return FA_ERR_INVALID_ARG;
+  if (total != 0 && (!k || !v)) return FA_ERR_INVALID_ARG;
   int rc = check_page_table(B, max_pages, num_pages, page_size);
   if (rc == FA_OK) rc = check_page_rows(1, num_pages, page_size, Hkv, d);
   if (rc != FA_OK) return rc;

@@ -235,7 +235,8 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
 /* New keys and values into the cache: packed rows k, v bf16 [total, Hkv, d],
  * sequence b being rows [cu_seqlens[b], cu_seqlens[b+1]) (DEVICE int32 [B + 1],
  * as for fa_fwd_varlen); row i of sequence b goes to place cache_lens[b] + i.
- * Rows past the table, or whose page entry names no page, are dropped. */
+ * Rows past the table, or whose page entry names no page, are dropped.  Without
+ * rows (total = 0) k and v are not looked at and may be NULL. */
 int fa_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, const int *page_table,
                     const int *cache_lens, const int *cu_seqlens, int B, int max_pages, int num_pages,
                     int page_size, int total, int Hkv, int d, void *stream);
