@@ -596,7 +596,7 @@ def cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted
     [num_pages,page_size,Hkv,d], or with a leading [layers]): the rows of place cache_lens[b] +
     accepted[b, i] go to place cache_lens[b] + i for i < n_accepted[b] -> new lengths int32 [B].
     accepted int32 [B,max_accepted] ascends along each path; a path ends before the first entry that
-    does not."""
+    does not.  Without columns (no token accepted anywhere) the lengths are copied and nothing moves."""
     if stream is None:
         lens = (_fast or _paged_binding()).compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted)
         if lens is not None:
@@ -611,6 +611,8 @@ def cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted
     dev = _same_device(*pages, *table, _check("accepted", accepted, torch.int32, (B, most)),
                        _check("n_accepted", n_accepted, torch.int32, (B,)))
     with _On(dev, stream):
+        if most == 0:  # no path has a token
+            return cache_lens.clone()
         lens = torch.empty_like(cache_lens)
         _done(fa_cache_compact(k_pages, v_pages, page_table, cache_lens, accepted, n_accepted, lens, B, most, max_pages,
                                num_pages, page_size, layers, Hkv, d), "fa_cache_compact")

@@ -161,6 +161,7 @@ PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const Cache c(o, a[0], a[1], a[2], a[3], true);
   const at::Tensor *path = o.take(a[4], at::kInt, 2, 2), *kept = o.take(a[5], at::kInt, 1, 1);
   if (!o.current() || path->size(0) != c.B || kept->size(0) != c.B) Py_RETURN_NONE;
+  if (path->size(1) == 0) return THPVariable_Wrap(c.lens->clone());  // no path has a token
   at::Tensor lens = at::empty({c.B}, c.lens->options());
   const int status = g_compact(c.k->data_ptr(), c.v->data_ptr(), ints(c.table), ints(c.lens), ints(path), ints(kept),
                                ints(&lens), c.B, size(path, 1), c.max_pages, c.num_pages, c.page_size, c.layers, c.Hkv, c.d,

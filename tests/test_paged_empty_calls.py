@@ -51,6 +51,21 @@ def test_append_of_no_rows(where):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layers", [None, 2])
+def test_compact_of_no_tokens(where, layers):
+    s = pm.Setup([10, 30], [4, 0], 16, 2, 64, seed=4, layers=layers, fill=3.0)
+    k, v = s.k_pages.clone(), s.v_pages.clone()
+    lens = i32([10, -4])
+    path = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for counts in ([0, 0], [3, -1]):  # a path is no longer than its columns
+        out = fa.cache_compact(s.k_pages, s.v_pages, s.t_table, lens, path, i32(counts), **where)
+        torch.cuda.synchronize()
+        assert out.tolist() == [10, -4] and out.dtype == torch.int32 and out.data_ptr() != lens.data_ptr()
+    assert torch.equal(s.k_pages, k) and torch.equal(s.v_pages, v)
+
+
+@pytest.mark.gpu
 def test_attention_of_no_tokens(where):
     s = pm.Setup([10, 30], [0, 0], 16, 2, 64, seed=4, H=4)
     for mask in (None, torch.zeros((0, 1), dtype=torch.int64, device="cuda")):
