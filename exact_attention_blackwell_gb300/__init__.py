@@ -516,6 +516,14 @@ def _workspace(given, nbytes, dev):
     return given, given.numel() * given.element_size()
 
 
+def _int32(name, x):
+    """x as the C int that the entry points take (ctypes would cut off what does not fit)."""
+    x = int(x)
+    if not -(2**31) <= x < 2**31:
+        raise ValueError(f"{name} must fit 32 bits, is {x}")
+    return x
+
+
 def _check_workspace(workspace):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -567,7 +575,7 @@ def attention_fwd_paged(q, k_pages, v_pages, page_table, cache_lens, cu_seqlens,
     if q.dim() != 3:
         raise ValueError("q must be [total, H, d]")
     total, H, _ = q.shape
-    max_new = int(max_new)
+    max_new = _int32("max_new", max_new)
     words = (max_new + 63) // 64 if tree_mask is not None else 0
     c = [_check("q", q, torch.bfloat16, (total, H, d)), *pages, *table,
          _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))]
@@ -633,11 +641,12 @@ def cache_fork(page_refs, page_table, cache_lens, parents, page_size, stream=Non
     if page_refs.dim() != 1:
         raise ValueError("page_refs must be [num_pages]")
     num_pages = page_refs.shape[0]
+    page_size = _int32("page_size", page_size)
     dev = _same_device(_check("page_refs", page_refs, torch.int32, (num_pages,)), *table,
                        _check("parents", parents, torch.int32, (B,)))
     with _On(dev, stream):
         lens = torch.empty_like(cache_lens)
-        _done(fa_cache_fork(page_refs, page_table, cache_lens, parents, lens, B, max_pages, num_pages, int(page_size)),
+        _done(fa_cache_fork(page_refs, page_table, cache_lens, parents, lens, B, max_pages, num_pages, page_size),
               "fa_cache_fork")
     return lens
 
