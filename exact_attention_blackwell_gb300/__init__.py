@@ -479,6 +479,13 @@ def _check_table(page_table, cache_lens):
 _fast = None
 
 
+class _NoBinding:
+    """Where no binding fits (none was built, or one for another torch): every call takes the code below,
+    which costs some 10 us more on the host."""
+
+    append = attention = compact = fork = resize = staticmethod(lambda *operands: None)
+
+
 def _paged_binding():
     global _fast
     if _fast is None:
@@ -488,15 +495,21 @@ def _paged_binding():
 
         from . import build
 
-        path = build.binding_path(torch)
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with exact_attention_blackwell_gb300.build.build()")
-        spec = importlib.util.spec_from_file_location("_paged_binding", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.connect(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
-            "fa_cache_append", "fa_fwd_paged_workspace_bytes", "fa_fwd_paged", "fa_cache_compact", "fa_cache_fork",
-            "fa_cache_resize_workspace_bytes", "fa_cache_resize")))
+        l = lib()
+        try:
+            spec = importlib.util.spec_from_file_location("_paged_binding", build.binding_path(torch))
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except ImportError as e:
+            import warnings
+
+            warnings.warn(f"paged-cache calls go through ctypes, some 10 us slower on the host: {e}", RuntimeWarning,
+                          stacklevel=3)
+            module = _NoBinding
+        else:
+            module.connect(*(ctypes.cast(getattr(l, name), ctypes.c_void_p).value for name in (
+                "fa_cache_append", "fa_fwd_paged_workspace_bytes", "fa_fwd_paged", "fa_cache_compact", "fa_cache_fork",
+                "fa_cache_resize_workspace_bytes", "fa_cache_resize")))
         _fast = module
     return _fast
 

@@ -5,7 +5,7 @@ then linked into one shared library with the CUDA runtime linked statically,
 so the C ABI of ``include/fa.h`` is the only interface.  The torch helpers of the
 paged cache have their ordinary call in a small CPython module beside it
 (``csrc/paged_binding.cpp``), compiled with the host compiler against the
-installed torch and named after its version.
+installed torch, where there is one, and named after its version.
 """
 from __future__ import annotations
 
@@ -44,20 +44,29 @@ def binding_path(torch) -> str:
     return os.path.join(HERE, "_paged_binding_" + re.sub(r"[^0-9A-Za-z]", "_", torch.__version__) + ".so")
 
 
-def build_binding(force: bool = False) -> str:
-    import torch
-
+def build_binding(force: bool = False) -> str | None:
+    """Path of the binding, or None where it cannot be built: no torch with CUDA, its headers, Python's, or a host
+    compiler.  The C library needs none of them, and without the binding the helpers call it through ctypes."""
+    try:
+        import torch
+    except ImportError:
+        return None
     path = binding_path(torch)
     header = os.path.join(os.path.dirname(HERE), "include", "fa.h")
     if not force and os.path.exists(path) and os.path.getmtime(path) >= max(map(os.path.getmtime, (BINDING_SRC, header))):
         return path
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
-    libs = os.path.join(root, "lib")
+    libs, include, python = os.path.join(root, "lib"), os.path.join(root, "include"), sysconfig.get_paths()["include"]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    needs = (os.path.join(include, "torch", "csrc", "autograd", "python_variable.h"), os.path.join(python, "Python.h"),
+             os.path.join(libs, "libc10_cuda.so"))
+    if not cxx or not all(map(os.path.exists, needs)):
+        return None
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{os.path.join(root, 'include')}",
-           f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{sysconfig.get_paths()['include']}",
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{include}",
+           f"-I{os.path.join(include, 'torch', 'csrc', 'api', 'include')}", f"-I{python}",
            f"-I{cuda}", BINDING_SRC, "-o", tmp, f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -96,14 +105,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(build_binding, force) if lib_path == LIB_PATH else None
         objs = list(ex.map(compile_one, srcs))
-        if binding is not None:
-            binding.result()
     tmp = lib_path + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs,
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if binding is not None:
+        binding.result()  # raises where it was compiled and failed; the library is there in any case
     return lib_path
 
 
