@@ -5,7 +5,7 @@ then linked into one shared library with the CUDA runtime linked statically,
 so the C ABI of ``include/fa.h`` is the only interface.  The torch helpers of the
 paged cache have their ordinary call in a small CPython module beside it
 (``csrc/paged_binding.cpp``), compiled with the host compiler against the
-installed torch, where there is one, and named after its version.
+installed torch, where there is one, and named after its version and Python's ABI.
 """
 from __future__ import annotations
 
@@ -41,7 +41,9 @@ BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
 
 
 def binding_path(torch) -> str:
-    return os.path.join(HERE, "_paged_binding_" + re.sub(r"[^0-9A-Za-z]", "_", torch.__version__) + ".so")
+    """Named after torch's version and the interpreter's ABI: it is compiled against both."""
+    abi = sysconfig.get_config_var("EXT_SUFFIX") or ".so"
+    return os.path.join(HERE, "_paged_binding_" + re.sub(r"[^0-9A-Za-z]", "_", torch.__version__) + abi)
 
 
 def build_binding(force: bool = False) -> str | None:

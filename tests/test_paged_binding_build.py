@@ -4,6 +4,7 @@ import builtins
 import os
 import shutil
 import subprocess
+import types
 import warnings
 
 import pytest
@@ -21,6 +22,17 @@ def lib():
 def test_it_is_built_and_loaded_here():
     assert os.path.exists(fa_build.build_binding())
     assert fa._paged_binding().__name__ == "_paged_binding" and callable(fa._paged_binding().attention)
+
+
+def test_each_interpreter_and_torch_has_its_own(monkeypatch):
+    names = set()
+    for abi in (".cpython-312-x86_64-linux-gnu.so", ".cpython-313-x86_64-linux-gnu.so", ".cpython-312-aarch64-linux-gnu.so"):
+        for version in ("2.9.1+cu130", "2.11.0+cu130"):
+            monkeypatch.setattr(fa_build.sysconfig, "get_config_var", lambda name: abi)
+            path = fa_build.binding_path(types.SimpleNamespace(__version__=version))
+            assert path.endswith(abi)
+            names.add(path)
+    assert len(names) == 6
 
 
 def without_torch(monkeypatch):
