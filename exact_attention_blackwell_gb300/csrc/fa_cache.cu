@@ -23,7 +23,7 @@ namespace {
 
 // ------------------------------------------------------------------ append
 // One warp per token: rows of Hkv * d bf16 of k and v, 16 bytes a lane and step.
-// Bound by HBM: 131 thousand tokens of 16 heads of dim 128 take 311 us, 6.9 TB/s; a decoding
+// Bound by HBM: 131 thousand tokens of 16 heads of dim 128 take 309 us, 6.95 TB/s; a decoding
 // step of 64 tokens 2.6 us, which is launching and a chain of three loads.
 constexpr int kAppendSteps = 4;  // 16-byte pieces of k and of v that a lane has in flight
 
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(128)
 // row i is never the source of a later move (source of move j > i is >= j), and
 // a thread touches its own columns only: no barrier is needed between moves, and
 // six of them are in flight (32 sequences x 32 layers, 8 heads of dim 128, paths of up to
-// 17: 17.2 us; one at a time 21, eight with fewer blocks on an SM 17.7, k and v by one
-// block 17.4).  Bound by the lookups along the path and then by HBM.
+// 17, replayed in a graph: 17.2 us; one at a time 21, eight with fewer blocks on an SM 17.7,
+// k and v by one block 17.4; a call among others 16.0, the kernel alone under ncu 15.5).  Bound by the lookups along the path and then by HBM.
 constexpr int kPathChunk = 128, kMoves = 6;
 
 __global__ void __launch_bounds__(128, 11)
@@ -167,8 +167,10 @@ __global__ void __launch_bounds__(1024)
 // growing rows' needs are summed, then free pages are handed out lowest first.
 // The block's time is a chain of loads, each about 0.6 us; so lengths are kept in
 // shared memory, and the counts of the first pages are fetched with them and used
-// where no row shrinks.  48 rows growing by up to 40 places and shrinking again take 16 us
-// in two calls.
+// where no row shrinks.  48 rows growing by up to 40 places and shrinking again take 17.6 us
+// in two calls in a graph; 64 rows taking 640 pages and giving them back 12.5 us with the free
+// pages in front and 55 where they follow 198000 held ones (13 stretches, read one after
+// another).
 constexpr int kBookThreads = 1024;
 constexpr int kPagesPerThread = 16, kStretch = kBookThreads * kPagesPerThread;
 

@@ -377,8 +377,13 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
 // Softmax with one pass over the keys: per row the running maximum m and sum l of
 // exp2(c2 S - m), O rescaled only where m grows by more than kRescaleTau.  Warps: 4 QT
 // of softmax (a thread to a row), one that issues tcgen05 MMAs, one that fetches tiles
-// page by page.  A byte of the cache meets 2 * rows FLOPs, so up to some 280 rows HBM is
-// the bound, and from 128 rows on the softmax: each place of a row costs an ex2.
+// page by page.  A byte of the cache meets `rows` FLOPs (an element 2 * rows), so up to some
+// 280 rows HBM is the bound, and from 128 rows on the softmax: each place of a row costs an
+// ex2.  P goes to P V in bf16, the type that V has there: each weight within 2^-8 of itself
+// (half a step), relative to the row's maximum.  The row sum takes the unrounded weights, so
+// that rounding does not shift it too.  O's error against 64 bits is 0.0023 of its norm, where
+// fp32 weights with one rounding at the end have 0.0017; they would need V widened in shared
+// memory and half the MMA rate.
 // One row tile: two blocks on an SM (head dims 64 and 128), tiles of 64 places, S one
 // tile ahead of the softmax.  Two: one block, 128 places (at 64 columns an MMA step costs
 // what it costs at 128), the softmax 64 columns at a time with one maximum for all 128
@@ -387,8 +392,8 @@ __device__ __noinline__ void add_unfinite(const PagedParams &p, const PagedSeq &
 // alternates between the row tiles (with one for each, both softmaxes ran in phase: 4100
 // instead of 3500 cycles for 128 places at that time; 3100 now, of which MMAs 2048).
 // Measured with the join: 16 ragged sequences of up to 7000 places, trees of up to 33
-// tokens, 4 kv heads of dim 256: 48 us, 4.8 TB/s; one of 32768 places, 64 tokens, 32 on 8
-// heads of dim 128: 36.5 us, 940 TFLOP/s; of both 13 to 14 us are set-up, the first tiles, the
+// tokens, 4 kv heads of dim 256: 49 us, 4.7 TB/s; one of 32768 places, 64 tokens, 32 on 8
+// heads of dim 128: 37 us, 930 TFLOP/s; of both 13 to 14 us are set-up, the first tiles, the
 // parts' way out and the join.
 template <int D, int BN, int QT>
 __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN, QT>::kMinBlocks)
@@ -870,8 +875,8 @@ __global__ void __launch_bounds__(PagedCfg<D, BN, QT>::kThreads, PagedCfg<D, BN,
 // together keeps DRAM pages and 256-byte L2 lines whole, and with HB = 4 each warp
 // has a head to itself and nothing to join.
 // Measured with the join: 64 sequences of up to 8192 places, one token each, 32 on 8
-// heads of dim 128: 153.5 us, 6.7 TB/s (the tcgen05 kernel: 164); 32 of up to 2500,
-// chains of up to 7, 16 heads of dim 64: 32.4 us, 5.1 TB/s, of which some 8 are set-up,
+// heads of dim 128: 154 to 156 us, 6.6 TB/s (the tcgen05 kernel: 164); 32 of up to 2500,
+// chains of up to 7, 16 heads of dim 64: 33 us, 5.0 TB/s, of which some 8 are set-up,
 // the first tiles and the join.
 template <int D>
 struct FewCfg {
@@ -1022,7 +1027,8 @@ __global__ void __launch_bounds__(FewCfg<D>::kThreads, FewCfg<D>::kMinBlocks)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
             top[hf] = fmaxf(fmaxf(s[0][2 * hf], s[0][2 * hf + 1]), fmaxf(s[1][2 * hf], s[1][2 * hf + 1])) * c2;
-          // the maximum moves only where a score is more than kRescaleTau above it (at first: above -inf)
+          // the maximum moves only where a score is more than kRescaleTau above it (at first: above -inf);
+          // the weights below go to P V in bf16 (2^-8 each), to the row sum unrounded, as in paged_fwd_kernel
           if (__any_sync(0xffffffffu, top[0] - m_ref[0] > kRescaleTau || top[1] - m_ref[1] > kRescaleTau)) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
