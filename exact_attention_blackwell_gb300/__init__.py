@@ -48,6 +48,13 @@ SIGNATURES = {
     "fa_cache_fork": (_I, [_P] * 5 + [_I] * 4 + [_P]),
     "fa_cache_resize_workspace_bytes": (_SZ, [_I]),
     "fa_cache_resize": (_I, [_P] * 8 + [_I] * 7 + [_P, _SZ, _P]),
+    "fa_qk_norm_rope": (_I, [_P, _LL, _LL] * 2 + [_P, _I, _P, _I, _P, _P, _P, _I, _F, _I, _P, _P] + [_I] * 4 + [_P]),
+    "fa_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I]),
+    "fa_qk_norm_rope_bwd": (_I, [_P, _LL, _LL] * 4 + [_P, _I, _P, _I, _P, _P, _P, _I, _F, _I] + [_P] * 4 + [_I] * 4
+                            + [_P, _SZ, _P]),
+    "fa_cache_append_rope": (_I, [_P, _LL, _LL] * 3 + [_P] * 6 + [_I, _P, _I, _P, _P, _P, _I, _F, _I, _P] + [_I] * 8 + [_P]),
+    "fa_attention_weights_paged": (_I, [_P] * 6 + [_I, _P, _P, _I, _F] + [_I] * 9 + [_F, _P]),
+    "fa_cache_evict": (_I, [_P] * 6 + [_I] * 3 + [_P] * 2 + [_I] * 7 + [_P]),
     "fa_exp2_poly": (_I, [_P, _P, _LL, _P]),
     "fa_last_device_status": (_I, [_P]),
     "fa_last_device_status_site": (_I, [_P, _P]),
@@ -222,6 +229,60 @@ def fa_cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_len
     return lib().fa_cache_resize(_ptr(page_refs), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens),
                                  _ptr(new_lens), _ptr(lens_out), _ptr(status), B, max_pages, num_pages, page_size,
                                  layers, Hkv, d, _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def _axes(axes):
+    """axes as the HOST array of ints the entry points take."""
+    return None if axes is None else (ctypes.c_int * len(axes))(*axes)
+
+
+def fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, positions, n_axes, inv_freq, rot, axes, q_weight, k_weight,
+                    bf16_weights, eps, interleaved, q_out, k_out, total, H, Hkv, d, stream=None) -> int:
+    return lib().fa_qk_norm_rope(_ptr(q), q_token, q_head, _ptr(k), k_token, k_head, _ptr(positions), n_axes,
+                                 _ptr(inv_freq), rot, _axes(axes), _ptr(q_weight), _ptr(k_weight), int(bool(bf16_weights)),
+                                 float(eps), int(bool(interleaved)), _ptr(q_out), _ptr(k_out), total, H, Hkv, d,
+                                 _stream(stream))
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(d) -> int:
+    return int(lib().fa_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+def fa_qk_norm_rope_bwd(dq_out, dq_token, dq_head, dk_out, dk_token, dk_head, q, q_token, q_head, k, k_token, k_head,
+                        positions, n_axes, inv_freq, rot, axes, q_weight, k_weight, bf16_weights, eps, interleaved, dq, dk,
+                        dq_weight, dk_weight, total, H, Hkv, d, workspace, workspace_bytes, stream=None) -> int:
+    return lib().fa_qk_norm_rope_bwd(_ptr(dq_out), dq_token, dq_head, _ptr(dk_out), dk_token, dk_head, _ptr(q), q_token,
+                                     q_head, _ptr(k), k_token, k_head, _ptr(positions), n_axes, _ptr(inv_freq), rot,
+                                     _axes(axes), _ptr(q_weight), _ptr(k_weight), int(bool(bf16_weights)), float(eps),
+                                     int(bool(interleaved)), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), total, H,
+                                     Hkv, d, _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fa_cache_append_rope(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, k_pages, v_pages, page_table,
+                         cache_lens, cu_seqlens, positions, n_axes, inv_freq, rot, axes, q_weight, k_weight, bf16_weights,
+                         eps, interleaved, q_out, B, max_pages, num_pages, page_size, total, H, Hkv, d,
+                         stream=None) -> int:
+    return lib().fa_cache_append_rope(_ptr(q), q_token, q_head, _ptr(k), k_token, k_head, _ptr(v), v_token, v_head,
+                                      _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens), _ptr(cu_seqlens),
+                                      _ptr(positions), n_axes, _ptr(inv_freq), rot, _axes(axes), _ptr(q_weight),
+                                      _ptr(k_weight), int(bool(bf16_weights)), float(eps), int(bool(interleaved)),
+                                      _ptr(q_out), B, max_pages, num_pages, page_size, total, H, Hkv, d, _stream(stream))
+
+
+def fa_attention_weights_paged(q, k_pages, page_table, cache_lens, cu_seqlens, tree_mask, mask_words, lse, weights, places,
+                               decay, B, max_pages, num_pages, page_size, max_new, total, H, Hkv, d, scale,
+                               stream=None) -> int:
+    return lib().fa_attention_weights_paged(_ptr(q), _ptr(k_pages), _ptr(page_table), _ptr(cache_lens), _ptr(cu_seqlens),
+                                            _ptr(tree_mask), mask_words, _ptr(lse), _ptr(weights), places, float(decay), B,
+                                            max_pages, num_pages, page_size, max_new, total, H, Hkv, d, float(scale),
+                                            _stream(stream))
+
+
+def fa_cache_evict(page_refs, k_pages, v_pages, page_table, cache_lens, weights, places, keep, recent, lens_out, kept, B,
+                   max_pages, num_pages, page_size, layers, Hkv, d, stream=None) -> int:
+    return lib().fa_cache_evict(_ptr(page_refs), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cache_lens),
+                                _ptr(weights), places, keep, recent, _ptr(lens_out), _ptr(kept), B, max_pages, num_pages,
+                                page_size, layers, Hkv, d, _stream(stream))
 
 
 def fa_exp2_poly(x, y, n, stream=None) -> int:
@@ -484,6 +545,7 @@ class _NoBinding:
     which costs some 10 us more on the host."""
 
     append = attention = compact = fork = resize = staticmethod(lambda *operands: None)
+    rope = rope_bwd = append_rope = weights = evict = staticmethod(lambda *operands: None)
 
 
 def _paged_binding():
@@ -509,7 +571,8 @@ def _paged_binding():
         else:
             module.connect(*(ctypes.cast(getattr(l, name), ctypes.c_void_p).value for name in (
                 "fa_cache_append", "fa_fwd_paged_workspace_bytes", "fa_fwd_paged", "fa_cache_compact", "fa_cache_fork",
-                "fa_cache_resize_workspace_bytes", "fa_cache_resize")))
+                "fa_cache_resize_workspace_bytes", "fa_cache_resize", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd_workspace_bytes",
+                "fa_qk_norm_rope_bwd", "fa_cache_append_rope", "fa_attention_weights_paged", "fa_cache_evict")))
         _fast = module
     return _fast
 
@@ -690,3 +753,252 @@ def cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, 
         _done(fa_cache_resize(page_refs, k_pages, v_pages, page_table, cache_lens, new_lens, lens, status, B, max_pages,
                               num_pages, page_size, layers, Hkv, d, workspace, nbytes), "fa_cache_resize")
     return lens, status
+
+
+# ------------------------------------------------------------------ queries and keys made ready
+def _rows(name, x, lead=None, heads=None, d=None):
+    """Checks bf16 rows [total, heads, d] or [B, N, heads, d] whose last dimension is dense and whose tokens
+    have one stride -> (the tensor, its tokens' and heads' strides in elements)."""
+    import torch
+
+    if x is None:
+        raise ValueError(f"{name} is None")
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [total, heads, d] or [B, N, heads, d]")
+    if (lead is not None and (tuple(x.shape[:-2]) != tuple(lead) or (heads is not None and x.shape[-2] != heads)
+                              or x.shape[-1] != d)):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {(*lead, 'heads' if heads is None else heads, d)}")
+    if x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    token, head = x.stride(-3), x.stride(-2)
+    if x.dim() == 4 and x.shape[0] > 1 and x.numel() > 0:
+        if x.shape[1] == 1:
+            token = x.stride(0)
+        elif x.stride(0) != x.shape[1] * token:
+            raise ValueError(f"{name}'s batches must follow one another with the stride of their tokens")
+    if x.shape[:-2].numel() <= 1:
+        token = 0
+    return (name, x), token, 0 if x.shape[-2] <= 1 else head
+
+
+def _angles(positions, inv_freq, axes, lead):
+    """Checks what the angles come from -> (checked tensors, n_axes, rot, axes as a tuple of ints or None)."""
+    import torch
+
+    if inv_freq is None or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    half = inv_freq.shape[0]
+    c, n_axes = [_check("inv_freq", inv_freq, torch.float32, (half,))], 1
+    if axes is not None:
+        axes = tuple(int(a) for a in axes)
+        if len(axes) != half:
+            raise ValueError(f"axes has {len(axes)} entries, expected {half}")
+        if positions is None:
+            n_axes = max(axes, default=0) + 1
+        elif positions.dim() != len(lead) + 1:
+            raise ValueError(f"positions must be [n_axes, {', '.join(map(str, lead))}] with axes")
+        else:
+            n_axes = positions.shape[0]
+        if any(not 0 <= a < n_axes for a in axes):
+            raise ValueError(f"axes must lie in [0, {n_axes})")
+    if positions is not None:
+        c.append(_check("positions", positions, torch.int32, (n_axes, *lead) if axes is not None else lead))
+    return c, n_axes, 2 * half, axes
+
+
+def _norms(q_weight, k_weight, d):
+    """Checks the weights of the norms -> (checked tensors, whether they are bf16)."""
+    import torch
+
+    given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    if any(w.dtype not in (torch.float32, torch.bfloat16) for _, w in given):
+        raise ValueError("q_weight and k_weight must be float32 or bfloat16")
+    return ([_check(n, w, given[0][1].dtype, (d,)) for n, w in given],
+            bool(given) and given[0][1].dtype == torch.bfloat16)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, axes=None, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """Queries q [total,H,d] or [B,N,H,d] and keys k (Hkv heads) bf16, each head's row normalised with q_weight
+    / k_weight ([d], float32 or bfloat16; None: not normalised) and rotated by its token's position -> (q, k)
+    dense bf16, as the attention calls take them.  q and k may be views with strides (of one projection's
+    output, say); inv_freq float32 [rot / 2] gives the rotation of each pair of the first rot columns, pairs
+    (i, rot / 2 + i) or, interleaved, (2 i, 2 i + 1).  positions int32 [total] or [B,N]; with axes (rot / 2
+    numbers, the axis of each pair: `(0,) * 16 + (1,) * 24 + (2,) * 24`) int32 [n_axes, ...], up to 4 axes."""
+    if stream is None and q_out is None and k_out is None:
+        both = (_fast or _paged_binding()).rope(q, k, positions, inv_freq, q_weight, k_weight, eps, axes, interleaved)
+        if both is not None:
+            return _done(both, "fa_qk_norm_rope")
+    import torch
+
+    cq, q_token, q_head = _rows("q", q)
+    lead, (H, d) = q.shape[:-2], q.shape[-2:]
+    ck, k_token, k_head = _rows("k", k, lead, None, d)
+    Hkv = k.shape[-2]
+    if positions is None:
+        raise ValueError("positions is None")
+    angles, n_axes, rot, axes = _angles(positions, inv_freq, axes, lead)
+    norms, bf16 = _norms(q_weight, k_weight, d)
+    outs = [_check(n, o, torch.bfloat16, x.shape) for n, o, x in (("q_out", q_out, q), ("k_out", k_out, k)) if o is not None]
+    dev = _same_device(cq, ck, *angles, *norms, *outs)
+    with _On(dev, stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
+        _done(fa_qk_norm_rope(q, q_token, q_head, k, k_token, k_head, positions, n_axes, inv_freq, rot, axes, q_weight,
+                              k_weight, bf16, eps, interleaved, q_out, k_out, lead.numel(), H, Hkv, d), "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, axes=None,
+                     interleaved=False, workspace=None, stream=None):
+    """Gradients of :func:`qk_norm_rope` from those of its results (dq_out, dk_out bf16; views with strides are
+    accepted) -> (dq, dk bf16, dq_weight, dk_weight float32 [d], each None without its weight).  q and k, the
+    forward's inputs, are looked at only where there is a weight (None is accepted without one)."""
+    if stream is None and workspace is None:
+        four = (_fast or _paged_binding()).rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, eps, axes,
+                                                    interleaved)
+        if four is not None:
+            return _done(four, "fa_qk_norm_rope_bwd")
+    import torch
+
+    cq, dq_token, dq_head = _rows("dq_out", dq_out)
+    lead, (H, d) = dq_out.shape[:-2], dq_out.shape[-2:]
+    ck, dk_token, dk_head = _rows("dk_out", dk_out, lead, None, d)
+    Hkv = dk_out.shape[-2]
+    if positions is None:
+        raise ValueError("positions is None")
+    angles, n_axes, rot, axes = _angles(positions, inv_freq, axes, lead)
+    norms, bf16 = _norms(q_weight, k_weight, d)
+    c = [cq, ck, *angles, *norms]
+    rows = []
+    for name, x, w, heads in (("q", q, q_weight, H), ("k", k, k_weight, Hkv)):
+        if w is None:
+            rows += [None, 0, 0]
+            continue
+        cx, token, head = _rows(name, x, lead, heads, d)
+        c.append(cx)
+        rows += [x, token, head]
+    if workspace is not None:
+        c.append(_check_workspace(workspace))
+    dev = _same_device(*c)
+    with _On(dev, stream):
+        dq = torch.empty(dq_out.shape, dtype=torch.bfloat16, device=dev)
+        dk = torch.empty(dk_out.shape, dtype=torch.bfloat16, device=dev)
+        dqw, dkw = [None if w is None else torch.empty(d, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
+        nbytes = 0
+        if norms:
+            workspace, nbytes = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(d), dev)
+        _done(fa_qk_norm_rope_bwd(dq_out, dq_token, dq_head, dk_out, dk_token, dk_head, *rows, positions, n_axes, inv_freq,
+                                  rot, axes, q_weight, k_weight, bf16, eps, interleaved, dq, dk, dqw, dkw, lead.numel(), H,
+                                  Hkv, d, workspace, nbytes), "fa_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
+def cache_append_rope(q, k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, inv_freq, positions=None,
+                      q_weight=None, k_weight=None, eps=1e-6, axes=None, interleaved=False, q_out=None, stream=None):
+    """:func:`qk_norm_rope` of packed new tokens q [total,H,d], k, v [total,Hkv,d] bf16 (views with strides are
+    accepted) and :func:`cache_append` of the keys, and of the values as they are, in one call -> q, dense bf16.
+    Without positions every token takes its place in the cache, cache_lens[b] + i, on every axis."""
+    if stream is None and q_out is None:
+        out = (_fast or _paged_binding()).append_rope(q, k, v, k_pages, v_pages, page_table, cache_lens, cu_seqlens, inv_freq,
+                                                      positions, q_weight, k_weight, eps, axes, interleaved)
+        if out is not None:
+            return _done(out, "fa_cache_append_rope")
+    import torch
+
+    pages, _, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, False)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be [total, H, d]")
+    total, H, _ = q.shape
+    cq, q_token, q_head = _rows("q", q, (total,), H, d)
+    ck, k_token, k_head = _rows("k", k, (total,), Hkv, d)
+    cv, v_token, v_head = _rows("v", v, (total,), Hkv, d)
+    angles, n_axes, rot, axes = _angles(positions, inv_freq, axes, (total,))
+    norms, bf16 = _norms(q_weight, k_weight, d)
+    c = [cq, ck, cv, *pages, *table, _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)), *angles, *norms]
+    if q_out is not None:
+        c.append(_check("q_out", q_out, torch.bfloat16, q.shape))
+    dev = _same_device(*c)
+    with _On(dev, stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+        _done(fa_cache_append_rope(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, k_pages, v_pages, page_table,
+                                   cache_lens, cu_seqlens, positions, n_axes, inv_freq, rot, axes, q_weight, k_weight, bf16,
+                                   eps, interleaved, q_out, B, max_pages, num_pages, page_size, total, H, Hkv, d),
+              "fa_cache_append_rope")
+    return q_out
+
+
+# ------------------------------------------------------------------ which places of the cache matter
+def attention_weights_paged(q, k_pages, page_table, cache_lens, cu_seqlens, max_new, lse, weights, tree_mask=None,
+                            decay=1.0, scale=None, stream=None):
+    """The attention weight that every place of the cache got in :func:`attention_fwd_paged` (same operands; lse
+    is what that call returned), summed over a sequence's new tokens and the query heads of each kv head and
+    added to decay times what weights (float32 [B,Hkv,places]) holds, in place -> weights.  decay 0 replaces
+    the old sums.  Columns behind a sequence, and sequences without new tokens, are left alone."""
+    if stream is None:
+        w = (_fast or _paged_binding()).weights(q, k_pages, page_table, cache_lens, cu_seqlens, max_new, lse, weights,
+                                                tree_mask, decay, scale)
+        if w is not None:
+            _done(w, "fa_attention_weights_paged")
+            return weights
+    import torch
+
+    if k_pages is None or k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, page_size, Hkv, d]")
+    num_pages, page_size, Hkv, d = k_pages.shape
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, H, d]")
+    total, H, _ = q.shape
+    if weights.dim() != 3:
+        raise ValueError("weights must be [B, Hkv, places]")
+    max_new = _int32("max_new", max_new)
+    words = (max_new + 63) // 64 if tree_mask is not None else 0
+    c = [_check("q", q, torch.bfloat16, (total, H, d)), _check("k_pages", k_pages, torch.bfloat16, k_pages.shape), *table,
+         _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)), _check("lse", lse, torch.float32, (H, total)),
+         _check("weights", weights, torch.float32, (B, Hkv, weights.shape[2]))]
+    if tree_mask is not None:
+        c.append(_check("tree_mask", tree_mask, torch.int64, (total, words)))
+    dev = _same_device(*c)
+    with _On(dev, stream):
+        if total > 0:
+            _done(fa_attention_weights_paged(q, k_pages, page_table, cache_lens, cu_seqlens, tree_mask, words, lse, weights,
+                                             weights.shape[2], decay, B, max_pages, num_pages, page_size, max_new, total, H,
+                                             Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale),
+                  "fa_attention_weights_paged")
+    return weights
+
+
+def cache_evict(page_refs, k_pages, v_pages, page_table, cache_lens, weights, keep, recent=0, stream=None):
+    """Cuts every sequence of more than keep places down to keep, each kv head (of each layer, where k/v_pages
+    and weights have a leading [layers]) for itself: the last recent places and, of those before, the ones with
+    the largest weights (float32 [B,Hkv,places], as :func:`attention_weights_paged` sums them up; of equal ones
+    the lower place) stay and move together in the pages, in their order, weights too -> (lengths int32 [B],
+    kept int32 [B,Hkv,keep]: which place each place was, -1 past the length).  A sequence that shares a page
+    that would be written (page_refs int32 [num_pages]), has a place without a page, or more places than weights
+    has columns, is left alone.  :func:`cache_resize` to the new lengths gives the freed pages back."""
+    if stream is None:
+        both = (_fast or _paged_binding()).evict(page_refs, k_pages, v_pages, page_table, cache_lens, weights, keep, recent)
+        if both is not None:
+            return _done(both, "fa_cache_evict")
+    import torch
+
+    pages, layers, num_pages, page_size, Hkv, d = _check_pages(k_pages, v_pages, True)
+    table, B, max_pages = _check_table(page_table, cache_lens)
+    keep, recent = _int32("keep", keep), _int32("recent", recent)
+    if not 0 <= recent <= keep:
+        raise ValueError(f"0 <= recent <= keep is required, got recent {recent}, keep {keep}")
+    if weights.dim() != k_pages.dim() - 1:
+        raise ValueError("weights must be [B, Hkv, places]" + (", with the pages' leading [layers]" if k_pages.dim() == 5 else ""))
+    lead = (*k_pages.shape[:-4], B, Hkv)
+    dev = _same_device(_check("page_refs", page_refs, torch.int32, (num_pages,)), *pages, *table,
+                       _check("weights", weights, torch.float32, (*lead, weights.shape[-1])))
+    with _On(dev, stream):
+        lens = torch.empty_like(cache_lens)
+        kept = torch.empty((*lead, keep), dtype=torch.int32, device=dev)
+        _done(fa_cache_evict(page_refs, k_pages, v_pages, page_table, cache_lens, weights, weights.shape[-1], keep, recent,
+                             lens, kept, B, max_pages, num_pages, page_size, layers, Hkv, d), "fa_cache_evict")
+    return lens, kept

@@ -1386,18 +1386,6 @@ __global__ void __maxnreg__(SHARED ? 72 : 80) paged_combine_kernel(const __grid_
   }
 }
 
-constexpr int kMaxNew = 256;
-
-int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new, int total, int H, int Hkv, int d) {
-  int rc = check_page_table(B, max_pages, num_pages, page_size);
-  if (rc == FA_OK) rc = check_page_rows(1, num_pages, page_size, Hkv, d);
-  if (rc != FA_OK) return rc;
-  if (H <= 0 || H % Hkv != 0 || max_new <= 0 || total < 0) return FA_ERR_INVALID_ARG;
-  if (H > 65535 || H / Hkv > 128 || max_new > kMaxNew) return FA_ERR_UNSUPPORTED;
-  if ((double)total * H * d >= (double)(1ll << 40) || (double)total * H > 2147483647.0) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
 // Blocks of the main kernel: as many as run at once.  (The SM count of a GB300;
 // the result does not depend on it.)
 constexpr int kSMs = 152;
@@ -1485,6 +1473,18 @@ int launch_few(PagedParams &p, int blocks, const void *k_pages, const void *v_pa
 }
 
 }  // namespace
+
+constexpr int kMaxNew = 256;
+
+int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new, int total, int H, int Hkv, int d) {
+  int rc = check_page_table(B, max_pages, num_pages, page_size);
+  if (rc == FA_OK) rc = check_page_rows(1, num_pages, page_size, Hkv, d);
+  if (rc != FA_OK) return rc;
+  if (H <= 0 || H % Hkv != 0 || max_new <= 0 || total < 0) return FA_ERR_INVALID_ARG;
+  if (H > 65535 || H / Hkv > 128 || max_new > kMaxNew) return FA_ERR_UNSUPPORTED;
+  if ((double)total * H * d >= (double)(1ll << 40) || (double)total * H > 2147483647.0) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
 
 #ifdef FA_TEST_STALL
 int set_test_stall_paged(int mode) {

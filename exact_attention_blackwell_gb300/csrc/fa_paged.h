@@ -44,6 +44,8 @@ inline bool ptr_aligned(const void *p, unsigned n) { return (reinterpret_cast<ui
 // Argument checks of the page table's and the pages' sizes (FA_OK or the error).
 int check_page_table(int B, int max_pages, int num_pages, int page_size);
 int check_page_rows(int layers, int num_pages, int page_size, int Hkv, int d);
+// The same of attention over the cache, with its new tokens (fa_paged.cu).
+int check_paged(int B, int max_pages, int num_pages, int page_size, int max_new, int total, int H, int Hkv, int d);
 
 #ifdef __CUDACC__
 // Page of place `pos` of sequence b, or -1 where there is none: outside the

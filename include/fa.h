@@ -301,6 +301,101 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
                     int page_size, int layers, int Hkv, int d, void *workspace, size_t workspace_bytes,
                     void *stream);
 
+/* ------------------------------------------------------------------------
+ * Queries and keys made ready for attention: each head's row normalised (or
+ * not) and rotated by its token's positions.  For a row x of d values,
+ *     y = x * (mean(x^2) + eps)^(-1/2) * weight          (y = x without a weight)
+ * and then, for pair i of rot / 2, with p the token's position on the pair's axis,
+ *     (y_a, y_b) -> (y_a cos(p f_i) - y_b sin(p f_i), y_b cos(p f_i) + y_a sin(p f_i)),
+ * f_i = inv_freq[i]: pair i is columns (i, rot / 2 + i), or (2 i, 2 i + 1) where
+ * `interleaved`; columns from rot on are not rotated.  The pages have no
+ * counterpart: fa_fwd and the paged attention take what these calls leave.
+ *   q, k, v    : bf16 [total, H or Hkv, d] with strides of tokens and heads in
+ *                elements (multiples of 8; a head's d values are contiguous), so
+ *                that views into one projection's output can be passed; 16-byte
+ *                aligned.  H and Hkv at most 65535, in any ratio
+ *   q_out, k_out : bf16, dense; may be q and k themselves where those are dense,
+ *                and otherwise overlap none of the inputs
+ *   positions  : DEVICE int32 [n_axes, total], any values; the angle is exact
+ *                to 1e-7 radians for all of them
+ *   inv_freq   : DEVICE fp32 [rot / 2], finite; rot a multiple of 16, at most d
+ *   axes       : HOST array of rot / 2 axes in [0, n_axes), read during the call,
+ *                or NULL (n_axes = 1); n_axes at most 4
+ *   q_weight, k_weight : DEVICE [d], fp32, or bf16 where bf16_weights; each may be
+ *                NULL: those rows are not normalised.  eps finite, >= 0
+ * Sums are fp32 and the result is rounded once.  Other rules as above.
+ * ------------------------------------------------------------------------ */
+int fa_qk_norm_rope(const void *q, long long q_token, long long q_head, const void *k, long long k_token,
+                    long long k_head, const int *positions, int n_axes, const float *inv_freq, int rot,
+                    const int *axes, const void *q_weight, const void *k_weight, int bf16_weights, float eps,
+                    int interleaved, void *q_out, void *k_out, int total, int H, int Hkv, int d, void *stream);
+
+/* Its gradients: from dq_out and dk_out (bf16, strides as for q and k) those of
+ * the inputs, dq and dk (bf16, dense), and of the weights, summed over all
+ * tokens and heads (fp32 [d]; required with the weight, not written without).
+ * q and k are the forward's inputs, needed where there is a weight (NULL is
+ * accepted where there is none).  dq may be dq_out itself where that is dense,
+ * dk may be dk_out.  workspace (with a weight): 256-byte aligned, at least
+ * fa_qk_norm_rope_bwd_workspace_bytes(d).  No atomics: bitwise reproducible. */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int d);
+int fa_qk_norm_rope_bwd(const void *dq_out, long long dq_token, long long dq_head, const void *dk_out,
+                        long long dk_token, long long dk_head, const void *q, long long q_token, long long q_head,
+                        const void *k, long long k_token, long long k_head, const int *positions, int n_axes,
+                        const float *inv_freq, int rot, const int *axes, const void *q_weight, const void *k_weight,
+                        int bf16_weights, float eps, int interleaved, void *dq, void *dk, float *dq_weight,
+                        float *dk_weight, int total, int H, int Hkv, int d, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* fa_qk_norm_rope and fa_cache_append in one: new tokens' queries to q_out, their
+ * keys, and their values as they are, into the pages, to places cache_lens[b] +
+ * i.  positions as above, or NULL: every axis takes the place in the cache
+ * (which stops being a token's position once places were evicted).  Rows past
+ * the table, or whose page entry names no page, are dropped (their queries are
+ * written); rows of q_out that belong to no sequence are left as they were. */
+int fa_cache_append_rope(const void *q, long long q_token, long long q_head, const void *k, long long k_token,
+                         long long k_head, const void *v, long long v_token, long long v_head, void *k_pages,
+                         void *v_pages, const int *page_table, const int *cache_lens, const int *cu_seqlens,
+                         const int *positions, int n_axes, const float *inv_freq, int rot, const int *axes,
+                         const void *q_weight, const void *k_weight, int bf16_weights, float eps, int interleaved,
+                         void *q_out, int B, int max_pages, int num_pages, int page_size, int total, int H, int Hkv,
+                         int d, void *stream);
+
+/* The attention weight that each place of the cache got from the new tokens of
+ * fa_fwd_paged, summed over the tokens and over the query heads of a kv head:
+ * for every place p < cache_lens[b] + n_b of a sequence with new tokens
+ *     weights[b][h][p] = decay * weights[b][h][p]
+ *                      + sum over heads g of h's group and tokens i that see p
+ *                        of exp(scale q_ig . k_p - lse[g][i])
+ * (0 for tokens that see nothing, whose lse is -infinity).  The same operands and
+ * rules as fa_fwd_paged, whose lse it takes (fp32 [H, total]).
+ *   weights : fp32 [B, Hkv, places]; places past the last column are not written,
+ *     nor are those behind a sequence, nor sequences without new tokens
+ *   decay   : finite, >= 0; with 0 the old contents are not read
+ * No atomics: bitwise reproducible. */
+int fa_attention_weights_paged(const void *q, const void *k_pages, const int *page_table, const int *cache_lens,
+                               const int *cu_seqlens, const long long *tree_mask, int mask_words, const float *lse,
+                               float *weights, int places, float decay, int B, int max_pages, int num_pages,
+                               int page_size, int max_new, int total, int H, int Hkv, int d, float scale,
+                               void *stream);
+
+/* Cuts every sequence of more than `keep` places down to keep, each (layer, kv
+ * head) for itself: its last `recent` places (recent <= keep) and, of the ones
+ * before them, the keep - recent with the largest weights stay; of equal ones
+ * the lower place, a NaN counting as lower than everything.  They move, in their
+ * order, to places 0 .. keep - 1, keys, values and weights alike; the weights of
+ * places keep .. cache_lens[b] - 1 become 0.  The pages that are no longer
+ * needed stay in the table until fa_cache_resize shrinks the rows to lens_out.
+ *   weights  : fp32 [layers, B, Hkv, places], as fa_attention_weights_paged sums them up
+ *   lens_out : int32 [B], keep, or cache_lens[b] where the sequence was left alone:
+ *     because it is no longer than keep, or has more places than columns of
+ *     weights or than the table, or a place without a page, or shares a page that
+ *     would be written with another row (page_refs above 1)
+ *   kept     : int32 [layers, B, Hkv, keep]: which place each place was, -1 from
+ *     lens_out[b] on (may be NULL where keep = 0) */
+int fa_cache_evict(const int *page_refs, void *k_pages, void *v_pages, const int *page_table, const int *cache_lens,
+                   float *weights, int places, int keep, int recent, int *lens_out, int *kept, int B, int max_pages,
+                   int num_pages, int page_size, int layers, int Hkv, int d, void *stream);
+
 /* The software 2^x the kernels evaluate on the FMA pipe (FlashAttention-4
  * paper summary, section 2.B: 2^x emulated with FMA instructions, a polynomial
  * of degree 3 to 5 for the fractional part).  Range reduction x = j + f with
