@@ -924,10 +924,11 @@ def cache_append_rope(q, k, v, k_pages, v_pages, page_table, cache_lens, cu_seql
     dev = _same_device(*c)
     with _On(dev, stream):
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-        _done(fa_cache_append_rope(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, k_pages, v_pages, page_table,
-                                   cache_lens, cu_seqlens, positions, n_axes, inv_freq, rot, axes, q_weight, k_weight, bf16,
-                                   eps, interleaved, q_out, B, max_pages, num_pages, page_size, total, H, Hkv, d),
-              "fa_cache_append_rope")
+        if total > 0:
+            _done(fa_cache_append_rope(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, k_pages, v_pages,
+                                       page_table, cache_lens, cu_seqlens, positions, n_axes, inv_freq, rot, axes, q_weight,
+                                       k_weight, bf16, eps, interleaved, q_out, B, max_pages, num_pages, page_size, total, H,
+                                       Hkv, d), "fa_cache_append_rope")
     return q_out
 
 
