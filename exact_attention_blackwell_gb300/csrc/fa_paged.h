@@ -87,9 +87,10 @@ int encode_page_map(CUtensorMap *map, const void *pages, int num_pages, int page
                     bool narrow);
 
 // Test builds only (-DFA_TEST_STALL), as in fa_internal.h: 4: the paged kernel's first P,
-// 5: the few-rows paged kernel's first tile read.
+// 5: the few-rows paged kernel's first tile read, 6: the weight sums' first product read.
 #ifdef FA_TEST_STALL
 int set_test_stall_paged(int mode);
+int set_test_stall_weights(int mode);
 #endif
 
 }  // namespace fa

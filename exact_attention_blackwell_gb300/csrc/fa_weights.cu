@@ -14,56 +14,499 @@
 namespace fa {
 namespace {
 
+// Work.  The products are taken the other way round than for attention: S^T = K Q^T with
+// 128 places as the MMA's rows and the new tokens' rows (tokens x G heads of a kv head) as
+// its columns.  A thread then has one place and adds up its columns: no sum crosses threads,
+// nothing is joined, and each place of a kv head belongs to one block, whatever the
+// division of work.  More rows than the columns of a product come in chunks, each
+// multiplied with the tiles in shared memory.
+//
+// A unit is two neighbouring tiles of one kv head, one for each of the block's two
+// warpgroups; it costs its sequence's number of chunks.  Units stand in one line (sequence,
+// group of HB kv heads, pair of tiles, head), so that the rows of neighbouring heads, which
+// are neighbours in memory, are fetched at about the same time; the line is cut by cost into
+// equal stretches for the blocks, which begin with the first unit that begins in theirs.
 struct WeightsParams {
-  const __nv_bfloat16 *q, *k_pages;
+  CUtensorMap tm_q;  // [total, Hkv, G, d]: box 64 columns x G heads x TB tokens
+  CUtensorMap tm_k;  // [num_pages, page_size, Hkv, d]: box 64 columns x min(page_size, 128) rows of one head
   const int *cu;
   const unsigned long long *mask;  // [total, words] or nullptr: a chain
   const float *lse;                // [H, total]
   float *weights;                  // [B, Hkv, places]
+  unsigned *status;
   PageGeom g;
-  int words, max_new, total, H, Hkv, G, places;
+  int words, max_new, total, Hkv, G, places;
+  int TB, HB, RH;  // tokens of a chunk, kv heads whose rows are in shared memory together, rows from one to the next
+  bool stream;     // several chunks: one after another for each unit, else an item's rows stay
   float scale_log2, decay;
 };
 
-// A warp takes one place of one kv head at a time.
-template <int D>
-__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ WeightsParams p) {
-  grid_go();
-  grid_wait();
-  const int b = blockIdx.y / p.Hkv, kh = blockIdx.y - b * p.Hkv, lane = threadIdx.x & 31;
-  const PagedSeq s = paged_seq_of(p.cu[b], p.cu[b + 1], p.g.cache_lens[b], p.total, p.max_new, p.g.max_pages * p.g.page_size);
-  if (s.n == 0) return;
-  for (int at = blockIdx.x * 8 + (threadIdx.x >> 5); at < min(s.keys, p.places); at += gridDim.x * 8) {
-    const int page = page_of(p.g, b, at);
-    float sum = 0.f;
-    if (page >= 0) {
-      const __nv_bfloat16 *k = p.k_pages + (((size_t)page * p.g.page_size + at % p.g.page_size) * p.Hkv + kh) * D;
-      float kx[D / 32];
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) kx[e] = __bfloat162float(k[32 * e + lane]);
-      for (int i = 0; i < s.n; ++i) {
-        const int j = at - s.len;
-        if (j >= 0 && (p.mask ? !((p.mask[(size_t)(s.start + i) * p.words + (j >> 6)] >> (j & 63)) & 1) : j > i)) continue;
-        for (int h = kh * p.G; h < (kh + 1) * p.G; ++h) {
-          const __nv_bfloat16 *q = p.q + ((size_t)(s.start + i) * p.H + h) * D;
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) dot = fmaf(kx[e], __bfloat162float(q[32 * e + lane]), dot);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-          const float lse = p.lse[(size_t)h * p.total + s.start + i];
-          if (lse != -INFINITY) sum += ex2_mufu(fmaf(dot, p.scale_log2, -lse * 1.4426950408889634f));
-        }
-      }
+// NQ: rows in shared memory.
+template <int D, int NQ>
+struct WeightsCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = 128 * D * 2, kBoxBytes = 128 * 128;  // a tile of K, its 64-column box
+  static constexpr int kQBytes = NQ * D * 2, kQBoxBytes = NQ * 128;
+  static constexpr int kQBufs = kQBytes > 32768 ? 1 : 2, kTermBufs = 4;
+  static constexpr int kWarps = 8, kMmaWarp = 8, kKeyWarp = 9, kThreads = 32 * 11;
+  static constexpr int kTermBytes = kTermBufs * 2 * NQ * 4;
+  static constexpr int kSmemMax = 227 * 1024;
+  static constexpr int kStagesFit = (kSmemMax - 1024 - 1024 - kQBufs * kQBytes - kTermBytes) / kTileBytes;
+  static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
+  static_assert(kStages >= 2, "a unit's two tiles");
+  // S^T of warpgroup w: two buffers of NQ columns from 2 w NQ on
+  static constexpr int kTmemCols = 4 * NQ;
+  static_assert(NQ >= 32 && NQ % 32 == 0 && kTmemCols <= 512, "TMEM budget");
+  static constexpr int kOffQ = 0, kOffRing = kQBufs * kQBytes, kOffTerms = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffTerms + kTermBytes;
+  // barriers: full[S], empty[S], q_full[QB], q_free[QB], t_full[TB], t_free[TB], s_full[4], s_free[4], drain
+  static constexpr int kNumBars = 2 * kStages + 2 * kQBufs + 2 * kTermBufs + 9;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+  static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
+  static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
+};
+
+FA_STALL_FLAG_DECL
+
+enum WeightsSite : int {
+  kWSiteKeys = 43, kWSiteRows = 44, kWSiteTerms = 45, kWSiteEmpty = 46, kWSiteSFree = 47, kWSiteSFull = 48,
+  kWSiteRowsFree = 49, kWSiteTermsFree = 50, kWSiteDrain = 51
+};
+
+// A block's units; every warp walks its own copy.
+struct WeightsWalk {
+  long long base, end;  // cost before the sequence, and where the block's stretch ends
+  PagedSeq s;
+  int b, u, units, chunks;  // the sequence's next unit
+  int last;                 // item (group of heads) of the unit before
+  // the current unit
+  int group, pair, hb;
+  bool first;  // of its item in this block
+
+  __device__ static PagedSeq seq(const WeightsParams &p, int b) {
+    return paged_seq_of(p.cu[b], p.cu[b + 1], p.g.cache_lens[b], p.total, p.max_new, p.g.max_pages * p.g.page_size);
+  }
+  __device__ static int units_of(const WeightsParams &p, const PagedSeq &s) {  // fits 31 bits (checked by the host)
+    return s.n == 0 ? 0 : ((s.keys + 255) >> 8) * p.Hkv;
+  }
+  __device__ static int chunks_of(const WeightsParams &p, const PagedSeq &s) { return p.stream ? (s.n + p.TB - 1) / p.TB : 1; }
+  __device__ void load(const WeightsParams &p) {
+    s = seq(p, b);
+    units = units_of(p, s);
+    chunks = chunks_of(p, s);
+    u = 0;
+    last = -1;
+  }
+  __device__ bool next(const WeightsParams &p) {
+    for (;;) {
+      if (b >= p.g.B || base >= end) return false;
+      if (u < units) break;
+      base += (long long)units * chunks;
+      if (++b < p.g.B) load(p);
     }
-    if (lane == 0) {
-      float *w = p.weights + (size_t)blockIdx.y * p.places + at;
-      *w = p.decay == 0.f ? sum : fmaf(*w, p.decay, sum);
+    if (base + (long long)u * chunks >= end) return false;
+    const int per = ((s.keys + 255) >> 8) * p.HB;  // units of an item
+    group = u / per;
+    const int at = u - group * per;
+    pair = at / p.HB;
+    hb = at - pair * p.HB;
+    first = group != last;
+    last = group;
+    ++u;
+    return true;
+  }
+};
+
+// The cost of all units and where this block begins, by the whole block together.
+template <int THREADS>
+__device__ __forceinline__ void weights_start(const WeightsParams &p, long long *sums, WeightsWalk *at) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PagedSeq s;
+  auto cost = [&](int b) -> long long {
+    if (b >= p.g.B) return 0;
+    s = WeightsWalk::seq(p, b);
+    return (long long)WeightsWalk::units_of(p, s) * WeightsWalk::chunks_of(p, s);
+  };
+  auto scan = [&](long long x, long long &total) -> long long {  // exclusive
+    long long sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
     }
+    __syncthreads();
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const long long y = sums[w];
+      if (w < warp) before += y;
+      total += y;
+    }
+    return before + sum - x;
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
+    long long sum;
+    scan(cost(b0 + (int)threadIdx.x), sum);
+    total += sum;
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long begin = min(per * blockIdx.x, total);
+  long long done = 0;
+  for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
+    const int b = b0 + (int)threadIdx.x;
+    long long sum;
+    const long long x = cost(b), before = done + scan(x, sum);
+    if (b < p.g.B && begin >= before && begin < before + x) {
+      at->b = b;
+      at->s = s;
+      at->units = WeightsWalk::units_of(p, s);
+      at->chunks = WeightsWalk::chunks_of(p, s);
+      at->base = before;
+      at->end = min(begin + per, total);
+      at->u = (int)((begin - before + at->chunks - 1) / at->chunks);
+      at->last = -1;
+    }
+    done += sum;
+    if (done > begin) break;
   }
 }
 
+// Bits [lo, hi) of a 32-bit word (both may lie outside it).
+__device__ __forceinline__ unsigned bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  if (lo >= hi) return 0;
+  return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+// Rounding.  Scores are fp32 sums.  A row's lse in log2 units is kept as a float and its
+// rounding error, which as a factor 2^-error goes into the sum: as the argument's error it
+// would be the same for all places of a row (up to 2^-20 of each weight).  Sums are fp32.
+template <int D, int NQ>
+__global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel(const __grid_constant__ WeightsParams p) {
+  using C = WeightsCfg<D, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto full_bar = [&](int i) { return bar0 + 8u * i; };
+  auto empty_bar = [&](int i) { return bar0 + 8u * (C::kStages + i); };
+  const uint32_t bar1 = bar0 + 8u * (2 * C::kStages);
+  auto q_full = [&](int i) { return bar1 + 8u * i; };
+  auto q_free = [&](int i) { return bar1 + 8u * (C::kQBufs + i); };
+  const uint32_t bar2 = bar1 + 8u * (2 * C::kQBufs);
+  auto t_full = [&](int i) { return bar2 + 8u * i; };
+  auto t_free = [&](int i) { return bar2 + 8u * (C::kTermBufs + i); };
+  const uint32_t bar3 = bar2 + 8u * (2 * C::kTermBufs);
+  auto s_full = [&](int w, int buf) { return bar3 + 8u * (2 * w + buf); };
+  auto s_free = [&](int w, int buf) { return bar3 + 8u * (4 + 2 * w + buf); };
+  const uint32_t drain_bar = bar3 + 8u * 8;
+  uint8_t *misc = smem + C::kOffMisc;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
+  WeightsWalk *at = reinterpret_cast<WeightsWalk *>(misc + 8);
+  long long *sums = reinterpret_cast<long long *>(misc + 104);  // [11]
+  static_assert(sizeof(WeightsWalk) <= 96, "");
+  float *terms = reinterpret_cast<float *>(smem + C::kOffTerms);  // [kTermBufs][2][NQ]: -lse2, factor
+  const WaitCtx wctx{abort_flag, p.status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const uint32_t bar = bar0 + 8u * i;
+      const bool all = bar >= t_free(0) && bar < t_free(0) + 8u * C::kTermBufs, half = bar >= s_free(0, 0) && bar < drain_bar;
+      mbar_init(bar, all ? C::kWarps : half ? C::kWarps / 2 : 1);
+    }
+    *abort_flag = 0;
+    at->b = p.g.B;
+    at->base = at->end = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == C::kKeyWarp && lane == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+  }
+  __syncthreads();
+  grid_go();  // only now: a kernel that begins early takes no tensor memory before this one has
+  grid_wait();
+  weights_start<C::kThreads>(p, sums, at);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  WeightsWalk walk = *at;
+  bool ok = true;
+
+  if (warp < C::kWarps) {
+    // ===================================================== two warpgroups, a thread to a place
+    const int w = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(2 * w * NQ);
+    const float c2 = p.scale_log2;
+    int step = 0, tile_no = 0;  // sets of rows, products of this warpgroup so far
+    while (ok && walk.next(p)) {
+      const int kv0 = (2 * walk.pair + w) * 128, pos = kv0 + r, kh = walk.group * p.HB + walk.hb;
+      const bool mine = kv0 < walk.s.keys, tail = kv0 + 128 > walk.s.len;
+      const bool out = mine && pos < walk.s.keys && pos < p.places;
+      const bool held = out && page_of(p.g, walk.b, pos) >= 0;
+      float *to = p.weights + ((size_t)walk.b * p.Hkv + kh) * p.places + pos;
+      const float old = out && p.decay != 0.f ? *to : 0.f;
+      const int j = pos - walk.s.len;  // this place among the new tokens
+      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+      for (int c = 0; c < walk.chunks && ok; ++c) {
+        const int tok0 = c * p.TB, tokens = min(p.TB, walk.s.n - tok0), rows = tokens * p.G;
+        // the rows that see this place
+        unsigned see[NQ / 32];
+#pragma unroll
+        for (int i = 0; i < NQ / 32; ++i) see[i] = held ? bit_range((max(j - tok0, 0)) * p.G - 32 * i, rows - 32 * i) : 0u;
+        if (held && j >= 0 && p.mask) {
+#pragma unroll
+          for (int i = 0; i < NQ / 32; ++i) see[i] = 0;
+          const unsigned long long *word = p.mask + (size_t)(walk.s.start + tok0) * p.words + (j >> 6);
+          for (int k = 0; k < tokens; ++k, word += p.words)
+            if ((*word >> (j & 63)) & 1) {
+#pragma unroll
+              for (int i = 0; i < NQ / 32; ++i) see[i] |= bit_range(k * p.G - 32 * i, (k + 1) * p.G - 32 * i);
+            }
+        }
+        if (p.stream || walk.first) {
+          if (!p.stream && step > 0) mbar_arrive_warp(t_free((step - 1) % C::kTermBufs));
+          ok = mbar_wait_warp(t_full(step % C::kTermBufs), (step / C::kTermBufs) & 1, wctx, kWSiteTerms);
+          if (!ok) break;
+          ++step;
+        }
+        if (mine) {
+          const float4 *neg = reinterpret_cast<const float4 *>(terms + (size_t)((step - 1) % C::kTermBufs) * 2 * NQ + walk.hb * p.RH);
+          const float4 *fac = neg + NQ / 4;
+          const int buf = tile_no & 1;
+          ok = mbar_wait_warp(s_full(w, buf), (tile_no >> 1) & 1, wctx, kWSiteSFull);
+          if (!ok) break;
+          tc_fence_after();
+          const bool whole = !tail && !__any_sync(0xffffffffu, out && !held);
+#pragma unroll
+          for (int i = 0; i < NQ / 32; ++i) {
+            if (32 * i >= rows) break;
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(s_tm + (uint32_t)(buf * NQ + 32 * i), s);
+            tmem_wait_ld(s);
+            if (32 * i + 32 >= rows) {  // the last of it is read
+              tc_fence_before();
+              if (!(FA_STALL(6) && tile_no == 0 && w == 0)) mbar_arrive_warp(s_free(w, buf));
+            }
+            auto add = [&](bool all) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 n = neg[8 * i + e / 4], f = fac[8 * i + e / 4];
+                float x[4];
+                ffma2(x[0], x[1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), c2, c2, n.x, n.y);
+                ffma2(x[2], x[3], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), c2, c2, n.z, n.w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = ex2_mufu(x[k]);
+                if (all) {
+                  ffma2(a0, a1, x[0], x[1], f.x, f.y, a0, a1);
+                  ffma2(a2, a3, x[2], x[3], f.z, f.w, a2, a3);
+                } else {  // rows past the last hold anything, and so do their factors
+                  const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) x[k] = (see[i] >> (e + k)) & 1 ? x[k] * g[k] : 0.f;
+                  fadd2(a0, a1, a0, a1, x[0], x[1]);
+                  fadd2(a2, a3, a2, a3, x[2], x[3]);
+                }
+              }
+            };
+            if (whole && 32 * i + 32 <= rows) add(true);
+            else add(false);
+          }
+          ++tile_no;
+        }
+        if (p.stream) mbar_arrive_warp(t_free((step - 1) % C::kTermBufs));
+      }
+      const float sum = (a0 + a1) + (a2 + a3);
+      if (ok && out) *to = p.decay == 0.f ? sum : fmaf(old, p.decay, sum);
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ===================================================== MMA issue (whole warp; the elected lane issues)
+    int fill = 0, step = 0, tile_no[2] = {0, 0};
+    const uint64_t k_desc = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
+    const uint64_t q_desc = make_sdesc_sw128(sbase + C::kOffQ, 0, 1024);
+    bool any = false;
+    while (ok && walk.next(p)) {
+      const int nt = (2 * walk.pair + 1) * 128 < walk.s.keys ? 2 : 1;
+      for (int t = 0; t < nt && ok; ++t)
+        ok = mbar_wait_warp(full_bar((fill + t) % C::kStages), ((fill + t) / C::kStages) & 1, wctx, kWSiteKeys);
+      for (int c = 0; c < walk.chunks && ok; ++c) {
+        if (p.stream || walk.first) {
+          if (!p.stream && step > 0) {
+            if (elect_one()) tc_commit(q_free((step - 1) % C::kQBufs));
+            __syncwarp();
+          }
+          ok = mbar_wait_warp(q_full(step % C::kQBufs), (step / C::kQBufs) & 1, wctx, kWSiteRows);
+          if (!ok) break;
+          ++step;
+        }
+        tc_fence_after();
+        const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G;
+        const uint32_t idesc = make_idesc_bf16(128, (rows + 15) & ~15, false, false);
+        const uint64_t qd = q_desc + (uint64_t)((((step - 1) % C::kQBufs) * C::kQBytes + walk.hb * p.RH * 128) >> 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= nt || !ok) continue;
+          const int buf = tile_no[t] & 1;
+          ok = mbar_wait_warp(s_free(t, buf), ((tile_no[t] >> 1) & 1) ^ 1, wctx, kWSiteSFree);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = k_desc + (uint64_t)((((fill + t) % C::kStages) * C::kTileBytes) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + (uint32_t)((2 * t + buf) * NQ), kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4),
+                     qd + (uint32_t)(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            tc_commit(s_full(t, buf));
+          }
+          __syncwarp();
+          any = true;
+          ++tile_no[t];
+        }
+        if (p.stream && ok) {
+          if (elect_one()) tc_commit(q_free((step - 1) % C::kQBufs));
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elect_one())
+        for (int t = 0; t < nt; ++t) tc_commit(empty_bar((fill + t) % C::kStages));
+      __syncwarp();
+      fill += nt;
+    }
+    // Drain: every MMA this warp issued completes before TMEM is released.
+    if (any) {
+      if (elect_one()) tc_commit(drain_bar);
+      __syncwarp();
+      if (!mbar_wait_warp(drain_bar, 0, wctx, kWSiteDrain) && *abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test(drain_bar, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      }
+    }
+  } else if (warp == C::kKeyWarp) {
+    // ===================================================== K tiles (one lane per page of a tile)
+    const uint64_t once = policy_evict_first();
+    const int box_rows = min(p.g.page_size, 128), boxes = 128 / box_rows;
+    const int shift = 31 - __clz(p.g.page_size);
+    int fill = 0;
+    while (ok && walk.next(p)) {
+      const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
+      for (int t = 0; t < 2 && ok; ++t) {
+        const int kv0 = (2 * walk.pair + t) * 128, pos = kv0 + lane * box_rows;
+        if (kv0 >= walk.s.keys) break;
+        int page = -1;
+        if (lane < boxes && pos < walk.s.keys) page = row[pos >> shift];
+        const int slot = fill % C::kStages;
+        ok = mbar_wait_warp(empty_bar(slot), ((fill / C::kStages) & 1) ^ 1, wctx, kWSiteEmpty);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), C::kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const int r0 = pos & (p.g.page_size - 1);
+          page = page >= 0 && page < p.g.num_pages ? page : -1;  // -1: zeros
+#pragma unroll
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_4d_hint(sbase + C::kOffRing + slot * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, &p.tm_k,
+                             full_bar(slot), bx * 64, walk.group * p.HB + walk.hb, r0, page, once);
+        }
+        ++fill;
+      }
+    }
+    // Every copy issued lands before the block exits (normally they already have).
+    const uint64_t t0 = global_timer_ns();
+    for (int f = max(0, fill - C::kStages); f < fill; ++f)
+      while (!mbar_test(full_bar(f % C::kStages), (f / C::kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  } else {
+    // ===================================================== the tokens' rows and what their lse puts into the sums
+    int step = 0;
+    while (ok && walk.next(p)) {
+      for (int c = 0; c < walk.chunks && ok; ++c) {
+        if (!(p.stream || walk.first)) continue;
+        const int qb = step % C::kQBufs, tb = step % C::kTermBufs, tok0 = walk.s.start + c * p.TB;
+        const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G, kh = walk.group * p.HB;
+        float lse[NQ / 32];
+#pragma unroll
+        for (int i = 0; i < NQ / 32; ++i) {
+          const int x = lane + 32 * i, hb = x / p.RH, y = x - hb * p.RH, tok = y / p.G;
+          lse[i] = 0.f;
+          if (hb < p.HB && y < rows) lse[i] = p.lse[(size_t)((kh + hb) * p.G + y - tok * p.G) * p.total + tok0 + tok];
+        }
+        ok = mbar_wait_warp(q_free(qb), ((step / C::kQBufs) & 1) ^ 1, wctx, kWSiteRowsFree);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full(qb), p.HB * C::kBoxes * p.TB * p.G * 128);
+          for (int hb = 0; hb < p.HB; ++hb)
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_4d(sbase + C::kOffQ + qb * C::kQBytes + bx * C::kQBoxBytes + hb * p.RH * 128, &p.tm_q, q_full(qb), bx * 64, 0,
+                          kh + hb, tok0);
+        }
+        ++step;
+        __syncwarp();
+        ok = mbar_wait_warp(t_free(tb), (((step - 1) / C::kTermBufs) & 1) ^ 1, wctx, kWSiteTermsFree);
+        if (!ok) break;
+        float *t = terms + (size_t)tb * 2 * NQ;
+#pragma unroll
+        for (int i = 0; i < NQ / 32; ++i) {
+          constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500920e-8f;  // log2(e) is their sum
+          const float hi = lse[i] * kLog2e, lo = fmaf(lse[i], kLog2e, -hi) + lse[i] * kLog2eLow;
+          // a token that saw nothing has lse = -inf and gives nothing
+          t[lane + 32 * i] = lse[i] == -INFINITY ? -INFINITY : -hi;
+          t[NQ + lane + 32 * i] = fabsf(hi) < INFINITY ? fmaf(lo, -0.693147180559945309f, 1.f) : 1.f;
+        }
+        mbar_arrive_warp(t_full(tb));
+      }
+    }
+    const uint64_t t0 = global_timer_ns();
+    for (int f = max(0, step - C::kQBufs); f < step; ++f)
+      while (!mbar_test(q_full(f % C::kQBufs), (f / C::kQBufs) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+constexpr int kSMs = 152;
+
+template <int D, int NQ>
+int launch_weights(WeightsParams &p, const void *q, const void *k_pages, cudaStream_t stream) {
+  using C = WeightsCfg<D, NQ>;
+  const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.total};
+  const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.Hkv * p.G * D * 2};
+  const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
+  // head dim 64, one head at a time: its neighbour's 128 bytes are not fetched with it (as in fa_paged.cu)
+  if (encode_bf16_box_map(&p.tm_q, q, dims, strides, box) ||
+      encode_page_map(&p.tm_k, k_pages, p.g.num_pages, p.g.page_size, p.Hkv, D, p.g.page_size < 128 ? p.g.page_size : 128,
+                      D == 64 && p.HB == 1))
+    return FA_ERR_CUDA;
+  // on every launch: the attribute belongs to the function on the current device
+  if (cudaFuncSetAttribute(weights_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return launch_after(weights_kernel<D, NQ>, kSMs, 1, C::kThreads, C::kSmemBytes, stream, p);
+}
+
 }  // namespace
+
+#ifdef FA_TEST_STALL
+int set_test_stall_weights(int mode) {
+  return cudaMemcpyToSymbol(g_test_stall, &mode, sizeof(int)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+#endif
+
 }  // namespace fa
 
 using namespace fa;
@@ -82,34 +525,45 @@ int fa_attention_weights_paged(const void *q, const void *k_pages, const int *pa
   if (tree_mask && (long long)mask_words * 64 < max_new) return FA_ERR_INVALID_ARG;
   if (places <= 0) return FA_ERR_INVALID_ARG;
   if ((double)B * Hkv * places >= (double)(1ll << 40)) return FA_ERR_UNSUPPORTED;
+  // the units of one sequence are counted in 31 bits
+  if (((double)max_pages * page_size / 256 + 1) * Hkv >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   if (!ptr_aligned(q, 16) || !ptr_aligned(k_pages, 16)) return FA_ERR_ALIGNMENT;
   for (const void *x : {(const void *)page_table, (const void *)cache_lens, (const void *)cu_seqlens, (const void *)lse,
                         (const void *)weights})
     if (!ptr_aligned(x, 4)) return FA_ERR_ALIGNMENT;
   if (!ptr_aligned(tree_mask, 8)) return FA_ERR_ALIGNMENT;
-  if ((long long)B * Hkv > 65535) return FA_ERR_UNSUPPORTED;
   if ((rc = check_device()) != FA_OK) return rc;
   if (total == 0) return FA_OK;
   WeightsParams p = {};
-  p.q = static_cast<const __nv_bfloat16 *>(q);
-  p.k_pages = static_cast<const __nv_bfloat16 *>(k_pages);
   p.cu = cu_seqlens;
   p.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
   p.lse = lse;
   p.weights = weights;
+  p.status = device_status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
   p.g = PageGeom{page_table, cache_lens, B, max_pages, num_pages, page_size};
   p.words = mask_words;
   p.max_new = max_new;
   p.total = total;
-  p.H = H;
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.places = places;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.decay = decay;
+  // Rows of up to 32 in all (a decoding step, a short chain): a longer ring of K tiles.
+  const bool few = max_new * p.G <= 32;
+  const int room = few ? 32 : 128;
+  p.TB = room / p.G < max_new ? room / p.G : max_new;
+  p.stream = max_new > p.TB;
+  p.RH = (p.TB * p.G + 7) & ~7;
+  p.HB = 1;
+  while (!p.stream && p.HB < 4 && Hkv % (2 * p.HB) == 0 && 2 * p.HB * p.RH <= room) p.HB *= 2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void (*kernel)(WeightsParams) = d == 64 ? weights_kernel<64> : d == 128 ? weights_kernel<128> : weights_kernel<256>;
-  return launch_after(kernel, 256, B * Hkv, 256, 0, s, p);
+  if (few)
+    return d == 64 ? launch_weights<64, 32>(p, q, k_pages, s)
+                   : d == 128 ? launch_weights<128, 32>(p, q, k_pages, s) : launch_weights<256, 32>(p, q, k_pages, s);
+  return d == 64 ? launch_weights<64, 128>(p, q, k_pages, s)
+                 : d == 128 ? launch_weights<128, 128>(p, q, k_pages, s) : launch_weights<256, 128>(p, q, k_pages, s);
 }
 
 }  // extern "C"

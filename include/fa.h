@@ -424,7 +424,9 @@ int fa_last_device_status(void *stream);
  * into registers, 25 dQ partial read out); paged attention 31-40 (31 Q tile
  * loaded, 32/33 K/V tile loaded, 34 P stored, 35 ring slot free, 36 S computed,
  * 37 O readable, 38 MMA drain, 39 Q tile free, 40 last V tile loaded) and, with
- * few rows, 41 K and V tile loaded, 42 ring slot free.  Outputs of a call in which a wait
+ * few rows, 41 K and V tile loaded, 42 ring slot free; weight sums 43-51 (43 K
+ * tile loaded, 44 rows loaded, 45 their lse ready, 46 ring slot free, 47 product
+ * read, 48 product computed, 49 rows free, 50 their lse read, 51 MMA drain).  Outputs of a call in which a wait
  * ran out are unspecified. */
 int fa_last_device_status_site(void *stream, int *site);
 
@@ -433,7 +435,8 @@ int fa_last_device_status_site(void *stream, int *site);
  * launch until called again with mode 0, so that a bounded wait runs out and
  * the kernel unwinds through its abort path (1: the forward's first P, 2: the
  * dK/dV kernels' first P, 3: the dQ kernel's first dS, 4: the paged attention
- * kernel's first P, 5: its few-rows kernel's first tile read); build such a library
+ * kernel's first P, 5: its few-rows kernel's first tile read, 6: the
+ * weight sums' first product read); build such a library
  * with a short -DFA_WAIT_LIMIT_NS.  Returns FA_ERR_INVALID_ARG for another
  * mode.  In every other build it does nothing and returns FA_ERR_UNSUPPORTED. */
 int fa_debug_stall(int mode);
