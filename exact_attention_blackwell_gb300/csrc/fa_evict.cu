@@ -11,6 +11,7 @@
 #include <climits>
 
 #include "fa_paged.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
@@ -35,8 +36,6 @@ __device__ __forceinline__ unsigned rank_of(float x) {
 }
 
 // ------------------------------------------------------------------ which places stay
-constexpr int kSelThreads = 1024;
-
 // Does the row hold more than the budget, fit the sums, have a page for every place and own
 // those that are written?
 __device__ __forceinline__ bool goes(const EvictParams &p, int b, int len) {
@@ -52,6 +51,7 @@ __device__ __forceinline__ bool goes(const EvictParams &p, int b, int len) {
 }
 
 // Exclusive sum over the block (of two 16-bit counts at once); *total gets the whole sum.
+template <int THREADS>
 __device__ __forceinline__ unsigned scan(unsigned x, unsigned *warp_sums, unsigned *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned s = x;
@@ -63,112 +63,257 @@ __device__ __forceinline__ unsigned scan(unsigned x, unsigned *warp_sums, unsign
   __syncthreads();
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  unsigned w = warp_sums[lane];
+  unsigned w = lane < THREADS / 32 ? warp_sums[lane] : 0u;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < THREADS / 32; o <<= 1) {
     const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
+  *total = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
   const unsigned before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   return s - x + (warp > 0 ? before : 0u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ unsigned hist[256], warp_sums[32];
-  __shared__ unsigned s_prefix, s_need;
+template <int CS>
+__device__ __forceinline__ void cluster_barrier() {
+  if (CS == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+// A word of another block's shared memory, at the same place as here.
+__device__ __forceinline__ unsigned load_of(const unsigned *here, int rank) {
+  uint32_t addr;
+  unsigned v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(here)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A cluster of CS blocks to a row of sums, each with a stretch of it, which it keeps in shared
+// memory (up to `cap` of them; longer rows are read again from L2, by one block).  The smallest
+// rank that stays is found from the top, BITS at a time: a histogram of the ranks that agree
+// with what is known so far, and the bin in which the count from above reaches what is needed;
+// ranks of a bin that all stay need no more bits.  Every block adds up all blocks' histograms
+// for itself, so that a round costs one barrier of the cluster.
+template <int THREADS, int BITS, int CS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictParams p, int cap) {
+  constexpr int kBins = 1 << BITS, kOwn = kBins / THREADS;
+  extern __shared__ float keys[];
+  __shared__ unsigned hists[CS == 1 ? 1 : 2][kBins], warp_sums[32], s_counts;
+  __shared__ unsigned s_prefix, s_need, s_count;
   grid_go();
   grid_wait();
   const int tid = threadIdx.x;
-  const int b = (int)(blockIdx.x / p.Hkv) % p.g.B;
+  const unsigned item = blockIdx.x / CS;
+  const int rank = CS == 1 ? 0 : (int)(blockIdx.x % CS);
+  const int b = (int)(item / p.Hkv) % p.g.B;
   const int len = p.g.cache_lens[b];
-  float *w = p.weights + (size_t)blockIdx.x * p.places;
-  int *kept = p.kept + (size_t)blockIdx.x * p.keep;
+  float *w = p.weights + (size_t)item * p.places;
+  int *kept = p.kept + (size_t)item * p.keep;
   const bool go = goes(p, b, len);
-  if (blockIdx.x < p.Hkv * p.g.B && blockIdx.x % p.Hkv == 0 && tid == 0) p.lens_out[b] = go ? p.keep : len;
-  if (!go) {
-    for (int i = tid; i < p.keep; i += kSelThreads) kept[i] = i < len ? i : -1;
+  if (rank == 0 && item < (unsigned)(p.Hkv * p.g.B) && item % p.Hkv == 0 && tid == 0) p.lens_out[b] = go ? p.keep : len;
+  if (!go) {  // the whole cluster
+    for (int i = rank * THREADS + tid; i < p.keep; i += CS * THREADS) kept[i] = i < len ? i : -1;
     return;
   }
-  // the rank of the last one that stays, eight bits at a time from the top
+  // this block's stretch [lo, hi), x[i - lo]
+  const int part = CS == 1 ? len : ((len + CS - 1) / CS + 3) & ~3;
+  const int lo = min(rank * part, len), hi = min(lo + part, len);
+  const float *x = w + lo;
+  if (hi - lo <= cap) {
+#pragma unroll 16
+    for (int i = tid; i < hi - lo; i += THREADS) keys[i] = w[lo + i];
+    x = keys;
+  }
   const int older = len - p.recent, stay = p.keep - p.recent;
   unsigned prefix = 0, need = stay;
-  for (int shift = 24; shift >= 0 && stay > 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < older; i += kSelThreads) {
-      const unsigned r = rank_of(w[i]);
-      if (shift == 24 || r >> (shift + 8) == prefix) atomicAdd(&hist[(r >> shift) & 255u], 1u);
+  int shift = 32, round = 0;
+  while (shift > 0 && stay > 0) {
+    const int bits = min(BITS, shift), known = shift;
+    shift -= bits;
+    unsigned *hist = hists[CS == 1 ? 0 : round & 1];
+    ++round;
+    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+    __syncthreads();  // and x is there
+#pragma unroll 4
+    for (int i = tid; i < min(hi, older) - lo; i += THREADS) {
+      const unsigned r = rank_of(x[i]);
+      if (known == 32 || r >> known == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1u)], 1u);
     }
-    __syncthreads();
-    if (tid == 0) {
-      unsigned above = 0;
-      int digit = 255;
-      while (digit > 0 && above + hist[digit] < need) above += hist[digit--];
-      s_prefix = prefix << 8 | digit;
-      s_need = need - above;
+    cluster_barrier<CS>();
+    unsigned own[kOwn], count = 0, total;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const unsigned *bin = hist + kBins - 1 - (tid * kOwn + e);
+      own[e] = *bin;
+#pragma unroll
+      for (int o = 1; o < CS; ++o) own[e] += load_of(bin, (rank + o) % CS);
+      count += own[e];
+    }
+    unsigned above = scan<THREADS>(count, warp_sums, &total);
+    if (above < need && above + count >= need) {
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) {
+        if (above < need && above + own[e] >= need) {
+          s_prefix = prefix << bits | (kBins - 1 - (tid * kOwn + e));
+          s_need = need - above;
+          s_count = own[e];
+        }
+        above += own[e];
+      }
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
+    if (s_count == need) break;
   }
-  // in order: all above it, and the first `need` that equal it
-  unsigned above = 0, equal = 0;
-  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float x = i < len ? w[i] : 0.f;
-    const unsigned r = rank_of(x);
-    const bool gt = i < len && (i >= older || (stay > 0 && r > prefix));
-    const bool eq = i < older && stay > 0 && r == prefix;
+  // In order: all above it, and the first `need` that equal it; four places to a thread.
+  auto flags = [&](int i, float y) -> unsigned {  // 1: stays, 0x10000: equal to the last that stays
+    if (i >= older) return i < len ? 1u : 0u;
+    if (stay == 0) return 0u;
+    const unsigned r = rank_of(y) >> shift;
+    return r > prefix ? 1u : r == prefix ? 0x10000u : 0u;
+  };
+  unsigned above = 0, equal = 0;  // before this block's stretch
+  if (CS > 1) {
+    for (int i = tid; i < hi - lo; i += THREADS) {
+      const unsigned f = flags(lo + i, x[i]);
+      above += f & 0xffffu;
+      equal += f >> 16;
+    }
+    __syncthreads();
+    if (tid == 0) s_counts = s_count = 0;
+    __syncthreads();
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if ((tid & 31) == 0) {
+      atomicAdd(&s_counts, above);
+      atomicAdd(&s_count, equal);
+    }
+    cluster_barrier<CS>();  // and every block holds its stretch, so that sums may be written
+    above = equal = 0;
+    for (int o = 0; o < rank; ++o) {
+      above += load_of(&s_counts, o);
+      equal += load_of(&s_count, o);
+    }
+  } else {
+    __syncthreads();
+  }
+  for (int i0 = lo; i0 < hi; i0 += 4 * THREADS) {
+    float y[4];
+    unsigned f[4], sum4 = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + 4 * tid + e;
+      y[e] = i < hi ? x[i - lo] : 0.f;
+      f[e] = i < hi ? flags(i, y[e]) : 0u;
+      sum4 += f[e];
+    }
     unsigned sum;
-    const unsigned at = scan((gt ? 1u : 0u) | (eq ? 0x10000u : 0u), warp_sums, &sum);
-    const unsigned a = above + (at & 0xffffu), e = equal + (at >> 16);
-    if (gt || (eq && e < need)) {
-      const unsigned to = a + min(e, need);
-      kept[to] = i;
-      w[to] = x;  // to <= i: read already
+    const unsigned at = scan<THREADS>(sum4, warp_sums, &sum);
+    unsigned a = above + (at & 0xffffu), q = equal + (at >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (f[e] == 1u || (f[e] && q < need)) {
+        const unsigned to = a + min(q, need);
+        kept[to] = i0 + 4 * tid + e;
+        w[to] = y[e];  // to <= its place: read already
+      }
+      a += f[e] & 0xffffu;
+      q += f[e] >> 16;
     }
     above += sum & 0xffffu;
     equal += sum >> 16;
   }
   __syncthreads();
-  for (int i = p.keep + tid; i < len; i += kSelThreads) w[i] = 0.f;
+  for (int i = max(p.keep, lo) + tid; i < hi; i += THREADS) w[i] = 0.f;
+  cluster_barrier<CS>();  // no block ends while another may read its counts
 }
 
 // ------------------------------------------------------------------ their rows
-// A block moves the k or the v rows of one (layer, sequence, kv head), a stretch of rows at
-// a time in ascending order: a stretch is read whole before it is written, and what later
-// stretches read lies behind what earlier ones wrote.
+// A cluster of CS blocks moves the k or the v rows of one (layer, sequence, kv head), a round
+// of CS * kRoundPieces 16-byte pieces at a time in ascending order.  A round is read whole
+// before any of it is written (a barrier of the cluster), and what later rounds read lies
+// behind what earlier ones wrote.  Where the rows are is looked up, a row to a thread, a round
+// ahead, while the data is on its way.
 constexpr int kMoveThreads = 256, kInFlight = 8;
+constexpr int kMaxRoundRows = kMoveThreads * kInFlight / 8;  // head dim 64
 
+template <int CS>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ long long s_from[3][kMaxRoundRows], s_to[3][kMaxRoundRows];  // in pieces; -1: nothing to move
   grid_go();
   grid_wait();
-  const unsigned item = blockIdx.x >> 1;
+  const unsigned stream = blockIdx.x / CS, item = stream >> 1;
+  const int rank = blockIdx.x % CS;
   const int b = (int)(item / p.Hkv) % p.g.B, h = item % p.Hkv, layer = item / p.Hkv / p.g.B;
-  if (p.g.cache_lens[b] <= p.keep || p.lens_out[b] != p.keep) return;
-  const int *kept = p.kept + (size_t)item * p.keep;
-  uint4 *pages = ((blockIdx.x & 1) ? p.v_pages : p.k_pages) + (size_t)layer * p.g.num_pages * p.g.page_size * p.Hkv * p.chunks;
-  const int c = threadIdx.x % p.chunks, rows = kMoveThreads / p.chunks;
-  for (int i0 = 0; i0 < p.keep; i0 += rows * kInFlight) {
-    uint4 x[kInFlight];
-    uint4 *to[kInFlight];
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const int i = i0 + u * rows + (int)threadIdx.x / p.chunks;
-      to[u] = nullptr;
-      if (i >= p.keep) continue;
-      const int from = kept[i];
-      const int fp = page_of(p.g, b, from), tp = page_of(p.g, b, i);
-      if (from == i || fp < 0 || tp < 0) continue;
-      x[u] = pages[(((size_t)fp * p.g.page_size + from % p.g.page_size) * p.Hkv + h) * p.chunks + c];
-      to[u] = pages + (((size_t)tp * p.g.page_size + i % p.g.page_size) * p.Hkv + h) * p.chunks + c;
+  if (p.g.cache_lens[b] <= p.keep || p.lens_out[b] != p.keep) return;  // the whole cluster
+  const int *kept = p.kept + (size_t)item * p.keep, *table = p.g.page_table + (size_t)b * p.g.max_pages;
+  uint4 *pages = ((stream & 1) ? p.v_pages : p.k_pages) + (size_t)layer * p.g.num_pages * p.g.page_size * p.Hkv * p.chunks;
+  const int shift = 31 - __clz(p.g.page_size), mask = p.g.page_size - 1;
+  const int step = kMoveThreads / p.chunks, rows = step * kInFlight;  // of a block's round
+  const int c = threadIdx.x % p.chunks, row = threadIdx.x / p.chunks;
+  const int rounds = (p.keep + CS * rows - 1) / (CS * rows);
+  auto look_up = [&](int n) {  // the rows of round n
+    const int i = (n * CS + rank) * rows + (int)threadIdx.x;
+    if ((int)threadIdx.x >= rows) return;
+    long long from = -1, to = -1;
+    if (i < p.keep) {
+      const int f = kept[i];
+      if (f != i) {
+        from = ((((long long)table[f >> shift] << shift) + (f & mask)) * p.Hkv + h) * p.chunks;
+        to = ((((long long)table[i >> shift] << shift) + (i & mask)) * p.Hkv + h) * p.chunks;
+      }
     }
-    __syncthreads();
+    s_from[n % 3][threadIdx.x] = from;
+    s_to[n % 3][threadIdx.x] = to;
+  };
+  look_up(0);
+  __syncthreads();
+  for (int n = 0; n < rounds; ++n) {
+    uint4 x[kInFlight];
+    long long from[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) from[u] = s_from[n % 3][u * step + row];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u)
-      if (to[u]) *to[u] = x[u];
+      if (from[u] >= 0) x[u] = pages[from[u] + c];
+    if (n + 1 < rounds) look_up(n + 1);
+    cluster_barrier<CS>();
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+      if (from[u] >= 0) pages[s_to[n % 3][u * step + row] + c] = x[u];
   }
+}
+
+// launch_after for clusters of CS blocks.
+template <int CS, typename... P, typename... A>
+int launch_clusters(void (*kernel)(P...), long long clusters, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * CS));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CS;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int THREADS, int BITS, int CS>
+int launch_select(const EvictParams &p, long long items, int most, cudaStream_t stream) {
+  const int part = (p.places + CS - 1) / CS + 3, cap = part < most ? part : most;  // a block's stretch
+  if (cap * 4 > 24 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, BITS, CS>,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return launch_clusters<CS>(evict_select_kernel<THREADS, BITS, CS>, items, THREADS, (size_t)cap * 4, stream, p, cap);
 }
 
 }  // namespace
@@ -210,9 +355,21 @@ int fa_cache_evict(const int *page_refs, void *k_pages, void *v_pages, const int
   p.recent = recent;
   p.chunks = d / 8;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = launch_after(evict_select_kernel, (long long)items, 1, kSelThreads, 0, s, p);
+  const long long rows = (long long)items;
+  // Short rows, many of them: small blocks, several to an SM.  Few long rows: clusters, one block to an SM.
+  constexpr int kMost = 48 * 1024;
+  if (places <= 8192 && rows > 152) rc = launch_select<256, 8, 1>(p, rows, 8192, s);
+  else if (places >= 4096 && rows * 8 <= 152 && places <= 8 * kMost) rc = launch_select<1024, 11, 8>(p, rows, kMost, s);
+  else if (places >= 4096 && rows * 4 <= 152 && places <= 4 * kMost) rc = launch_select<1024, 11, 4>(p, rows, kMost, s);
+  else rc = launch_select<1024, 11, 1>(p, rows, kMost, s);
   if (rc != FA_OK || keep == 0) return rc;
-  return launch_after(evict_move_kernel, 2 * (long long)items, 1, kMoveThreads, 0, s, p);
+  // few streams of rows: clusters, as long as one wave holds them and there are rows for all their blocks
+  const long long streams = 2 * rows, round = kMoveThreads * kInFlight / p.chunks, full = (keep + round - 1) / round;
+  auto fits = [&](int cs) { return streams * cs <= 2 * 152 && full >= cs; };
+  if (fits(8)) return launch_clusters<8>(evict_move_kernel<8>, streams, kMoveThreads, 0, s, p);
+  if (fits(4)) return launch_clusters<4>(evict_move_kernel<4>, streams, kMoveThreads, 0, s, p);
+  if (fits(2)) return launch_clusters<2>(evict_move_kernel<2>, streams, kMoveThreads, 0, s, p);
+  return launch_clusters<1>(evict_move_kernel<1>, streams, kMoveThreads, 0, s, p);
 }
 
 }  // extern "C"
