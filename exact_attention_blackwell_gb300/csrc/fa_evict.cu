@@ -82,27 +82,21 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
 }
-// A word of another block's shared memory, at the same place as here.
-__device__ __forceinline__ unsigned load_of(const unsigned *here, int rank) {
-  uint32_t addr;
-  unsigned v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(here)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // A cluster of CS blocks to a row of sums, each with a stretch of it, which it keeps in shared
 // memory (up to `cap` of them; longer rows are read again from L2, by one block).  The smallest
-// rank that stays is found from the top, BITS at a time: a histogram of the ranks that agree
+// rank that stays is found from the top, 8 bits at a time: a histogram of the ranks that agree
 // with what is known so far, and the bin in which the count from above reaches what is needed;
-// ranks of a bin that all stay need no more bits.  Every block adds up all blocks' histograms
-// for itself, so that a round costs one barrier of the cluster.
-template <int THREADS, int BITS, int CS>
+// ranks of a bin that all stay need no more bits.  Every block stores its histogram into all of
+// them, so that a round costs one barrier of the cluster and no read of another block's memory
+// (reading them cost 1.3 us a round); beside the sums over all blocks it adds up those of the
+// blocks before its own, which say where its places will go.
+template <int THREADS, int CS>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictParams p, int cap) {
-  constexpr int kBins = 1 << BITS, kOwn = kBins / THREADS;
+  constexpr int kBins = 256, kOwn = kBins / 32, kEarly = 8;
   extern __shared__ float keys[];
-  __shared__ unsigned hists[CS == 1 ? 1 : 2][kBins], warp_sums[32], s_counts;
-  __shared__ unsigned s_prefix, s_need, s_count;
+  __shared__ __align__(16) unsigned hist[kBins], hists[CS == 1 ? 1 : 2][CS == 1 ? 1 : CS][kBins];  // of all blocks
+  __shared__ unsigned warp_sums[32];
+  __shared__ unsigned s_prefix, s_need, s_count, s_above, s_equal;
   grid_go();
   grid_wait();
   const int tid = threadIdx.x;
@@ -112,103 +106,122 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   const int len = p.g.cache_lens[b];
   float *w = p.weights + (size_t)item * p.places;
   int *kept = p.kept + (size_t)item * p.keep;
+  // this block's stretch [lo, hi), x[i - lo]
+  const int n = min(max(len, 0), p.places);
+  const int part = CS == 1 ? n : ((n + CS - 1) / CS + 3) & ~3;
+  const int lo = min(rank * part, n), hi = min(lo + part, n);
+  const bool held = hi - lo <= cap;
+  float early[kEarly];  // on their way while the table is looked at
+#pragma unroll
+  for (int e = 0; e < kEarly; ++e) {
+    const int i = tid + e * THREADS;
+    early[e] = held && i < hi - lo ? w[lo + i] : 0.f;
+  }
+  // every block of the cluster has begun before another one stores into its shared memory
+  if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const bool go = goes(p, b, len);
+  if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (rank == 0 && item < (unsigned)(p.Hkv * p.g.B) && item % p.Hkv == 0 && tid == 0) p.lens_out[b] = go ? p.keep : len;
   if (!go) {  // the whole cluster
     for (int i = rank * THREADS + tid; i < p.keep; i += CS * THREADS) kept[i] = i < len ? i : -1;
     return;
   }
-  // this block's stretch [lo, hi), x[i - lo]
-  const int part = CS == 1 ? len : ((len + CS - 1) / CS + 3) & ~3;
-  const int lo = min(rank * part, len), hi = min(lo + part, len);
   const float *x = w + lo;
-  if (hi - lo <= cap) {
-#pragma unroll 16
-    for (int i = tid; i < hi - lo; i += THREADS) keys[i] = w[lo + i];
+  if (held) {
+#pragma unroll
+    for (int e = 0; e < kEarly; ++e)
+      if (const int i = tid + e * THREADS; i < hi - lo) keys[i] = early[e];
+#pragma unroll 8
+    for (int i = tid + kEarly * THREADS; i < hi - lo; i += THREADS) keys[i] = w[lo + i];
     x = keys;
   }
   const int older = len - p.recent, stay = p.keep - p.recent;
   unsigned prefix = 0, need = stay;
+  // what stays before this block's stretch: recent places, and by rank above the last one; equal to it
+  unsigned above = (unsigned)max(lo - older, 0), equal = 0;
   int shift = 32, round = 0;
   while (shift > 0 && stay > 0) {
-    const int bits = min(BITS, shift), known = shift;
-    shift -= bits;
-    unsigned *hist = hists[CS == 1 ? 0 : round & 1];
-    ++round;
-    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+    const int known = shift;
+    shift -= 8;
+    if (tid < kBins) hist[tid] = 0;
     __syncthreads();  // and x is there
 #pragma unroll 4
     for (int i = tid; i < min(hi, older) - lo; i += THREADS) {
       const unsigned r = rank_of(x[i]);
-      if (known == 32 || r >> known == prefix) atomicAdd(&hist[(r >> shift) & ((1u << bits) - 1u)], 1u);
+      if (known == 32 || r >> known == prefix) atomicAdd(&hist[(r >> shift) & 255u], 1u);
+    }
+    if (CS > 1) {
+      __syncthreads();
+      for (int i = tid; i < CS * kBins / 4; i += THREADS) {  // what these arrays held two rounds ago has been read
+        const uint4 v = reinterpret_cast<const uint4 *>(hist)[i % (kBins / 4)];
+        const uint32_t to = smem_u32(&hists[round & 1][rank][4 * (i % (kBins / 4))]);
+        st_cluster_v4(mapa_shared(to, i / (kBins / 4)), v.x, v.y, v.z, v.w);
+      }
     }
     cluster_barrier<CS>();
-    unsigned own[kOwn], count = 0, total;
+    if (tid < 32) {
+      // eight bins to a lane, the highest first; low word: all blocks, high word: those before this one
+      unsigned long long own[kOwn] = {};
 #pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-      const unsigned *bin = hist + kBins - 1 - (tid * kOwn + e);
-      own[e] = *bin;
+      for (int o = 0; o < CS; ++o)
 #pragma unroll
-      for (int o = 1; o < CS; ++o) own[e] += load_of(bin, (rank + o) % CS);
-      count += own[e];
-    }
-    unsigned above = scan<THREADS>(count, warp_sums, &total);
-    if (above < need && above + count >= need) {
+        for (int g = 0; g < 2; ++g) {
+          const unsigned *from = CS == 1 ? hist : hists[round & 1][o];
+          const uint4 v = *reinterpret_cast<const uint4 *>(from + kBins - kOwn * (tid + 1) + 4 * (1 - g));
+          const unsigned bin[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
-      for (int e = 0; e < kOwn; ++e) {
-        if (above < need && above + own[e] >= need) {
-          s_prefix = prefix << bits | (kBins - 1 - (tid * kOwn + e));
-          s_need = need - above;
-          s_count = own[e];
+          for (int e = 0; e < 4; ++e) {
+            own[4 * g + e] += bin[e];
+            if (CS > 1 && o < rank) own[4 * g + e] += (unsigned long long)bin[e] << 32;
+          }
         }
-        above += own[e];
+      unsigned long long count = 0;
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) count += own[e];
+      unsigned long long over = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, over, o);
+        if (tid >= o) over += y;
+      }
+      over -= count;
+      if ((unsigned)over < need && (unsigned)over + (unsigned)count >= need) {
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) {
+          if ((unsigned)over < need && (unsigned)over + (unsigned)own[e] >= need) {
+            s_prefix = prefix << 8 | (kBins - 1 - (kOwn * tid + e));
+            s_need = need - (unsigned)over;
+            s_count = (unsigned)own[e];
+            s_above = (unsigned)(over >> 32);
+            s_equal = (unsigned)(own[e] >> 32);
+          }
+          over += own[e];
+        }
       }
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
+    above += s_above;
+    equal = s_equal;
+    ++round;
     if (s_count == need) break;
   }
+  if (CS == 1) __syncthreads();
+  else if (stay == 0) cluster_barrier<CS>();  // every block holds its stretch, so that sums may be written
   // In order: all above it, and the first `need` that equal it; four places to a thread.
-  auto flags = [&](int i, float y) -> unsigned {  // 1: stays, 0x10000: equal to the last that stays
-    if (i >= older) return i < len ? 1u : 0u;
-    if (stay == 0) return 0u;
-    const unsigned r = rank_of(y) >> shift;
-    return r > prefix ? 1u : r == prefix ? 0x10000u : 0u;
-  };
-  unsigned above = 0, equal = 0;  // before this block's stretch
-  if (CS > 1) {
-    for (int i = tid; i < hi - lo; i += THREADS) {
-      const unsigned f = flags(lo + i, x[i]);
-      above += f & 0xffffu;
-      equal += f >> 16;
-    }
-    __syncthreads();
-    if (tid == 0) s_counts = s_count = 0;
-    __syncthreads();
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if ((tid & 31) == 0) {
-      atomicAdd(&s_counts, above);
-      atomicAdd(&s_count, equal);
-    }
-    cluster_barrier<CS>();  // and every block holds its stretch, so that sums may be written
-    above = equal = 0;
-    for (int o = 0; o < rank; ++o) {
-      above += load_of(&s_counts, o);
-      equal += load_of(&s_count, o);
-    }
-  } else {
-    __syncthreads();
-  }
   for (int i0 = lo; i0 < hi; i0 += 4 * THREADS) {
     float y[4];
-    unsigned f[4], sum4 = 0;
+    unsigned f[4], sum4 = 0;  // 1: stays, 0x10000: equal to the last that stays
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = i0 + 4 * tid + e;
       y[e] = i < hi ? x[i - lo] : 0.f;
-      f[e] = i < hi ? flags(i, y[e]) : 0u;
+      f[e] = i < hi && i >= older ? 1u : 0u;
+      if (i < min(hi, older) && stay > 0) {
+        const unsigned r = rank_of(y[e]) >> shift;
+        f[e] = r > prefix ? 1u : r == prefix ? 0x10000u : 0u;
+      }
       sum4 += f[e];
     }
     unsigned sum;
@@ -229,7 +242,6 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   }
   __syncthreads();
   for (int i = max(p.keep, lo) + tid; i < hi; i += THREADS) w[i] = 0.f;
-  cluster_barrier<CS>();  // no block ends while another may read its counts
 }
 
 // ------------------------------------------------------------------ their rows
@@ -307,13 +319,13 @@ int launch_clusters(void (*kernel)(P...), long long clusters, int threads, size_
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int THREADS, int BITS, int CS>
+template <int THREADS, int CS>
 int launch_select(const EvictParams &p, long long items, int most, cudaStream_t stream) {
   const int part = (p.places + CS - 1) / CS + 3, cap = part < most ? part : most;  // a block's stretch
-  if (cap * 4 > 24 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, BITS, CS>,
+  if (cap * 4 > 24 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, CS>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
     return FA_ERR_CUDA;
-  return launch_clusters<CS>(evict_select_kernel<THREADS, BITS, CS>, items, THREADS, (size_t)cap * 4, stream, p, cap);
+  return launch_clusters<CS>(evict_select_kernel<THREADS, CS>, items, THREADS, (size_t)cap * 4, stream, p, cap);
 }
 
 }  // namespace
@@ -358,10 +370,10 @@ int fa_cache_evict(const int *page_refs, void *k_pages, void *v_pages, const int
   const long long rows = (long long)items;
   // Short rows, many of them: small blocks, several to an SM.  Few long rows: clusters, one block to an SM.
   constexpr int kMost = 48 * 1024;
-  if (places <= 8192 && rows > 152) rc = launch_select<256, 8, 1>(p, rows, 8192, s);
-  else if (places >= 4096 && rows * 8 <= 152 && places <= 8 * kMost) rc = launch_select<1024, 11, 8>(p, rows, kMost, s);
-  else if (places >= 4096 && rows * 4 <= 152 && places <= 4 * kMost) rc = launch_select<1024, 11, 4>(p, rows, kMost, s);
-  else rc = launch_select<1024, 11, 1>(p, rows, kMost, s);
+  if (places <= 8192 && rows > 152) rc = launch_select<256, 1>(p, rows, 8192, s);
+  else if (places >= 4096 && rows * 8 <= 152 && places <= 8 * kMost) rc = launch_select<1024, 8>(p, rows, kMost, s);
+  else if (places >= 4096 && rows * 4 <= 152 && places <= 4 * kMost) rc = launch_select<1024, 4>(p, rows, kMost, s);
+  else rc = launch_select<1024, 1>(p, rows, kMost, s);
   if (rc != FA_OK || keep == 0) return rc;
   // few streams of rows: clusters, as long as one wave holds them and there are rows for all their blocks
   const long long streams = 2 * rows, round = kMoveThreads * kInFlight / p.chunks, full = (keep + round - 1) / round;
