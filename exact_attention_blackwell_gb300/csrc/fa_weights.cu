@@ -37,7 +37,7 @@ struct WeightsParams {
   PageGeom g;
   int words, max_new, total, Hkv, G, places;
   int TB, HB, RH;  // tokens of a chunk, kv heads whose rows are in shared memory together, rows from one to the next
-  bool stream;     // several chunks: one after another for each unit, else an item's rows stay
+  bool stream;     // more chunks than shared memory holds: one after another for each unit, else an item's rows stay
   float scale_log2, decay;
 };
 
@@ -49,7 +49,7 @@ struct WeightsCfg {
   static constexpr int kQBytes = NQ * D * 2, kQBoxBytes = NQ * 128;
   static constexpr int kQBufs = kQBytes > 32768 ? 1 : 2, kTermBufs = 4;
   static constexpr int kWarps = 8, kMmaWarp = 8, kKeyWarp = 9, kThreads = 32 * 11;
-  static constexpr int kTermBytes = kTermBufs * 2 * NQ * 4;
+  static constexpr int kTermBytes = kTermBufs * (3 * NQ + 4) * 4;
   static constexpr int kSmemMax = 227 * 1024;
   static constexpr int kStagesFit = (kSmemMax - 1024 - 1024 - kQBufs * kQBytes - kTermBytes) / kTileBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
@@ -62,7 +62,7 @@ struct WeightsCfg {
   // barriers: full[S], empty[S], q_full[QB], q_free[QB], t_full[TB], t_free[TB], s_full[4], s_free[4], drain
   static constexpr int kNumBars = 2 * kStages + 2 * kQBufs + 2 * kTermBufs + 9;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 256 + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 320 + 1024;
   static_assert(kSmemBytes <= kSmemMax, "shared memory budget");
 };
 
@@ -77,11 +77,10 @@ enum WeightsSite : int {
 struct WeightsWalk {
   long long base, end;  // cost before the sequence, and where the block's stretch ends
   PagedSeq s;
-  int b, u, units, chunks;  // the sequence's next unit
-  int last;                 // item (group of heads) of the unit before
+  int b, u, units, chunks, pairs;  // the sequence's next unit, its units, their cost, pairs of tiles
   // the current unit
   int group, pair, hb;
-  bool first;  // of its item in this block
+  bool first, entered;  // first: of its item in this block
 
   __device__ static PagedSeq seq(const WeightsParams &p, int b) {
     return paged_seq_of(p.cu[b], p.cu[b + 1], p.g.cache_lens[b], p.total, p.max_new, p.g.max_pages * p.g.page_size);
@@ -89,33 +88,55 @@ struct WeightsWalk {
   __device__ static int units_of(const WeightsParams &p, const PagedSeq &s) {  // fits 31 bits (checked by the host)
     return s.n == 0 ? 0 : ((s.keys + 255) >> 8) * p.Hkv;
   }
-  __device__ static int chunks_of(const WeightsParams &p, const PagedSeq &s) { return p.stream ? (s.n + p.TB - 1) / p.TB : 1; }
-  __device__ void load(const WeightsParams &p) {
-    s = seq(p, b);
+  __device__ static int chunks_of(const WeightsParams &p, const PagedSeq &s) { return (s.n + p.TB - 1) / p.TB; }
+  __device__ void enter(const WeightsParams &p, int u0) {  // the next unit is u0
     units = units_of(p, s);
     chunks = chunks_of(p, s);
-    u = 0;
-    last = -1;
+    pairs = max((s.keys + 255) >> 8, 1);
+    u = u0;
+    group = pair = 0;
+    hb = u0;
+    if (u0 > 0) {
+      group = u0 / (pairs * p.HB);
+      hb = u0 - group * pairs * p.HB;
+      pair = hb / p.HB;
+      hb -= pair * p.HB;
+    }
+    --hb;
+    entered = true;
   }
   __device__ bool next(const WeightsParams &p) {
-    for (;;) {
-      if (b >= p.g.B || base >= end) return false;
-      if (u < units) break;
+    if (b >= p.g.B) return false;
+    while (u >= units) {
       base += (long long)units * chunks;
-      if (++b < p.g.B) load(p);
+      if (++b >= p.g.B || base >= end) {
+        b = p.g.B;
+        return false;
+      }
+      s = seq(p, b);
+      enter(p, 0);
     }
     if (base + (long long)u * chunks >= end) return false;
-    const int per = ((s.keys + 255) >> 8) * p.HB;  // units of an item
-    group = u / per;
-    const int at = u - group * per;
-    pair = at / p.HB;
-    hb = at - pair * p.HB;
-    first = group != last;
-    last = group;
     ++u;
+    first = entered;
+    entered = false;
+    if (++hb == p.HB) {
+      hb = 0;
+      if (++pair == pairs) {
+        pair = 0;
+        ++group;
+        first = true;
+      }
+    }
     return true;
   }
 };
+
+// a / b rounded up, a >= 0, b > 0, in 32 bits where both fit (nearly always).
+__device__ __forceinline__ long long quot_up(long long a, long long b) {
+  const long long c = a + b - 1;
+  return ((c | b) >> 32) == 0 ? (long long)((unsigned)c / (unsigned)b) : c / b;
+}
 
 // The cost of all units and where this block begins, by the whole block together.
 template <int THREADS>
@@ -147,32 +168,73 @@ __device__ __forceinline__ void weights_start(const WeightsParams &p, long long 
     }
     return before + sum - x;
   };
-  long long total = 0;
+  long long total = 0, done = 0;
   for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
     long long sum;
     scan(cost(b0 + (int)threadIdx.x), sum);
     total += sum;
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long begin = min(per * blockIdx.x, total);
-  long long done = 0;
-  for (int b0 = 0; b0 < p.g.B; b0 += THREADS) {
+  const long long per = quot_up(total, gridDim.x), begin = min(per * blockIdx.x, total);
+  for (int b0 = 0; b0 < p.g.B && done <= begin; b0 += THREADS) {
     const int b = b0 + (int)threadIdx.x;
     long long sum;
     const long long x = cost(b), before = done + scan(x, sum);
     if (b < p.g.B && begin >= before && begin < before + x) {
-      at->b = b;
       at->s = s;
-      at->units = WeightsWalk::units_of(p, s);
-      at->chunks = WeightsWalk::chunks_of(p, s);
+      at->b = b;
       at->base = before;
       at->end = min(begin + per, total);
-      at->u = (int)((begin - before + at->chunks - 1) / at->chunks);
-      at->last = -1;
+      at->enter(p, (int)quot_up(begin - before, WeightsWalk::chunks_of(p, s)));
     }
     done += sum;
-    if (done > begin) break;
   }
+}
+
+// The same of up to 128 sequences by every warp for itself, four to a lane: no barrier, and one
+// round of loads (by the block 2900 cycles from the wait on, so 1.5 us of every call).
+constexpr int kByWarp = 128;
+__device__ __forceinline__ WeightsWalk weights_start_by_warp(const WeightsParams &p) {
+  const int lane = threadIdx.x & 31;
+  long long x[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = 4 * lane + i;
+    x[i] = 0;
+    if (b < p.g.B) {
+      const PagedSeq s = WeightsWalk::seq(p, b);
+      x[i] = (long long)WeightsWalk::units_of(p, s) * WeightsWalk::chunks_of(p, s);
+    }
+    sum += x[i];
+  }
+  long long before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  const long long total = __shfl_sync(0xffffffffu, before, 31), per = quot_up(total, gridDim.x);
+  const long long begin = min(per * blockIdx.x, total);
+  before -= sum;
+  int mine = -1;
+  long long base = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (begin >= before && begin < before + x[i]) mine = 4 * lane + i, base = before;
+    before += x[i];
+  }
+  const unsigned here = __ballot_sync(0xffffffffu, mine >= 0);
+  WeightsWalk w;
+  w.b = p.g.B;
+  w.base = w.end = 0;
+  if (here) {
+    const int from = __ffs(here) - 1;
+    w.b = __shfl_sync(0xffffffffu, mine, from);
+    w.base = __shfl_sync(0xffffffffu, base, from);
+    w.end = min(begin + per, total);
+    w.s = WeightsWalk::seq(p, w.b);
+    w.enter(p, (int)quot_up(begin - w.base, WeightsWalk::chunks_of(p, w.s)));
+  }
+  return w;
 }
 
 // Bits [lo, hi) of a 32-bit word (both may lie outside it).
@@ -209,17 +271,18 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
   WeightsWalk *at = reinterpret_cast<WeightsWalk *>(misc + 8);
-  long long *sums = reinterpret_cast<long long *>(misc + 104);  // [11]
+  long long *sums = reinterpret_cast<long long *>(misc + 104);  // [kThreads / 32]
   static_assert(sizeof(WeightsWalk) <= 96, "");
-  float *terms = reinterpret_cast<float *>(smem + C::kOffTerms);  // [kTermBufs][2][NQ]: -lse2, factor
+  constexpr int kTerms = 3 * NQ + 4;  // of a set of rows: -lse2, its factor, the weight at their base; the base
+  float *terms = reinterpret_cast<float *>(smem + C::kOffTerms);
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) {
       const uint32_t bar = bar0 + 8u * i;
-      const bool all = bar >= t_free(0) && bar < t_free(0) + 8u * C::kTermBufs, half = bar >= s_free(0, 0) && bar < drain_bar;
-      mbar_init(bar, all ? C::kWarps : half ? C::kWarps / 2 : 1);
+      const bool all = bar >= t_free(0) && bar < bar3, half = bar >= s_free(0, 0) && bar < drain_bar;
+      mbar_init(bar, all ? C::kWarps : half ? 4 : 1);
     }
     *abort_flag = 0;
     at->b = p.g.B;
@@ -234,15 +297,20 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     prefetch_tmap(&p.tm_q);
     prefetch_tmap(&p.tm_k);
   }
+  tc_fence_before();
   __syncthreads();
   grid_go();  // only now: a kernel that begins early takes no tensor memory before this one has
   grid_wait();
-  weights_start<C::kThreads>(p, sums, at);
-  tc_fence_before();
-  __syncthreads();
   tc_fence_after();
+  WeightsWalk walk;
+  if (p.g.B <= kByWarp) {
+    walk = weights_start_by_warp(p);
+  } else {
+    weights_start<C::kThreads>(p, sums, at);
+    __syncthreads();
+    walk = *at;
+  }
   const uint32_t tmem = *tmem_slot;
-  WeightsWalk walk = *at;
   bool ok = true;
 
   if (warp < C::kWarps) {
@@ -250,18 +318,58 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     const int w = warp >> 2, r = threadIdx.x & 127;
     const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(2 * w * NQ);
     const float c2 = p.scale_log2;
-    int step = 0, tile_no = 0;  // sets of rows, products of this warpgroup so far
-    while (ok && walk.next(p)) {
-      const int kv0 = (2 * walk.pair + w) * 128, pos = kv0 + r, kh = walk.group * p.HB + walk.hb;
-      const bool mine = kv0 < walk.s.keys, tail = kv0 + 128 > walk.s.len;
-      const bool out = mine && pos < walk.s.keys && pos < p.places;
-      const bool held = out && page_of(p.g, walk.b, pos) >= 0;
-      float *to = p.weights + ((size_t)walk.b * p.Hkv + kh) * p.places + pos;
-      const float old = out && p.decay != 0.f ? *to : 0.f;
-      const int j = pos - walk.s.len;  // this place among the new tokens
+    const int shift = 31 - __clz(p.g.page_size);
+    int tile_no = 0;  // products of this warpgroup so far
+    // A set of rows is a step: of an item's chunk, or (p.stream) of a unit's.  Steps looked up, waited for, given back.
+    int steps = 0, entered = 0, left = 0;
+    // A unit's place of this thread; its page and old sum are on their way while the unit before is worked on.
+    struct Unit {
+      float *to;
+      int pos, keys, len, n, start, chunks, hb, page, step;
+      float old;
+    };
+    auto look_up = [&](Unit &u) {
+      if (!walk.next(p)) return false;
+      u.keys = walk.s.keys;
+      u.len = walk.s.len;
+      u.n = walk.s.n;
+      u.start = walk.s.start;
+      u.chunks = walk.chunks;
+      u.hb = walk.hb;
+      if (p.stream || walk.first) steps += walk.chunks;
+      u.step = steps - walk.chunks;
+      u.pos = (2 * walk.pair + w) * 128 + r;
+      u.to = p.weights + ((size_t)walk.b * p.Hkv + walk.group * p.HB + walk.hb) * p.places + u.pos;
+      u.page = -1;
+      u.old = 0.f;
+      if (u.pos < min(u.keys, p.places)) {
+        u.page = p.g.page_table[(size_t)walk.b * p.g.max_pages + (u.pos >> shift)];
+        if (p.decay != 0.f) u.old = *u.to;
+      }
+      return true;
+    };
+    auto enter = [&](int step) {
+      while (ok && entered <= step) {
+        ok = mbar_wait_warp(t_full(entered % C::kTermBufs), (entered / C::kTermBufs) & 1, wctx, kWSiteTerms);
+        ++entered;
+      }
+    };
+    auto leave = [&](int step) {  // all before it (entered, as every unit goes through all its chunks)
+      for (; left < step; ++left) mbar_arrive_warp(t_free(left % C::kTermBufs));
+    };
+    Unit u;
+    bool more = look_up(u);
+    while (ok && more) {
+      Unit following;
+      more = look_up(following);
+      const int kv0 = u.pos - r;
+      const bool mine = kv0 < u.keys, tail = kv0 + 128 > u.len;
+      const bool out = u.pos < min(u.keys, p.places), held = u.page >= 0 && u.page < p.g.num_pages;
+      const bool whole = !tail && !__any_sync(0xffffffffu, out && !held);
+      const int j = u.pos - u.len;  // this place among the new tokens
       float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-      for (int c = 0; c < walk.chunks && ok; ++c) {
-        const int tok0 = c * p.TB, tokens = min(p.TB, walk.s.n - tok0), rows = tokens * p.G;
+      for (int c = 0; c < u.chunks && ok; ++c) {
+        const int tok0 = c * p.TB, tokens = min(p.TB, u.n - tok0), rows = tokens * p.G;
         // the rows that see this place
         unsigned see[NQ / 32];
 #pragma unroll
@@ -269,92 +377,115 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
         if (held && j >= 0 && p.mask) {
 #pragma unroll
           for (int i = 0; i < NQ / 32; ++i) see[i] = 0;
-          const unsigned long long *word = p.mask + (size_t)(walk.s.start + tok0) * p.words + (j >> 6);
+          const unsigned long long *word = p.mask + (size_t)(u.start + tok0) * p.words + (j >> 6);
           for (int k = 0; k < tokens; ++k, word += p.words)
             if ((*word >> (j & 63)) & 1) {
 #pragma unroll
               for (int i = 0; i < NQ / 32; ++i) see[i] |= bit_range(k * p.G - 32 * i, (k + 1) * p.G - 32 * i);
             }
         }
-        if (p.stream || walk.first) {
-          if (!p.stream && step > 0) mbar_arrive_warp(t_free((step - 1) % C::kTermBufs));
-          ok = mbar_wait_warp(t_full(step % C::kTermBufs), (step / C::kTermBufs) & 1, wctx, kWSiteTerms);
-          if (!ok) break;
-          ++step;
-        }
+        leave(u.step + (p.stream ? c : 0));
+        enter(u.step + c);
+        if (!ok) break;
         if (mine) {
-          const float4 *neg = reinterpret_cast<const float4 *>(terms + (size_t)((step - 1) % C::kTermBufs) * 2 * NQ + walk.hb * p.RH);
-          const float4 *fac = neg + NQ / 4;
+          const float *set = terms + ((u.step + c) % C::kTermBufs) * kTerms;
+          const float4 *neg = reinterpret_cast<const float4 *>(set + u.hb * p.RH), *fac = neg + NQ / 4, *at_base = fac + NQ / 4;
+          const float base = set[3 * NQ];  // not finite where the rows have none
           const int buf = tile_no & 1;
           ok = mbar_wait_warp(s_full(w, buf), (tile_no >> 1) & 1, wctx, kWSiteSFull);
           if (!ok) break;
           tc_fence_after();
-          const bool whole = !tail && !__any_sync(0xffffffffu, out && !held);
+          const uint32_t from = s_tm + (uint32_t)(buf * NQ);
+          // four columns from 4 q on, whose rows all see this place: 2^(c2 s - base) 2^(base - lse2)
+          auto add4 = [&](const uint32_t *s, int q) {
+            const float4 f = at_base[q];
+            float x[4];
+            ffma2(x[0], x[1], __uint_as_float(s[0]), __uint_as_float(s[1]), c2, c2, -base, -base);
+            ffma2(x[2], x[3], __uint_as_float(s[2]), __uint_as_float(s[3]), c2, c2, -base, -base);
 #pragma unroll
-          for (int i = 0; i < NQ / 32; ++i) {
-            if (32 * i >= rows) break;
-            uint32_t s[32];
-            tmem_ld_32x32b_x32(s_tm + (uint32_t)(buf * NQ + 32 * i), s);
-            tmem_wait_ld(s);
-            if (32 * i + 32 >= rows) {  // the last of it is read
-              tc_fence_before();
-              if (!(FA_STALL(6) && tile_no == 0 && w == 0)) mbar_arrive_warp(s_free(w, buf));
+            for (int k = 0; k < 4; ++k) x[k] = ex2_mufu(x[k]);
+            ffma2(a0, a1, x[0], x[1], f.x, f.y, a0, a1);
+            ffma2(a2, a3, x[2], x[3], f.z, f.w, a2, a3);
+          };
+          // those of them whose bits are set (rows past the last hold anything, and so do their factors)
+          auto add4_seen = [&](const uint32_t *s, int q, unsigned bits) {
+            const float4 n = neg[q], f = fac[q];
+            const float m[4] = {n.x, n.y, n.z, n.w}, g[4] = {f.x, f.y, f.z, f.w};
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = ex2_mufu(fmaf(__uint_as_float(s[k]), c2, m[k])) * g[k];
+              x[k] = (bits >> k) & 1 ? x[k] : 0.f;
             }
-            auto add = [&](bool all) {
+            fadd2(a0, a1, a0, a1, x[0], x[1]);
+            fadd2(a2, a3, a2, a3, x[2], x[3]);
+          };
+          auto read = [&] {  // the product is in registers
+            tc_fence_before();
+            if (!(FA_STALL(6) && tile_no == 0 && w == 0)) mbar_arrive_warp(s_free(w, buf));
+          };
+          if (NQ == 32 && rows <= 16) {  // a decoding step
+            uint32_t s[16];
+            tmem_ld_32x32b_x16(from, s);
+            tmem_wait_ld(s);
+            read();
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 n = neg[8 * i + e / 4], f = fac[8 * i + e / 4];
-                float x[4];
-                ffma2(x[0], x[1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), c2, c2, n.x, n.y);
-                ffma2(x[2], x[3], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), c2, c2, n.z, n.w);
+            for (int q = 0; q < 4; ++q)
+              if (4 * q < rows) add4_seen(s + 4 * q, q, see[0] >> (4 * q));
+          } else {
+            const bool fast = NQ > 32 && whole && fabsf(base) < INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = ex2_mufu(x[k]);
-                if (all) {
-                  ffma2(a0, a1, x[0], x[1], f.x, f.y, a0, a1);
-                  ffma2(a2, a3, x[2], x[3], f.z, f.w, a2, a3);
-                } else {  // rows past the last hold anything, and so do their factors
-                  const float g[4] = {f.x, f.y, f.z, f.w};
+            for (int i = 0; i < NQ / 32; ++i) {
+              if (32 * i >= rows) break;
+              uint32_t s[32];
+              tmem_ld_32x32b_x32(from + (uint32_t)(32 * i), s);
+              tmem_wait_ld(s);
+              if (32 * i + 32 >= rows) read();
+              if (fast && 32 * i + 32 <= rows) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) x[k] = (see[i] >> (e + k)) & 1 ? x[k] * g[k] : 0.f;
-                  fadd2(a0, a1, a0, a1, x[0], x[1]);
-                  fadd2(a2, a3, a2, a3, x[2], x[3]);
-                }
+                for (int q = 0; q < 8; ++q) add4(s + 4 * q, 8 * i + q);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, see[i] >> (4 * q));
               }
-            };
-            if (whole && 32 * i + 32 <= rows) add(true);
-            else add(false);
+            }
           }
           ++tile_no;
         }
-        if (p.stream) mbar_arrive_warp(t_free((step - 1) % C::kTermBufs));
       }
       const float sum = (a0 + a1) + (a2 + a3);
-      if (ok && out) *to = p.decay == 0.f ? sum : fmaf(old, p.decay, sum);
+      if (ok && out) *u.to = p.decay == 0.f ? sum : fmaf(u.old, p.decay, sum);
+      u = following;
     }
   } else if (warp == C::kMmaWarp) {
     // ===================================================== MMA issue (whole warp; the elected lane issues)
-    int fill = 0, step = 0, tile_no[2] = {0, 0};
+    int fill = 0, step = 0, base = 0, tile_no[2] = {0, 0};  // step: sets of rows entered, base: the first one of the item or unit
     const uint64_t k_desc = make_sdesc_sw128(sbase + C::kOffRing, 0, 1024);
     const uint64_t q_desc = make_sdesc_sw128(sbase + C::kOffQ, 0, 1024);
     bool any = false;
     while (ok && walk.next(p)) {
       const int nt = (2 * walk.pair + 1) * 128 < walk.s.keys ? 2 : 1;
+      if (p.stream || walk.first) {
+        if (!p.stream) {
+          if (elect_one())
+            for (int i = base; i < step; ++i) tc_commit(q_free(i % C::kQBufs));
+          __syncwarp();
+        }
+        base = step;
+      }
       for (int t = 0; t < nt && ok; ++t)
         ok = mbar_wait_warp(full_bar((fill + t) % C::kStages), ((fill + t) / C::kStages) & 1, wctx, kWSiteKeys);
       for (int c = 0; c < walk.chunks && ok; ++c) {
-        if (p.stream || walk.first) {
-          if (!p.stream && step > 0) {
-            if (elect_one()) tc_commit(q_free((step - 1) % C::kQBufs));
-            __syncwarp();
-          }
-          ok = mbar_wait_warp(q_full(step % C::kQBufs), (step / C::kQBufs) & 1, wctx, kWSiteRows);
+        const int qb = (base + c) % C::kQBufs;
+        if (base + c == step) {
+          ok = mbar_wait_warp(q_full(qb), (step / C::kQBufs) & 1, wctx, kWSiteRows);
           if (!ok) break;
           ++step;
         }
         tc_fence_after();
         const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G;
         const uint32_t idesc = make_idesc_bf16(128, (rows + 15) & ~15, false, false);
-        const uint64_t qd = q_desc + (uint64_t)((((step - 1) % C::kQBufs) * C::kQBytes + walk.hb * p.RH * 128) >> 4);
+        const uint64_t qd = q_desc + (uint64_t)((qb * C::kQBytes + walk.hb * p.RH * 128) >> 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= nt || !ok) continue;
@@ -375,7 +506,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
           ++tile_no[t];
         }
         if (p.stream && ok) {
-          if (elect_one()) tc_commit(q_free((step - 1) % C::kQBufs));
+          if (elect_one()) tc_commit(q_free(qb));
           __syncwarp();
         }
       }
@@ -420,6 +551,11 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
             tma_load_4d_hint(sbase + C::kOffRing + slot * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, &p.tm_k,
                              full_bar(slot), bx * 64, walk.group * p.HB + walk.hb, r0, page, once);
         }
+        // The old sums come with the tile: in a stream of tiles that fills the memory's queues a load takes
+        // longer than a unit.
+        if (p.decay != 0.f && lane < 4 && kv0 + 32 * lane < min(walk.s.keys, p.places))
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((size_t)walk.b * p.Hkv + walk.group * p.HB + walk.hb) * p.places +
+                                                       kv0 + 32 * lane));
         ++fill;
       }
     }
@@ -430,17 +566,25 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
   } else {
     // ===================================================== the tokens' rows and what their lse puts into the sums
     int step = 0;
+    int row_hb[NQ / 32], row_tok[NQ / 32], row_head[NQ / 32];  // of this lane's rows: kv head of the item, token, query head
+#pragma unroll
+    for (int i = 0; i < NQ / 32; ++i) {
+      const int x = lane + 32 * i, hb = x / p.RH, y = x - hb * p.RH;
+      row_tok[i] = y / p.G;
+      row_hb[i] = hb < p.HB && row_tok[i] < p.TB ? hb : -1;
+      row_head[i] = hb * p.G + y - row_tok[i] * p.G;
+    }
     while (ok && walk.next(p)) {
       for (int c = 0; c < walk.chunks && ok; ++c) {
         if (!(p.stream || walk.first)) continue;
         const int qb = step % C::kQBufs, tb = step % C::kTermBufs, tok0 = walk.s.start + c * p.TB;
-        const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G, kh = walk.group * p.HB;
-        float lse[NQ / 32];
+        const int tokens = min(p.TB, walk.s.n - c * p.TB), kh = walk.group * p.HB;
+        float lse[NQ / 32];  // on their way during the waits below
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) {
-          const int x = lane + 32 * i, hb = x / p.RH, y = x - hb * p.RH, tok = y / p.G;
           lse[i] = 0.f;
-          if (hb < p.HB && y < rows) lse[i] = p.lse[(size_t)((kh + hb) * p.G + y - tok * p.G) * p.total + tok0 + tok];
+          if (row_hb[i] >= 0 && row_tok[i] < tokens)
+            lse[i] = p.lse[(size_t)(kh * p.G + row_head[i]) * p.total + tok0 + row_tok[i]];
         }
         ok = mbar_wait_warp(q_free(qb), ((step / C::kQBufs) & 1) ^ 1, wctx, kWSiteRowsFree);
         if (!ok) break;
@@ -455,14 +599,37 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
         __syncwarp();
         ok = mbar_wait_warp(t_free(tb), (((step - 1) / C::kTermBufs) & 1) ^ 1, wctx, kWSiteTermsFree);
         if (!ok) break;
-        float *t = terms + (size_t)tb * 2 * NQ;
+        float *t = terms + tb * kTerms;
+        float hi[NQ / 32], lo[NQ / 32], top = -INFINITY, low = INFINITY;
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) {
           constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500920e-8f;  // log2(e) is their sum
-          const float hi = lse[i] * kLog2e, lo = fmaf(lse[i], kLog2e, -hi) + lse[i] * kLog2eLow;
+          hi[i] = lse[i] * kLog2e;
+          lo[i] = fmaf(lse[i], kLog2e, -hi[i]) + lse[i] * kLog2eLow;
+          if (!(fabsf(hi[i]) < INFINITY)) lo[i] = 0.f;
           // a token that saw nothing has lse = -inf and gives nothing
-          t[lane + 32 * i] = lse[i] == -INFINITY ? -INFINITY : -hi;
-          t[NQ + lane + 32 * i] = fabsf(hi) < INFINITY ? fmaf(lo, -0.693147180559945309f, 1.f) : 1.f;
+          t[lane + 32 * i] = lse[i] == -INFINITY ? -INFINITY : -hi[i];
+          t[NQ + lane + 32 * i] = fmaf(lo[i], -0.693147180559945309f, 1.f);
+          if (NQ > 32 && row_hb[i] >= 0 && row_tok[i] < tokens && fabsf(hi[i]) < INFINITY) {
+            top = fmaxf(top, hi[i]);
+            low = fminf(low, hi[i]);
+          }
+        }
+        if (NQ > 32) {  // with few rows the base is not used
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          }
+          // one base for all: a weight below 2^-62 of its row's sum may become 0
+          const float base = top - low <= 64.f ? top : INFINITY;
+#pragma unroll
+          for (int i = 0; i < NQ / 32; ++i) {
+            const float d = base - hi[i], back = base - d, rest = (base - (d + back)) + (back - hi[i]);  // base - hi = d + rest
+            const float more = fabsf(hi[i]) < INFINITY ? fmaf(rest - lo[i], 0.693147180559945309f, 1.f) : 1.f;
+            t[2 * NQ + lane + 32 * i] = lse[i] == -INFINITY ? 0.f : exp2f(d) * more;
+          }
+          if (lane == 0) t[3 * NQ] = base;
         }
         mbar_arrive_warp(t_full(tb));
       }
@@ -485,6 +652,7 @@ constexpr int kSMs = 152;
 template <int D, int NQ>
 int launch_weights(WeightsParams &p, const void *q, const void *k_pages, cudaStream_t stream) {
   using C = WeightsCfg<D, NQ>;
+  p.stream = (p.max_new + p.TB - 1) / p.TB > C::kQBufs;
   const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.total};
   const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.G * D * 2, (uint64_t)p.Hkv * p.G * D * 2};
   const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.TB};
@@ -554,10 +722,9 @@ int fa_attention_weights_paged(const void *q, const void *k_pages, const int *pa
   const bool few = max_new * p.G <= 32;
   const int room = few ? 32 : 128;
   p.TB = room / p.G < max_new ? room / p.G : max_new;
-  p.stream = max_new > p.TB;
   p.RH = (p.TB * p.G + 7) & ~7;
   p.HB = 1;
-  while (!p.stream && p.HB < 4 && Hkv % (2 * p.HB) == 0 && 2 * p.HB * p.RH <= room) p.HB *= 2;
+  while (max_new == p.TB && p.HB < 4 && Hkv % (2 * p.HB) == 0 && 2 * p.HB * p.RH <= room) p.HB *= 2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (few)
     return d == 64 ? launch_weights<64, 32>(p, q, k_pages, s)
