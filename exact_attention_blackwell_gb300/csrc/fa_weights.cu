@@ -37,6 +37,7 @@ struct WeightsParams {
   PageGeom g;
   int words, max_new, total, Hkv, G, places;
   int TB, HB, RH;  // tokens of a chunk, kv heads whose rows are in shared memory together, rows from one to the next
+  bool by_warp;    // few sequences, whose cost fits 31 bits
   bool stream;     // more chunks than shared memory holds: one after another for each unit, else an item's rows stay
   float scale_log2, decay;
 };
@@ -88,7 +89,7 @@ struct WeightsWalk {
   __device__ static int units_of(const WeightsParams &p, const PagedSeq &s) {  // fits 31 bits (checked by the host)
     return s.n == 0 ? 0 : ((s.keys + 255) >> 8) * p.Hkv;
   }
-  __device__ static int chunks_of(const WeightsParams &p, const PagedSeq &s) { return (s.n + p.TB - 1) / p.TB; }
+  __device__ static int chunks_of(const WeightsParams &p, const PagedSeq &s) { return s.n <= p.TB ? 1 : (s.n + p.TB - 1) / p.TB; }
   __device__ void enter(const WeightsParams &p, int u0) {  // the next unit is u0
     units = units_of(p, s);
     chunks = chunks_of(p, s);
@@ -190,49 +191,51 @@ __device__ __forceinline__ void weights_start(const WeightsParams &p, long long 
   }
 }
 
-// The same of up to 128 sequences by every warp for itself, four to a lane: no barrier, and one
-// round of loads (by the block 2900 cycles from the wait on, so 1.5 us of every call).
+// The same of up to 128 sequences whose cost surely fits 31 bits (p.by_warp), by every warp for
+// itself: no barrier.  A call's first product is some 5 us after its launch, most of it these
+// loads, the page table's, the first tiles' and the instructions' own way in: so little code.
 constexpr int kByWarp = 128;
 __device__ __forceinline__ WeightsWalk weights_start_by_warp(const WeightsParams &p) {
   const int lane = threadIdx.x & 31;
-  long long x[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = 4 * lane + i;
-    x[i] = 0;
-    if (b < p.g.B) {
-      const PagedSeq s = WeightsWalk::seq(p, b);
-      x[i] = (long long)WeightsWalk::units_of(p, s) * WeightsWalk::chunks_of(p, s);
-    }
-    sum += x[i];
-  }
-  long long before = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
-  }
-  const long long total = __shfl_sync(0xffffffffu, before, 31), per = quot_up(total, gridDim.x);
-  const long long begin = min(per * blockIdx.x, total);
-  before -= sum;
-  int mine = -1;
-  long long base = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (begin >= before && begin < before + x[i]) mine = 4 * lane + i, base = before;
-    before += x[i];
-  }
-  const unsigned here = __ballot_sync(0xffffffffu, mine >= 0);
+  PagedSeq s = {0, 0, 0, 0};
+  auto cost = [&](int b) -> unsigned {
+    if (b >= p.g.B) return 0u;
+    s = WeightsWalk::seq(p, b);
+    return (unsigned)(WeightsWalk::units_of(p, s) * WeightsWalk::chunks_of(p, s));
+  };
+  unsigned total = 0, done = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.g.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, cost(b0 + lane));
+  const unsigned per = (total + gridDim.x - 1) / gridDim.x, begin = min(per * blockIdx.x, total);
   WeightsWalk w;
   w.b = p.g.B;
   w.base = w.end = 0;
-  if (here) {
-    const int from = __ffs(here) - 1;
-    w.b = __shfl_sync(0xffffffffu, mine, from);
-    w.base = __shfl_sync(0xffffffffu, base, from);
-    w.end = min(begin + per, total);
-    w.s = WeightsWalk::seq(p, w.b);
-    w.enter(p, (int)quot_up(begin - w.base, WeightsWalk::chunks_of(p, w.s)));
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.g.B; b0 += 32) {
+    const unsigned x = cost(b0 + lane);
+    unsigned after = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, after, o);
+      if (lane >= o) after += y;
+    }
+    const unsigned before = done + after - x;
+    const unsigned here = __ballot_sync(0xffffffffu, begin >= before && begin - before < x);
+    if (here) {
+      const int from = __ffs(here) - 1;
+      w.b = b0 + from;
+      const unsigned base = __shfl_sync(0xffffffffu, before, from);
+      w.base = base;
+      w.end = min(begin + per, total);
+      w.s.start = __shfl_sync(0xffffffffu, s.start, from);
+      w.s.n = __shfl_sync(0xffffffffu, s.n, from);
+      w.s.len = __shfl_sync(0xffffffffu, s.len, from);
+      w.s.keys = __shfl_sync(0xffffffffu, s.keys, from);
+      const int chunks = WeightsWalk::chunks_of(p, w.s);
+      w.enter(p, chunks == 1 ? (int)(begin - base) : (int)((begin - base + chunks - 1) / chunks));
+      break;
+    }
+    done += __shfl_sync(0xffffffffu, after, 31);
   }
   return w;
 }
@@ -278,16 +281,17 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
   const WaitCtx wctx{abort_flag, p.status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  static_assert(C::kNumBars <= 32 * C::kWarps, "a thread to a barrier");
+  if (threadIdx.x < C::kNumBars) {
+    const uint32_t bar = bar0 + 8u * threadIdx.x;
+    const bool all = bar >= t_free(0) && bar < bar3, half = bar >= s_free(0, 0) && bar < drain_bar;
+    mbar_init(bar, all ? C::kWarps : half ? 4 : 1);
+    fence_mbar_init();
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kNumBars; ++i) {
-      const uint32_t bar = bar0 + 8u * i;
-      const bool all = bar >= t_free(0) && bar < bar3, half = bar >= s_free(0, 0) && bar < drain_bar;
-      mbar_init(bar, all ? C::kWarps : half ? 4 : 1);
-    }
     *abort_flag = 0;
     at->b = p.g.B;
     at->base = at->end = 0;
-    fence_mbar_init();
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -297,13 +301,22 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     prefetch_tmap(&p.tm_q);
     prefetch_tmap(&p.tm_k);
   }
+  // The last warp's rows (it needs them early): kv head of the item, token, query head.
+  int row_hb[NQ / 32], row_tok[NQ / 32], row_head[NQ / 32];  // of this lane's rows
+#pragma unroll
+  for (int i = 0; i < NQ / 32; ++i) {
+    const int x = lane + 32 * i, hb = x / p.RH, y = x - hb * p.RH;
+    row_tok[i] = y / p.G;
+    row_hb[i] = hb < p.HB && row_tok[i] < p.TB ? hb : -1;
+    row_head[i] = hb * p.G + y - row_tok[i] * p.G;
+  }
   tc_fence_before();
   __syncthreads();
   grid_go();  // only now: a kernel that begins early takes no tensor memory before this one has
   grid_wait();
   tc_fence_after();
   WeightsWalk walk;
-  if (p.g.B <= kByWarp) {
+  if (p.by_warp) {
     walk = weights_start_by_warp(p);
   } else {
     weights_start<C::kThreads>(p, sums, at);
@@ -566,14 +579,6 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
   } else {
     // ===================================================== the tokens' rows and what their lse puts into the sums
     int step = 0;
-    int row_hb[NQ / 32], row_tok[NQ / 32], row_head[NQ / 32];  // of this lane's rows: kv head of the item, token, query head
-#pragma unroll
-    for (int i = 0; i < NQ / 32; ++i) {
-      const int x = lane + 32 * i, hb = x / p.RH, y = x - hb * p.RH;
-      row_tok[i] = y / p.G;
-      row_hb[i] = hb < p.HB && row_tok[i] < p.TB ? hb : -1;
-      row_head[i] = hb * p.G + y - row_tok[i] * p.G;
-    }
     while (ok && walk.next(p)) {
       for (int c = 0; c < walk.chunks && ok; ++c) {
         if (!(p.stream || walk.first)) continue;
@@ -694,7 +699,8 @@ int fa_attention_weights_paged(const void *q, const void *k_pages, const int *pa
   if (places <= 0) return FA_ERR_INVALID_ARG;
   if ((double)B * Hkv * places >= (double)(1ll << 40)) return FA_ERR_UNSUPPORTED;
   // the units of one sequence are counted in 31 bits
-  if (((double)max_pages * page_size / 256 + 1) * Hkv >= 2147483648.0) return FA_ERR_UNSUPPORTED;
+  const double seq_units = ((double)max_pages * page_size / 256 + 1) * Hkv;
+  if (seq_units >= 2147483648.0) return FA_ERR_UNSUPPORTED;
   if (!ptr_aligned(q, 16) || !ptr_aligned(k_pages, 16)) return FA_ERR_ALIGNMENT;
   for (const void *x : {(const void *)page_table, (const void *)cache_lens, (const void *)cu_seqlens, (const void *)lse,
                         (const void *)weights})
@@ -725,6 +731,7 @@ int fa_attention_weights_paged(const void *q, const void *k_pages, const int *pa
   p.RH = (p.TB * p.G + 7) & ~7;
   p.HB = 1;
   while (max_new == p.TB && p.HB < 4 && Hkv % (2 * p.HB) == 0 && 2 * p.HB * p.RH <= room) p.HB *= 2;
+  p.by_warp = B <= kByWarp && B * seq_units * ((max_new + p.TB - 1) / p.TB) < 2147483648.0 - 4 * kSMs;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (few)
     return d == 64 ? launch_weights<64, 32>(p, q, k_pages, s)
