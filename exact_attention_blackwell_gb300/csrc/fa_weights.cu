@@ -79,8 +79,8 @@ struct WeightsWalk {
   long long base, end;  // cost before the sequence, and where the block's stretch ends
   PagedSeq s;
   int b, u, units, chunks, pairs;  // the sequence's next unit, its units, their cost, pairs of tiles
-  // the current unit
-  int group, pair, hb;
+  // the current run: units of neighbouring heads [hb, hb1) on the same places
+  int group, pair, hb, hb1;
   bool first, entered;  // first: of its item in this block
 
   __device__ static PagedSeq seq(const WeightsParams &p, int b) {
@@ -96,14 +96,13 @@ struct WeightsWalk {
     pairs = max((s.keys + 255) >> 8, 1);
     u = u0;
     group = pair = 0;
-    hb = u0;
+    hb1 = u0;  // where the next run begins
     if (u0 > 0) {
       group = u0 / (pairs * p.HB);
-      hb = u0 - group * pairs * p.HB;
-      pair = hb / p.HB;
-      hb -= pair * p.HB;
+      hb1 = u0 - group * pairs * p.HB;
+      pair = hb1 / p.HB;
+      hb1 -= pair * p.HB;
     }
-    --hb;
     entered = true;
   }
   __device__ bool next(const WeightsParams &p) {
@@ -118,17 +117,21 @@ struct WeightsWalk {
       enter(p, 0);
     }
     if (base + (long long)u * chunks >= end) return false;
-    ++u;
     first = entered;
     entered = false;
-    if (++hb == p.HB) {
-      hb = 0;
+    if (hb1 == p.HB) {
+      hb1 = 0;
       if (++pair == pairs) {
         pair = 0;
         ++group;
         first = true;
       }
     }
+    hb = hb1;
+    do {  // as far as the block's stretch goes
+      ++hb1;
+      ++u;
+    } while (hb1 < p.HB && base + (long long)u * chunks < end);
     return true;
   }
 };
@@ -335,13 +338,14 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     int tile_no = 0;  // products of this warpgroup so far
     // A set of rows is a step: of an item's chunk, or (p.stream) of a unit's.  Steps looked up, waited for, given back.
     int steps = 0, entered = 0, left = 0;
-    // A unit's place of this thread; its page and old sum are on their way while the unit before is worked on.
-    struct Unit {
-      float *to;
-      int pos, keys, len, n, start, chunks, hb, page, step;
+    // A run's place of this thread; its page and the first head's old sum are on their way while the run before is
+    // worked on.
+    struct Run {
+      float *to;  // the first head's sum
+      int pos, keys, len, n, start, chunks, hb, hb1, page, step;
       float old;
     };
-    auto look_up = [&](Unit &u) {
+    auto look_up = [&](Run &u) {
       if (!walk.next(p)) return false;
       u.keys = walk.s.keys;
       u.len = walk.s.len;
@@ -349,6 +353,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
       u.start = walk.s.start;
       u.chunks = walk.chunks;
       u.hb = walk.hb;
+      u.hb1 = walk.hb1;
       if (p.stream || walk.first) steps += walk.chunks;
       u.step = steps - walk.chunks;
       u.pos = (2 * walk.pair + w) * 128 + r;
@@ -370,21 +375,20 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     auto leave = [&](int step) {  // all before it (entered, as every unit goes through all its chunks)
       for (; left < step; ++left) mbar_arrive_warp(t_free(left % C::kTermBufs));
     };
-    Unit u;
+    Run u;
     bool more = look_up(u);
     while (ok && more) {
-      Unit following;
+      Run following;
       more = look_up(following);
       const int kv0 = u.pos - r;
       const bool mine = kv0 < u.keys, tail = kv0 + 128 > u.len;
       const bool out = u.pos < min(u.keys, p.places), held = u.page >= 0 && u.page < p.g.num_pages;
       const bool whole = !tail && !__any_sync(0xffffffffu, out && !held);
       const int j = u.pos - u.len;  // this place among the new tokens
-      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-      for (int c = 0; c < u.chunks && ok; ++c) {
-        const int tok0 = c * p.TB, tokens = min(p.TB, u.n - tok0), rows = tokens * p.G;
-        // the rows that see this place
-        unsigned see[NQ / 32];
+      // the rows of a chunk that see this place (with several heads in a run there is one chunk)
+      unsigned see[NQ / 32];
+      auto look = [&](int tok0, int tokens) {
+        const int rows = tokens * p.G;
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) see[i] = held ? bit_range((max(j - tok0, 0)) * p.G - 32 * i, rows - 32 * i) : 0u;
         if (held && j >= 0 && p.mask) {
@@ -397,77 +401,88 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
               for (int i = 0; i < NQ / 32; ++i) see[i] |= bit_range(k * p.G - 32 * i, (k + 1) * p.G - 32 * i);
             }
         }
-        leave(u.step + (p.stream ? c : 0));
-        enter(u.step + c);
-        if (!ok) break;
-        if (mine) {
-          const float *set = terms + ((u.step + c) % C::kTermBufs) * kTerms;
-          const float4 *neg = reinterpret_cast<const float4 *>(set + u.hb * p.RH), *fac = neg + NQ / 4, *at_base = fac + NQ / 4;
-          const float base = set[3 * NQ];  // not finite where the rows have none
-          const int buf = tile_no & 1;
-          ok = mbar_wait_warp(s_full(w, buf), (tile_no >> 1) & 1, wctx, kWSiteSFull);
+      };
+      float *to = u.to;
+      float old = u.old;
+      for (int h = u.hb; h < u.hb1 && ok; ++h, to += p.places) {
+        const float old_next = h + 1 < u.hb1 && out && p.decay != 0.f ? to[p.places] : 0.f;
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        for (int c = 0; c < u.chunks && ok; ++c) {
+          const int tok0 = c * p.TB, tokens = min(p.TB, u.n - tok0), rows = tokens * p.G;
+          if (h == u.hb) look(tok0, tokens);
+          leave(u.step + (p.stream ? c : 0));
+          enter(u.step + c);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t from = s_tm + (uint32_t)(buf * NQ);
-          // four columns from 4 q on, whose rows all see this place: 2^(c2 s - base) 2^(base - lse2)
-          auto add4 = [&](const uint32_t *s, int q) {
-            const float4 f = at_base[q];
-            float x[4];
-            ffma2(x[0], x[1], __uint_as_float(s[0]), __uint_as_float(s[1]), c2, c2, -base, -base);
-            ffma2(x[2], x[3], __uint_as_float(s[2]), __uint_as_float(s[3]), c2, c2, -base, -base);
+          if (mine) {
+            const float *set = terms + ((u.step + c) % C::kTermBufs) * kTerms;
+            const float4 *neg = reinterpret_cast<const float4 *>(set + h * p.RH), *fac = neg + NQ / 4, *at_base = fac + NQ / 4;
+            const float base = set[3 * NQ];  // not finite where the rows have none
+            const int buf = tile_no & 1;
+            ok = mbar_wait_warp(s_full(w, buf), (tile_no >> 1) & 1, wctx, kWSiteSFull);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t from = s_tm + (uint32_t)(buf * NQ);
+            // four columns from 4 q on, whose rows all see this place: 2^(c2 s - base) 2^(base - lse2)
+            auto add4 = [&](const uint32_t *s, int q) {
+              const float4 f = at_base[q];
+              float x[4];
+              ffma2(x[0], x[1], __uint_as_float(s[0]), __uint_as_float(s[1]), c2, c2, -base, -base);
+              ffma2(x[2], x[3], __uint_as_float(s[2]), __uint_as_float(s[3]), c2, c2, -base, -base);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = ex2_mufu(x[k]);
-            ffma2(a0, a1, x[0], x[1], f.x, f.y, a0, a1);
-            ffma2(a2, a3, x[2], x[3], f.z, f.w, a2, a3);
-          };
-          // those of them whose bits are set (rows past the last hold anything, and so do their factors)
-          auto add4_seen = [&](const uint32_t *s, int q, unsigned bits) {
-            const float4 n = neg[q], f = fac[q];
-            const float m[4] = {n.x, n.y, n.z, n.w}, g[4] = {f.x, f.y, f.z, f.w};
-            float x[4];
+              for (int k = 0; k < 4; ++k) x[k] = ex2_mufu(x[k]);
+              ffma2(a0, a1, x[0], x[1], f.x, f.y, a0, a1);
+              ffma2(a2, a3, x[2], x[3], f.z, f.w, a2, a3);
+            };
+            // those of them whose bits are set (rows past the last hold anything, and so do their factors)
+            auto add4_seen = [&](const uint32_t *s, int q, unsigned bits) {
+              const float4 n = neg[q], f = fac[q];
+              const float m[4] = {n.x, n.y, n.z, n.w}, g[4] = {f.x, f.y, f.z, f.w};
+              float x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[k] = ex2_mufu(fmaf(__uint_as_float(s[k]), c2, m[k])) * g[k];
-              x[k] = (bits >> k) & 1 ? x[k] : 0.f;
-            }
-            fadd2(a0, a1, a0, a1, x[0], x[1]);
-            fadd2(a2, a3, a2, a3, x[2], x[3]);
-          };
-          auto read = [&] {  // the product is in registers
-            tc_fence_before();
-            if (!(FA_STALL(6) && tile_no == 0 && w == 0)) mbar_arrive_warp(s_free(w, buf));
-          };
-          if (NQ == 32 && rows <= 16) {  // a decoding step
-            uint32_t s[16];
-            tmem_ld_32x32b_x16(from, s);
-            tmem_wait_ld(s);
-            read();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (4 * q < rows) add4_seen(s + 4 * q, q, see[0] >> (4 * q));
-          } else {
-            const bool fast = NQ > 32 && whole && fabsf(base) < INFINITY;
-#pragma unroll
-            for (int i = 0; i < NQ / 32; ++i) {
-              if (32 * i >= rows) break;
-              uint32_t s[32];
-              tmem_ld_32x32b_x32(from + (uint32_t)(32 * i), s);
+              for (int k = 0; k < 4; ++k) {
+                x[k] = ex2_mufu(fmaf(__uint_as_float(s[k]), c2, m[k])) * g[k];
+                x[k] = (bits >> k) & 1 ? x[k] : 0.f;
+              }
+              fadd2(a0, a1, a0, a1, x[0], x[1]);
+              fadd2(a2, a3, a2, a3, x[2], x[3]);
+            };
+            auto read = [&] {  // the product is in registers
+              tc_fence_before();
+              if (!(FA_STALL(6) && tile_no == 0 && w == 0)) mbar_arrive_warp(s_free(w, buf));
+            };
+            if (NQ == 32 && rows <= 16) {  // a decoding step
+              uint32_t s[16];
+              tmem_ld_32x32b_x16(from, s);
               tmem_wait_ld(s);
-              if (32 * i + 32 >= rows) read();
-              if (fast && 32 * i + 32 <= rows) {
+              read();
 #pragma unroll
-                for (int q = 0; q < 8; ++q) add4(s + 4 * q, 8 * i + q);
-              } else {
+              for (int q = 0; q < 4; ++q)
+                if (4 * q < rows) add4_seen(s + 4 * q, q, see[0] >> (4 * q));
+            } else {
+              const bool fast = NQ > 32 && whole && fabsf(base) < INFINITY;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, see[i] >> (4 * q));
+              for (int i = 0; i < NQ / 32; ++i) {
+                if (32 * i >= rows) break;
+                uint32_t s[32];
+                tmem_ld_32x32b_x32(from + (uint32_t)(32 * i), s);
+                tmem_wait_ld(s);
+                if (32 * i + 32 >= rows) read();
+                if (fast && 32 * i + 32 <= rows) {
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) add4(s + 4 * q, 8 * i + q);
+                } else {
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, see[i] >> (4 * q));
+                }
               }
             }
+            ++tile_no;
           }
-          ++tile_no;
         }
+        const float sum = (a0 + a1) + (a2 + a3);
+        if (ok && out) *to = p.decay == 0.f ? sum : fmaf(old, p.decay, sum);
+        old = old_next;
       }
-      const float sum = (a0 + a1) + (a2 + a3);
-      if (ok && out) *u.to = p.decay == 0.f ? sum : fmaf(u.old, p.decay, sum);
       u = following;
     }
   } else if (warp == C::kMmaWarp) {
@@ -486,48 +501,50 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
         }
         base = step;
       }
-      for (int t = 0; t < nt && ok; ++t)
-        ok = mbar_wait_warp(full_bar((fill + t) % C::kStages), ((fill + t) / C::kStages) & 1, wctx, kWSiteKeys);
-      for (int c = 0; c < walk.chunks && ok; ++c) {
-        const int qb = (base + c) % C::kQBufs;
-        if (base + c == step) {
-          ok = mbar_wait_warp(q_full(qb), (step / C::kQBufs) & 1, wctx, kWSiteRows);
-          if (!ok) break;
-          ++step;
-        }
-        tc_fence_after();
-        const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G;
-        const uint32_t idesc = make_idesc_bf16(128, (rows + 15) & ~15, false, false);
-        const uint64_t qd = q_desc + (uint64_t)((qb * C::kQBytes + walk.hb * p.RH * 128) >> 4);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t >= nt || !ok) continue;
-          const int buf = tile_no[t] & 1;
-          ok = mbar_wait_warp(s_free(t, buf), ((tile_no[t] >> 1) & 1) ^ 1, wctx, kWSiteSFree);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t kd = k_desc + (uint64_t)((((fill + t) % C::kStages) * C::kTileBytes) >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + (uint32_t)((2 * t + buf) * NQ), kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4),
-                     qd + (uint32_t)(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0);
-            tc_commit(s_full(t, buf));
+      for (int h = walk.hb; h < walk.hb1 && ok; ++h) {
+        for (int t = 0; t < nt && ok; ++t)
+          ok = mbar_wait_warp(full_bar((fill + t) % C::kStages), ((fill + t) / C::kStages) & 1, wctx, kWSiteKeys);
+        for (int c = 0; c < walk.chunks && ok; ++c) {
+          const int qb = (base + c) % C::kQBufs;
+          if (base + c == step) {
+            ok = mbar_wait_warp(q_full(qb), (step / C::kQBufs) & 1, wctx, kWSiteRows);
+            if (!ok) break;
+            ++step;
           }
-          __syncwarp();
-          any = true;
-          ++tile_no[t];
+          tc_fence_after();
+          const int rows = min(p.TB, walk.s.n - c * p.TB) * p.G;
+          const uint32_t idesc = make_idesc_bf16(128, (rows + 15) & ~15, false, false);
+          const uint64_t qd = q_desc + (uint64_t)((qb * C::kQBytes + h * p.RH * 128) >> 4);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= nt || !ok) continue;
+            const int buf = tile_no[t] & 1;
+            ok = mbar_wait_warp(s_free(t, buf), ((tile_no[t] >> 1) & 1) ^ 1, wctx, kWSiteSFree);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = k_desc + (uint64_t)((((fill + t) % C::kStages) * C::kTileBytes) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tmem + (uint32_t)((2 * t + buf) * NQ), kd + (uint32_t)(((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4),
+                       qd + (uint32_t)(((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4), idesc, kk > 0);
+              tc_commit(s_full(t, buf));
+            }
+            __syncwarp();
+            any = true;
+            ++tile_no[t];
+          }
+          if (p.stream && ok) {
+            if (elect_one()) tc_commit(q_free(qb));
+            __syncwarp();
+          }
         }
-        if (p.stream && ok) {
-          if (elect_one()) tc_commit(q_free(qb));
-          __syncwarp();
-        }
+        if (!ok) break;
+        if (elect_one())
+          for (int t = 0; t < nt; ++t) tc_commit(empty_bar((fill + t) % C::kStages));
+        __syncwarp();
+        fill += nt;
       }
-      if (!ok) break;
-      if (elect_one())
-        for (int t = 0; t < nt; ++t) tc_commit(empty_bar((fill + t) % C::kStages));
-      __syncwarp();
-      fill += nt;
     }
     // Drain: every MMA this warp issued completes before TMEM is released.
     if (any) {
@@ -546,30 +563,37 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
     int fill = 0;
     while (ok && walk.next(p)) {
       const int *row = p.g.page_table + (size_t)walk.b * p.g.max_pages;
-      for (int t = 0; t < 2 && ok; ++t) {
-        const int kv0 = (2 * walk.pair + t) * 128, pos = kv0 + lane * box_rows;
-        if (kv0 >= walk.s.keys) break;
-        int page = -1;
-        if (lane < boxes && pos < walk.s.keys) page = row[pos >> shift];
-        const int slot = fill % C::kStages;
-        ok = mbar_wait_warp(empty_bar(slot), ((fill / C::kStages) & 1) ^ 1, wctx, kWSiteEmpty);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), C::kTileBytes);
-        __syncwarp();
-        if (lane < boxes) {
-          const int r0 = pos & (p.g.page_size - 1);
-          page = page >= 0 && page < p.g.num_pages ? page : -1;  // -1: zeros
+      int pages[2];
 #pragma unroll
-          for (int bx = 0; bx < C::kBoxes; ++bx)
-            tma_load_4d_hint(sbase + C::kOffRing + slot * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, &p.tm_k,
-                             full_bar(slot), bx * 64, walk.group * p.HB + walk.hb, r0, page, once);
+      for (int t = 0; t < 2; ++t) {
+        const int pos = (2 * walk.pair + t) * 128 + lane * box_rows;
+        pages[t] = lane < boxes && pos < walk.s.keys ? row[pos >> shift] : -1;
+        if (pages[t] < 0 || pages[t] >= p.g.num_pages) pages[t] = -1;  // zeros
+      }
+      for (int h = walk.hb; h < walk.hb1 && ok; ++h) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int kv0 = (2 * walk.pair + t) * 128, pos = kv0 + lane * box_rows;
+          if (kv0 >= walk.s.keys || !ok) break;
+          const int slot = fill % C::kStages;
+          ok = mbar_wait_warp(empty_bar(slot), ((fill / C::kStages) & 1) ^ 1, wctx, kWSiteEmpty);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), C::kTileBytes);
+          __syncwarp();
+          if (lane < boxes) {
+            const int r0 = pos & (p.g.page_size - 1);
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_4d_hint(sbase + C::kOffRing + slot * C::kTileBytes + bx * C::kBoxBytes + lane * box_rows * 128, &p.tm_k,
+                               full_bar(slot), bx * 64, walk.group * p.HB + h, r0, pages[t], once);
+          }
+          // The old sums come with the tile: in a stream of tiles that fills the memory's queues a load takes
+          // longer than a unit.
+          if (p.decay != 0.f && lane < 4 && kv0 + 32 * lane < min(walk.s.keys, p.places))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((size_t)walk.b * p.Hkv + walk.group * p.HB + h) * p.places +
+                                                         kv0 + 32 * lane));
+          ++fill;
         }
-        // The old sums come with the tile: in a stream of tiles that fills the memory's queues a load takes
-        // longer than a unit.
-        if (p.decay != 0.f && lane < 4 && kv0 + 32 * lane < min(walk.s.keys, p.places))
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((size_t)walk.b * p.Hkv + walk.group * p.HB + walk.hb) * p.places +
-                                                       kv0 + 32 * lane));
-        ++fill;
       }
     }
     // Every copy issued lands before the block exits (normally they already have).
