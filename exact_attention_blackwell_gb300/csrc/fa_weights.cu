@@ -48,7 +48,7 @@ struct WeightsCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = 128 * D * 2, kBoxBytes = 128 * 128;  // a tile of K, its 64-column box
   static constexpr int kQBytes = NQ * D * 2, kQBoxBytes = NQ * 128;
-  static constexpr int kQBufs = kQBytes > 32768 ? 1 : 2, kTermBufs = 4;
+  static constexpr int kQBufs = NQ == 32 ? 2 : 65536 / kQBytes, kTermBufs = 8;  // sets of rows in shared memory; of their terms
   static constexpr int kWarps = 8, kMmaWarp = 8, kKeyWarp = 9, kThreads = 32 * 11;
   static constexpr int kTermBytes = kTermBufs * (3 * NQ + 4) * 4;
   static constexpr int kSmemMax = 227 * 1024;
@@ -603,18 +603,22 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
   } else {
     // ===================================================== the tokens' rows and what their lse puts into the sums
     int step = 0;
-    while (ok && walk.next(p)) {
-      for (int c = 0; c < walk.chunks && ok; ++c) {
-        if (!(p.stream || walk.first)) continue;
-        const int qb = step % C::kQBufs, tb = step % C::kTermBufs, tok0 = walk.s.start + c * p.TB;
-        const int tokens = min(p.TB, walk.s.n - c * p.TB), kh = walk.group * p.HB;
-        float lse[NQ / 32];  // on their way during the waits below
+    float lse[NQ / 32];  // of the next chunk: on their way during the waits of the one before
+    auto look_up = [&](int c) {
+      const int tok0 = c * p.TB, tokens = min(p.TB, walk.s.n - tok0);
 #pragma unroll
-        for (int i = 0; i < NQ / 32; ++i) {
-          lse[i] = 0.f;
-          if (row_hb[i] >= 0 && row_tok[i] < tokens)
-            lse[i] = p.lse[(size_t)(kh * p.G + row_head[i]) * p.total + tok0 + row_tok[i]];
-        }
+      for (int i = 0; i < NQ / 32; ++i) {
+        lse[i] = 0.f;
+        if (row_hb[i] >= 0 && row_tok[i] < tokens)
+          lse[i] = p.lse[(size_t)(walk.group * p.HB * p.G + row_head[i]) * p.total + walk.s.start + tok0 + row_tok[i]];
+      }
+    };
+    while (ok && walk.next(p)) {
+      if (!(p.stream || walk.first)) continue;
+      look_up(0);
+      for (int c = 0; c < walk.chunks && ok; ++c) {
+        const int qb = step % C::kQBufs, tb = step % C::kTermBufs;
+        const int tokens = min(p.TB, walk.s.n - c * p.TB);
         ok = mbar_wait_warp(q_free(qb), ((step / C::kQBufs) & 1) ^ 1, wctx, kWSiteRowsFree);
         if (!ok) break;
         if (lane == 0) {
@@ -622,22 +626,26 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
           for (int hb = 0; hb < p.HB; ++hb)
             for (int bx = 0; bx < C::kBoxes; ++bx)
               tma_load_4d(sbase + C::kOffQ + qb * C::kQBytes + bx * C::kQBoxBytes + hb * p.RH * 128, &p.tm_q, q_full(qb), bx * 64, 0,
-                          kh + hb, tok0);
+                          walk.group * p.HB + hb, walk.s.start + c * p.TB);
         }
         ++step;
         __syncwarp();
         ok = mbar_wait_warp(t_free(tb), (((step - 1) / C::kTermBufs) & 1) ^ 1, wctx, kWSiteTermsFree);
         if (!ok) break;
         float *t = terms + tb * kTerms;
+        float here[NQ / 32];
+#pragma unroll
+        for (int i = 0; i < NQ / 32; ++i) here[i] = lse[i];
+        if (c + 1 < walk.chunks) look_up(c + 1);
         float hi[NQ / 32], lo[NQ / 32], top = -INFINITY, low = INFINITY;
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) {
           constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500920e-8f;  // log2(e) is their sum
-          hi[i] = lse[i] * kLog2e;
-          lo[i] = fmaf(lse[i], kLog2e, -hi[i]) + lse[i] * kLog2eLow;
+          hi[i] = here[i] * kLog2e;
+          lo[i] = fmaf(here[i], kLog2e, -hi[i]) + here[i] * kLog2eLow;
           if (!(fabsf(hi[i]) < INFINITY)) lo[i] = 0.f;
           // a token that saw nothing has lse = -inf and gives nothing
-          t[lane + 32 * i] = lse[i] == -INFINITY ? -INFINITY : -hi[i];
+          t[lane + 32 * i] = here[i] == -INFINITY ? -INFINITY : -hi[i];
           t[NQ + lane + 32 * i] = fmaf(lo[i], -0.693147180559945309f, 1.f);
           if (NQ > 32 && row_hb[i] >= 0 && row_tok[i] < tokens && fabsf(hi[i]) < INFINITY) {
             top = fmaxf(top, hi[i]);
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
           for (int i = 0; i < NQ / 32; ++i) {
             const float d = base - hi[i], back = base - d, rest = (base - (d + back)) + (back - hi[i]);  // base - hi = d + rest
             const float more = fabsf(hi[i]) < INFINITY ? fmaf(rest - lo[i], 0.693147180559945309f, 1.f) : 1.f;
-            t[2 * NQ + lane + 32 * i] = lse[i] == -INFINITY ? 0.f : exp2f(d) * more;
+            t[2 * NQ + lane + 32 * i] = here[i] == -INFINITY ? 0.f : exp2f(d) * more;
           }
           if (lane == 0) t[3 * NQ] = base;
         }
