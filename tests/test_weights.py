@@ -101,6 +101,8 @@ CASES = [
     ([700, 300], [33, 31], 128, 20, 4, 256),
     ([40, 500, 90], [4, 2, 4], 16, 12, 3, 128),
     ([2] * 700, [1] * 700, 16, 2, 1, 64),
+    ([500, 20], [256, 70], 32, 4, 1, 64),
+    ([300, 290, 10], [1, 40, 130], 32, 4, 2, 128),
 ]
 
 
