@@ -381,9 +381,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
       Run following;
       more = look_up(following);
       const int kv0 = u.pos - r;
-      const bool mine = kv0 < u.keys, tail = kv0 + 128 > u.len;
+      const bool mine = kv0 < u.keys;
       const bool out = u.pos < min(u.keys, p.places), held = u.page >= 0 && u.page < p.g.num_pages;
-      const bool whole = !tail && !__any_sync(0xffffffffu, out && !held);
       const int j = u.pos - u.len;  // this place among the new tokens
       // the rows of a chunk that see this place (with several heads in a run there is one chunk)
       unsigned see[NQ / 32];
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
               for (int q = 0; q < 4; ++q)
                 if (4 * q < rows) add4_seen(s + 4 * q, q, see[0] >> (4 * q));
             } else {
-              const bool fast = NQ > 32 && whole && fabsf(base) < INFINITY;
+              const bool based = NQ > 32 && fabsf(base) < INFINITY;
 #pragma unroll
               for (int i = 0; i < NQ / 32; ++i) {
                 if (32 * i >= rows) break;
@@ -467,10 +466,12 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
                 tmem_ld_32x32b_x32(from + (uint32_t)(32 * i), s);
                 tmem_wait_ld(s);
                 if (32 * i + 32 >= rows) read();
-                if (fast && 32 * i + 32 <= rows) {
+                // 32 rows that see all of the warp's places, or none (what a thread without a place sums up is lost)
+                const bool all = __all_sync(0xffffffffu, !out || see[i] == 0xffffffffu);
+                if (based && all) {
 #pragma unroll
                   for (int q = 0; q < 8; ++q) add4(s + 4 * q, 8 * i + q);
-                } else {
+                } else if (__any_sync(0xffffffffu, out && see[i] != 0u)) {
 #pragma unroll
                   for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, see[i] >> (4 * q));
                 }
