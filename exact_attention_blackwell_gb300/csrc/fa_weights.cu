@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
       const bool mine = kv0 < u.keys;
       const bool out = u.pos < min(u.keys, p.places), held = u.page >= 0 && u.page < p.g.num_pages;
       const int j = u.pos - u.len;  // this place among the new tokens
+      // every row sees all of the warp's places (what a thread without a place sums up is lost)
+      const bool whole = __all_sync(0xffffffffu, !out || (held && j < 0));
       // the rows of a chunk that see this place (with several heads in a run there is one chunk)
       unsigned see[NQ / 32];
       auto look = [&](int tok0, int tokens) {
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         for (int c = 0; c < u.chunks && ok; ++c) {
           const int tok0 = c * p.TB, tokens = min(p.TB, u.n - tok0), rows = tokens * p.G;
-          if (h == u.hb) look(tok0, tokens);
+          if (!whole && h == u.hb) look(tok0, tokens);
           leave(u.step + (p.stream ? c : 0));
           enter(u.step + c);
           if (!ok) break;
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
               read();
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                if (4 * q < rows) add4_seen(s + 4 * q, q, see[0] >> (4 * q));
+                if (4 * q < rows) add4_seen(s + 4 * q, q, (whole ? bit_range(0, rows) : see[0]) >> (4 * q));
             } else {
               const bool based = NQ > 32 && fabsf(base) < INFINITY;
 #pragma unroll
@@ -466,14 +468,14 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
                 tmem_ld_32x32b_x32(from + (uint32_t)(32 * i), s);
                 tmem_wait_ld(s);
                 if (32 * i + 32 >= rows) read();
-                // 32 rows that see all of the warp's places, or none (what a thread without a place sums up is lost)
-                const bool all = __all_sync(0xffffffffu, !out || see[i] == 0xffffffffu);
-                if (based && all) {
+                // 32 rows that see all of the warp's places, or none
+                const unsigned bits = whole ? bit_range(0, rows - 32 * i) : see[i];
+                if (based && __all_sync(0xffffffffu, !out || bits == 0xffffffffu)) {
 #pragma unroll
                   for (int q = 0; q < 8; ++q) add4(s + 4 * q, 8 * i + q);
-                } else if (__any_sync(0xffffffffu, out && see[i] != 0u)) {
+                } else if (__any_sync(0xffffffffu, out && bits != 0u)) {
 #pragma unroll
-                  for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, see[i] >> (4 * q));
+                  for (int q = 0; q < 8; ++q) add4_seen(s + 4 * q, 8 * i + q, bits >> (4 * q));
                 }
               }
             }
