@@ -938,7 +938,9 @@ def attention_weights_paged(q, k_pages, page_table, cache_lens, cu_seqlens, max_
     """The attention weight that every place of the cache got in :func:`attention_fwd_paged` (same operands; lse
     is what that call returned), summed over a sequence's new tokens and the query heads of each kv head and
     added to decay times what weights (float32 [B,Hkv,places]) holds, in place -> weights.  decay 0 replaces
-    the old sums.  Columns behind a sequence, and sequences without new tokens, are left alone."""
+    the old sums.  Columns behind a sequence, and sequences without new tokens, are left alone.  What
+    :func:`cache_fork` and :func:`cache_compact` do to rows and places is the caller's to do to the sums too, and
+    to clear those behind a sequence that became shorter (:func:`cache_evict` moves and clears its own)."""
     if stream is None:
         w = (_fast or _paged_binding()).weights(q, k_pages, page_table, cache_lens, cu_seqlens, max_new, lse, weights,
                                                 tree_mask, decay, scale)

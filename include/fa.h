@@ -317,7 +317,7 @@ int fa_cache_resize(int *page_refs, void *k_pages, void *v_pages, int *page_tabl
  *   q_out, k_out : bf16, dense; may be q and k themselves where those are dense,
  *                and otherwise overlap none of the inputs
  *   positions  : DEVICE int32 [n_axes, total], any values; the angle is exact
- *                to 1e-7 radians for all of them
+ *                to 2e-7 radians for all of them
  *   inv_freq   : DEVICE fp32 [rot / 2], finite; rot a multiple of 16, at most d
  *   axes       : HOST array of rot / 2 axes in [0, n_axes), read during the call,
  *                or NULL (n_axes = 1); n_axes at most 4
@@ -371,7 +371,11 @@ int fa_cache_append_rope(const void *q, long long q_token, long long q_head, con
  *   weights : fp32 [B, Hkv, places]; places past the last column are not written,
  *     nor are those behind a sequence, nor sequences without new tokens
  *   decay   : finite, >= 0; with 0 the old contents are not read
- * No atomics: bitwise reproducible. */
+ * The sums are the caller's: fa_cache_fork and fa_cache_compact know nothing of
+ * them, so rows that change have to be copied, places that move moved, and sums
+ * behind a sequence that became shorter cleared before new tokens come there
+ * (fa_cache_evict does all that for its own moves).  No atomics: bitwise
+ * reproducible. */
 int fa_attention_weights_paged(const void *q, const void *k_pages, const int *page_table, const int *cache_lens,
                                const int *cu_seqlens, const long long *tree_mask, int mask_words, const float *lse,
                                float *weights, int places, float decay, int B, int max_pages, int num_pages,
