@@ -347,7 +347,8 @@ int fa_cache_evict(const int *page_refs, void *k_pages, void *v_pages, const int
   int rc = check_page_table(B, max_pages, num_pages, page_size);
   if (rc == FA_OK) rc = check_page_rows(layers, num_pages, page_size, Hkv, d);
   if (rc != FA_OK) return rc;
-  if (places <= 0 || keep < 0 || recent < 0 || recent > keep || lens_out == cache_lens) return FA_ERR_INVALID_ARG;
+  if (places <= 0 || keep < 0 || recent < 0 || recent > keep || lens_out == cache_lens || k_pages == v_pages)
+    return FA_ERR_INVALID_ARG;
   const double items = (double)layers * B * Hkv;
   if (items > 1073741823.0 || items * places >= (double)(1ll << 40) || items * keep >= (double)(1ll << 40))
     return FA_ERR_UNSUPPORTED;

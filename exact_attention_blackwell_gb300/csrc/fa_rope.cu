@@ -765,7 +765,7 @@ int fa_cache_append_rope(const void *q, long long q_token, long long q_head, con
   if (rc == FA_OK) rc = check_page_rows(1, num_pages, page_size, Hkv, d);
   if (rc == FA_OK) rc = check_rope(total, H, Hkv, d, rot, n_axes, axes, eps, inv_freq, positions);
   if (rc != FA_OK) return rc;
-  if (total > 0 && (!q || !k || !v || !q_out)) return FA_ERR_INVALID_ARG;
+  if ((total > 0 && (!q || !k || !v || !q_out)) || k_pages == v_pages) return FA_ERR_INVALID_ARG;
   if (check_rows(q, q_token, q_head) || check_rows(k, k_token, k_head) || check_rows(v, v_token, v_head) ||
       check_rows(q_out, 0, 0) || check_rows(k_pages, 0, 0) || check_rows(v_pages, 0, 0) ||
       check_weights(q_weight, k_weight, bf16_weights))

@@ -351,7 +351,8 @@ int fa_qk_norm_rope_bwd(const void *dq_out, long long dq_token, long long dq_hea
  * i.  positions as above, or NULL: every axis takes the place in the cache
  * (which stops being a token's position once places were evicted).  Rows past
  * the table, or whose page entry names no page, are dropped (their queries are
- * written); rows of q_out that belong to no sequence are left as they were. */
+ * written); rows of q_out that belong to no sequence are left as they were.
+ * k_pages and v_pages are two tensors. */
 int fa_cache_append_rope(const void *q, long long q_token, long long q_head, const void *k, long long k_token,
                          long long k_head, const void *v, long long v_token, long long v_head, void *k_pages,
                          void *v_pages, const int *page_table, const int *cache_lens, const int *cu_seqlens,
@@ -395,7 +396,8 @@ int fa_attention_weights_paged(const void *q, const void *k_pages, const int *pa
  *     weights or than the table, or a place without a page, or shares a page that
  *     would be written with another row (page_refs above 1)
  *   kept     : int32 [layers, B, Hkv, keep]: which place each place was, -1 from
- *     lens_out[b] on (may be NULL where keep = 0) */
+ *     lens_out[b] on (may be NULL where keep = 0)
+ * k_pages and v_pages are two tensors. */
 int fa_cache_evict(const int *page_refs, void *k_pages, void *v_pages, const int *page_table, const int *cache_lens,
                    float *weights, int places, int keep, int recent, int *lens_out, int *kept, int B, int max_pages,
                    int num_pages, int page_size, int layers, int Hkv, int d, void *stream);

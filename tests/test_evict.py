@@ -193,11 +193,11 @@ def test_captured_on_a_stream_and_twice():
     (dict(lens_out=A), INV), (dict(places=0), INV), (dict(keep=-1), INV), (dict(recent=-1), INV), (dict(recent=4), INV),
     (dict(B=0), INV), (dict(B=65536), UNS), (dict(page_size=24), UNS), (dict(layers=0), INV), (dict(layers=65536), UNS),
     (dict(Hkv=0), INV), (dict(d=96), UNS), (dict(max_pages=1 << 27), UNS), (dict(k_pages=A + 8), ALI), (dict(v_pages=A + 4), ALI),
-    (dict(page_refs=A + 2), ALI), (dict(weights=A + 1), ALI), (dict(lens_out=A + 66), ALI), (dict(kept=A + 2), ALI),
+    (dict(v_pages=A), INV), (dict(page_refs=A + 2), ALI), (dict(weights=A + 1), ALI), (dict(lens_out=A + 66), ALI), (dict(kept=A + 2), ALI),
     (dict(B=65535, layers=65535, num_pages=1), UNS), (dict(B=65535, Hkv=1000, num_pages=1, places=2**31 - 1), UNS),
     (dict(B=65535, Hkv=1000, num_pages=1, keep=2**31 - 1), UNS)], ids=lambda x: str(x) if isinstance(x, dict) else None)
 def test_refusals(args, code):
-    a = dict(page_refs=A, k_pages=A, v_pages=A, page_table=A, cache_lens=A, weights=A, places=70, keep=3, recent=1, lens_out=A + 64,
+    a = dict(page_refs=A, k_pages=A, v_pages=A + 4096, page_table=A, cache_lens=A, weights=A, places=70, keep=3, recent=1, lens_out=A + 64,
              kept=A, B=2, max_pages=4, num_pages=9, page_size=16, layers=2, Hkv=2, d=128, stream=0) | args
     assert fa.fa_cache_evict(**a) == code
 

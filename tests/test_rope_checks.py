@@ -69,12 +69,12 @@ def test_backward_workspace():
 @pytest.mark.parametrize("args,code", COMMON + [
     (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(q_out=None), INV), (dict(q=A + 8), ALI), (dict(k=A + 8), ALI),
     (dict(v=A + 8), ALI), (dict(q_out=A + 8), ALI), (dict(k_pages=A + 8), ALI), (dict(v_pages=A + 8), ALI), (dict(v_token=4), ALI),
-    (dict(v_head=4), ALI), (dict(k_pages=None), INV), (dict(v_pages=None), INV), (dict(page_table=None), INV),
+    (dict(v_head=4), ALI), (dict(k_pages=None), INV), (dict(v_pages=None), INV), (dict(v_pages=A), INV), (dict(page_table=None), INV),
     (dict(cache_lens=None), INV), (dict(cu_seqlens=None), INV), (dict(cu_seqlens=A + 2), ALI), (dict(page_table=A + 2), ALI),
     (dict(cache_lens=A + 2), ALI), (dict(B=0), INV), (dict(B=65536), UNS), (dict(page_size=24), UNS), (dict(max_pages=0), INV),
     (dict(num_pages=0), INV), (dict(max_pages=1 << 27), UNS)], ids=ids)
 def test_append(args, code):
-    a = ROWS | dict(v=A, v_token=128, v_head=64, k_pages=A, v_pages=A, page_table=A, cache_lens=A, cu_seqlens=A) | ANGLES | dict(
+    a = ROWS | dict(v=A, v_token=128, v_head=64, k_pages=A, v_pages=A + 4096, page_table=A, cache_lens=A, cu_seqlens=A) | ANGLES | dict(
         q_out=A, B=2, max_pages=4, num_pages=9, page_size=16, total=5, H=4, Hkv=2, d=64, stream=0) | args
     assert fa.fa_cache_append_rope(**a) == code
 
