@@ -326,7 +326,7 @@ int launch_clusters(void (*kernel)(P...), long long clusters, int threads, size_
 template <int THREADS, int CS>
 int launch_select(const EvictParams &p, long long items, int most, cudaStream_t stream) {
   const int part = (p.places + CS - 1) / CS + 3, cap = part < most ? part : most;  // a block's stretch
-  if (cap * 4 > 24 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, CS>,
+  if (cap * 4 > 30 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, CS>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
     return FA_ERR_CUDA;
   return launch_clusters<CS>(evict_select_kernel<THREADS, CS>, items, THREADS, (size_t)cap * 4, stream, p, cap);
