@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   const bool go = goes(p, b, len);
   if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (rank == 0 && item < (unsigned)(p.Hkv * p.g.B) && item % p.Hkv == 0 && tid == 0) p.lens_out[b] = go ? p.keep : len;
-  if (!go) {  // the whole cluster
-    for (int i = rank * THREADS + tid; i < p.keep; i += CS * THREADS) kept[i] = i < len ? i : -1;
+  if (!go) {  // the whole cluster; the budget may be any number, and a step past it pass 31 bits
+    for (long long i = rank * THREADS + tid; i < p.keep; i += CS * THREADS) kept[i] = i < len ? (int)i : -1;
     return;
   }
   const float *x = w + lo;
@@ -325,7 +325,8 @@ int launch_clusters(void (*kernel)(P...), long long clusters, int threads, size_
 
 template <int THREADS, int CS>
 int launch_select(const EvictParams &p, long long items, int most, cudaStream_t stream) {
-  const int part = (p.places + CS - 1) / CS + 3, cap = part < most ? part : most;  // a block's stretch
+  const long long part = ((long long)p.places + CS - 1) / CS + 3;  // a block's stretch
+  const int cap = part < most ? (int)part : most;
   if (cap * 4 > 30 * 1024 && cudaFuncSetAttribute(evict_select_kernel<THREADS, CS>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
     return FA_ERR_CUDA;
