@@ -262,6 +262,10 @@ __device__ __forceinline__ unsigned bit_range(int lo, int hi) {
 // Rounding.  Scores are fp32 sums.  A row's lse in log2 units is kept as a float and its
 // rounding error, which as a factor 2^-error goes into the sum: as the argument's error it
 // would be the same for all places of a row (up to 2^-20 of each weight).  Sums are fp32.
+// Rows of a set share a base only where their lse lie within 8 (in log2 units) of one another:
+// an argument c2 s - base is rounded to half a step of its size, so that a base b away from a
+// row's own lse costs a weight near 1 up to b 2^-24 of it, 2^-22 with the 4 allowed here (with
+// the largest lse as the base and up to 64 between them it was 2.8e-6).
 template <int D, int NQ>
 __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel(const __grid_constant__ WeightsParams p) {
   using C = WeightsCfg<D, NQ>;
@@ -669,8 +673,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
           }
-          // one base for all: a weight below 2^-62 of its row's sum may become 0
-          const float base = top - low <= 64.f ? top : INFINITY;
+          // one base for all, at most 4 from each
+          const float base = top - low <= 8.f ? low + 0.5f * (top - low) : INFINITY;
 #pragma unroll
           for (int i = 0; i < NQ / 32; ++i) {
             const float d = base - hi[i], back = base - d, rest = (base - (d + back)) + (back - hi[i]);  // base - hi = d + rest
