@@ -653,6 +653,7 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
         for (int i = 0; i < NQ / 32; ++i) here[i] = lse[i];
         if (c + 1 < walk.chunks) look_up(c + 1);
         float hi[NQ / 32], lo[NQ / 32], top = -INFINITY, low = INFINITY;
+        bool finite = true;  // the lse of all rows
 #pragma unroll
         for (int i = 0; i < NQ / 32; ++i) {
           constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500920e-8f;  // log2(e) is their sum
@@ -662,7 +663,8 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
           // a token that saw nothing has lse = -inf and gives nothing
           t[lane + 32 * i] = here[i] == -INFINITY ? -INFINITY : -hi[i];
           t[NQ + lane + 32 * i] = fmaf(lo[i], -0.693147180559945309f, 1.f);
-          if (NQ > 32 && row_hb[i] >= 0 && row_tok[i] < tokens && fabsf(hi[i]) < INFINITY) {
+          if (NQ > 32 && row_hb[i] >= 0 && row_tok[i] < tokens) {
+            finite &= fabsf(hi[i]) < INFINITY;
             top = fmaxf(top, hi[i]);
             low = fminf(low, hi[i]);
           }
@@ -673,13 +675,13 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
           }
-          // one base for all, at most 4 from each
-          const float base = top - low <= 8.f ? low + 0.5f * (top - low) : INFINITY;
+          // One base for all, at most 4 from each.  A row that its lse leaves out may have any score: beside the others'
+          // base 2^score may be infinite, which times a factor of 0 is not 0, so such a set goes row by row.
+          const float base = __all_sync(0xffffffffu, finite) && top - low <= 8.f ? low + 0.5f * (top - low) : INFINITY;
 #pragma unroll
           for (int i = 0; i < NQ / 32; ++i) {
             const float d = base - hi[i], back = base - d, rest = (base - (d + back)) + (back - hi[i]);  // base - hi = d + rest
-            const float more = fabsf(hi[i]) < INFINITY ? fmaf(rest - lo[i], 0.693147180559945309f, 1.f) : 1.f;
-            t[2 * NQ + lane + 32 * i] = here[i] == -INFINITY ? 0.f : exp2f(d) * more;
+            t[2 * NQ + lane + 32 * i] = exp2f(d) * fmaf(rest - lo[i], 0.693147180559945309f, 1.f);
           }
           if (lane == 0) t[3 * NQ] = base;
         }
