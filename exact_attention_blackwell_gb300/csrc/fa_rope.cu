@@ -61,19 +61,28 @@ struct RowCfg {
 // can be dropped exactly: step = f / (2 pi) in units of 2^-64 turns, wrapped, and position
 // * step in wrapping 64-bit integers is the angle whatever the position's size (off by
 // |position| * 2^-63 turns: 1e-9 radians at the far end of 32 bits; fp32 products lose
-// whole turns past 2^24).  f = m 2^e with a 24-bit m; m * 2^64 / (2 pi) is 88 bits.
+// whole turns past 2^24).  f = m 2^-s with a 24-bit m.  f may be as large as 2^128, so that
+// 1 / (2 pi) has to be known to 64 + 128 bits: m * 2^192 / (2 pi) is 216 bits, of which the
+// step is the 64 from 128 + s on.  (With the first 64 bits of 1 / (2 pi) alone the step was
+// off by f / 2 units: 4e-6 radians at the far end for f = 1e4.)
 __device__ __forceinline__ unsigned long long turns_per_step(float f) {
-  constexpr unsigned long long kInvTwoPi = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+  constexpr unsigned long long k2 = 0x28BE60DB9391054Aull, k1 = 0x7F09D5F47D4D3770ull, k0 = 0x36D8A5664F10E410ull;
   const unsigned bits = __float_as_uint(f);
   const int e = (bits >> 23) & 0xff;
   const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
-  const unsigned long long lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
-  const int s = 150 - (e ? e : 1);  // f = m 2^-s
-  unsigned long long g;
-  if (s >= 128) g = 0;
-  else if (s >= 64) g = hi >> (s - 64);
-  else if (s > 0) g = (lo >> s) | (hi << (64 - s));
-  else g = -s < 64 ? lo << -s : 0;
+  const int from = 278 - (e ? e : 1), word = from >> 6, r = from & 63;  // 128 + s
+  unsigned long long v[5] = {m * k0, m * k1, m * k2, __umul64hi(m, k2), 0};
+  const unsigned long long c0 = __umul64hi(m, k0), c1 = __umul64hi(m, k1);
+  v[1] += c0;
+  v[2] += c1 + (v[1] < c0);  // c1 < 2^24
+  v[3] += v[2] < c1 + (v[1] < c0);
+  unsigned long long lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    if (i == word) lo = v[i];
+    if (i == word + 1) hi = v[i];
+  }
+  const unsigned long long g = r ? lo >> r | hi << (64 - r) : lo;
   return bits >> 31 ? 0ull - g : g;
 }
 
