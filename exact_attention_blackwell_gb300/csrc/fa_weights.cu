@@ -675,9 +675,10 @@ __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
           }
-          // One base for all, at most 4 from each.  A row that its lse leaves out may have any score: beside the others'
-          // base 2^score may be infinite, which times a factor of 0 is not 0, so such a set goes row by row.
-          const float base = __all_sync(0xffffffffu, finite) && top - low <= 8.f ? low + 0.5f * (top - low) : INFINITY;
+          // One base for all, at most 4 from each: the largest, or 4 above the smallest.  A row that its lse leaves out
+          // may have any score: beside the others' base 2^score may be infinite, which times a factor of 0 is not 0, so
+          // such a set goes row by row.
+          const float base = __all_sync(0xffffffffu, finite) && top - low <= 8.f ? fminf(top, low + 4.f) : INFINITY;
 #pragma unroll
           for (int i = 0; i < NQ / 32; ++i) {
             const float d = base - hi[i], back = base - d, rest = (base - (d + back)) + (back - hi[i]);  // base - hi = d + rest
