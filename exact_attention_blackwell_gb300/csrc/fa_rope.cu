@@ -66,23 +66,23 @@ struct RowCfg {
 // step is the 64 from 128 + s on.  (With the first 64 bits of 1 / (2 pi) alone the step was
 // off by f / 2 units: 4e-6 radians at the far end for f = 1e4.)
 __device__ __forceinline__ unsigned long long turns_per_step(float f) {
-  constexpr unsigned long long k2 = 0x28BE60DB9391054Aull, k1 = 0x7F09D5F47D4D3770ull, k0 = 0x36D8A5664F10E410ull;
+  // the lowest word first
+  constexpr unsigned kInvTwoPi[6] = {0x4F10E410u, 0x36D8A566u, 0x7D4D3770u, 0x7F09D5F4u, 0x9391054Au, 0x28BE60DBu};
   const unsigned bits = __float_as_uint(f);
   const int e = (bits >> 23) & 0xff;
-  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
-  const int from = 278 - (e ? e : 1), word = from >> 6, r = from & 63;  // 128 + s
-  unsigned long long v[5] = {m * k0, m * k1, m * k2, __umul64hi(m, k2), 0};
-  const unsigned long long c0 = __umul64hi(m, k0), c1 = __umul64hi(m, k1);
-  v[1] += c0;
-  v[2] += c1 + (v[1] < c0);  // c1 < 2^24
-  v[3] += v[2] < c1 + (v[1] < c0);
-  unsigned long long lo = 0, hi = 0;
+  const unsigned m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int from = 278 - (e ? e : 1), word = from >> 5;  // 128 + s, 23 to 277
+  unsigned long long sum = 0;
+  unsigned a = 0, b = 0, c = 0;  // the product's words from there on
 #pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    if (i == word) lo = v[i];
-    if (i == word + 1) hi = v[i];
+  for (int i = 0; i < 7; ++i) {
+    sum = (i < 6 ? (unsigned long long)m * kInvTwoPi[i < 6 ? i : 0] : 0ull) + (sum >> 32);
+    if (i == word) a = (unsigned)sum;
+    if (i == word + 1) b = (unsigned)sum;
+    if (i == word + 2) c = (unsigned)sum;
   }
-  const unsigned long long g = r ? lo >> r | hi << (64 - r) : lo;
+  const unsigned lo = __funnelshift_r(a, b, from), hi = __funnelshift_r(b, c, from);  // by from % 32
+  const unsigned long long g = (unsigned long long)hi << 32 | lo;
   return bits >> 31 ? 0ull - g : g;
 }
 
