@@ -29,11 +29,14 @@ namespace {
 // stretches for the blocks, which begin with the first unit that begins in theirs.
 //
 // Bound by HBM with few rows: 64 users of up to 8192 places, one token, 32 on 8 heads of dim
-// 128 take 77 us, 6.3 TB/s; 32 of up to 2500, trees of up to 7, 16 heads of dim 64 21 us,
+// 128 take 78 us, 6.2 TB/s; 32 of up to 2500, trees of up to 7, 16 heads of dim 64 21.5 us,
 // 3.4 TB/s, of which 7 are the way to the first product and the rest what surrounds a tile's
-// (with one head to a run 29).  With many rows by that way too and by the exponentials: 64
-// tokens of 32 on 8 heads of dim 128 over 32768 places 28 us, of 128 columns some 1650 cycles of
-// a warpgroup (the two share 1024 of the exponential unit) and 500 around them.
+// (with one head to a run 29).  With many rows by that way too and by what a warpgroup does
+// itself (products are there when it asks for them): 64 tokens of 32 on 8 heads of dim 128 over
+// 32768 places 28.5 us, of which 4.6 to the first product, then 7 units of some 6450 cycles:
+// twice 2030 for the 128 columns of a set, 630 between the sets and 1760 from unit to unit.  For
+// each set the two warpgroups share 1024 cycles of the exponential unit, and shared memory
+// serves 2400: 1100 of reads of the terms, 1024 of the products' operands, 256 of the tiles' way in.
 struct WeightsParams {
   CUtensorMap tm_q;  // [total, Hkv, G, d]: box 64 columns x G heads x TB tokens
   CUtensorMap tm_k;  // [num_pages, page_size, Hkv, d]: box 64 columns x min(page_size, 128) rows of one head
@@ -265,7 +268,8 @@ __device__ __forceinline__ unsigned bit_range(int lo, int hi) {
 // Rows of a set share a base only where their lse lie within 8 (in log2 units) of one another:
 // an argument c2 s - base is rounded to half a step of its size, so that a base b away from a
 // row's own lse costs a weight near 1 up to b 2^-24 of it, 2^-22 with the 4 allowed here (with
-// the largest lse as the base and up to 64 between them it was 2.8e-6).
+// the largest lse as the base and up to 64 between them it was 2.8e-6).  Row by row the window
+// above takes 38.4 us.  A weight below 2^-122 of its row's sum may become 0.
 template <int D, int NQ>
 __global__ void __launch_bounds__(WeightsCfg<D, NQ>::kThreads, 1) weights_kernel(const __grid_constant__ WeightsParams p) {
   using C = WeightsCfg<D, NQ>;
